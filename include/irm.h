@@ -80,6 +80,7 @@ typedef struct CUstream_st* cudaStream_t; /* identical to the CUDA runtime's typ
 #define IRM_CARVE_OUT 32     /* positions 0..31 are always fresh */
 #define IRM_MAX_HEADS 128
 #define IRM_WORKSPACE_HEADER 256
+#define IRM_MAX_TREE 1024    /* drafted tokens of one request */
 
 typedef enum irm_status {
   IRM_OK = 0,
@@ -90,7 +91,9 @@ typedef enum irm_status {
   IRM_ERR_CUDA = -5,           /* a CUDA runtime call failed (see irm_last_error) */
   IRM_ERR_DEVICE_TIMEOUT = -6, /* a device pipeline wait ran out (from irm_device_status) */
   IRM_ERR_DEVICE_BOUNDS = -7,  /* a kernel met a source row outside the row store */
-  IRM_ERR_WORKSPACE = -8       /* workspace missing or smaller than required */
+  IRM_ERR_WORKSPACE = -8,      /* workspace missing or smaller than required */
+  IRM_ERR_OUT_OF_PAGES = -9,   /* a resize or fork found too few free pages (from irm_device_status) */
+  IRM_ERR_SHARED_PAGE = -10    /* a request would grow inside a page that it shares (from irm_device_status) */
 } irm_status;
 
 /* One chunk of a request's table, listed in target order [walkthrough §5].
@@ -291,6 +294,126 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
                                      const void* kv_rows, int64_t n_rows, float softmax_scale,
                                      void* out, float* lse, const irm_rope* rope, void* workspace,
                                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Speculative decoding over the paged cache.  The calls below work on 64-row pages, the layout
+ * irm_assemble_kv writes, and make up one step: irm_pages_resize makes room for the drafts,
+ * the model writes their rows, irm_mla_attn_tree attends (once a layer), irm_tree_verify
+ * accepts a path and draws the next token, irm_pages_compact moves the path's rows up, and
+ * irm_pages_resize gives the rest back.
+ *
+ * A request's tree has n nodes, numbered so that a parent comes before its children; node 0
+ * is the last committed token (its row is not in the cache yet).  Node i's KV row sits at slot
+ * ctx + i of the request, encoded at position ctx + depth(i).  q_indptr_host [B + 1] (host
+ * memory, q_indptr_host[0] == 0, non-decreasing) lays the batch's nodes end to end: request
+ * b owns nodes [q_indptr_host[b], q_indptr_host[b + 1]), at most IRM_MAX_TREE, possibly none.
+ * Host arrays of these calls travel in the launch parameters: the caller may reuse them as
+ * soon as the call returns, and a captured graph replays the lengths as they were given.
+ */
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache (absorbed MLA, as the decode).
+ *   node i of request b sees the request's rows t < ctx_b, and the rows ctx_b + k of the
+ *   drafts k whose bit k is set in its mask; bits of k >= n_b are ignored
+ *   O = softmax(s) . cKV, s_t = scale * (q_lat . cKV_t + q_rope . k_r,t); a node that sees no
+ *   row gets O = 0 and lse = -inf
+ *
+ *   q_lat   device bf16 [T, H, 512], q_rope device bf16 [T, H, 64] (encoded at the node's
+ *           position), T = q_indptr_host[B]; H in 1..128
+ *   ctx_host [B] host: rows of each request before its drafts, >= 0
+ *   paged_kv device bf16 [n_pages, 64, 576], n_pages < 2^25
+ *   page_table device int32 [B, max_pages]: the pages holding rows 0 .. ctx_b + n_b - 1 must
+ *           lie in [0, n_pages); an entry outside is recorded as IRM_ERR_DEVICE_BOUNDS and its
+ *           rows are read as zeros
+ *   tree_mask device uint32 [T, mask_words], bit k of a row in word k / 32; 32 * mask_words
+ *           must cover the largest tree
+ *   softmax_scale  finite and positive
+ *   out     device bf16 [T, H, 512];  lse device fp32 [T, H] or NULL
+ * Rows of the last page behind ctx_b + n_b - 1, and rows of drafts that no node of the request
+ * sees, may hold anything (NaN included).  A NaN or infinity in any other row may spread to
+ * every node of its request.
+ * Workspace: irm_mla_attn_tree_workspace_size bytes for the same lengths and H.
+ */
+irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32_t* q_indptr_host, int B, int H,
+                                            size_t* bytes);
+irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H, const int32_t* ctx_host,
+                             const int32_t* q_indptr_host, const void* paged_kv, int64_t n_pages,
+                             const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
+                             float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/*
+ * Verification of a batch's trees against the target's probabilities, from given uniform
+ * numbers.  With p_u, q_u the target's and the draft model's row at node u:
+ *   u = 0, w = p_0, S = 1; for the children i of u in index order, x = tokens[i]:
+ *     r_i q_u(x) S < w(x): accepted, u = i, w = p_i, S = 1;
+ *     else w <- max(w - S q_u, 0), S <- sum w
+ *   no child left: the next token is the lowest v with cumsum(w)(v) > r_0 sum(w)
+ * draft_probs NULL: the drafts were chosen without chance (top-k, lookup): q_u is 1 at the
+ * child's token, so a rejection only takes that token out of w.  With draft_probs the children
+ * must have been drawn independently from q_u.  Either way the emitted tokens follow the
+ * target's distribution.  If no mass is left in w, the next token is drawn from p_u.
+ *
+ *   target_probs, draft_probs  device fp32, row i of T at i * row_stride, vocab entries that sum
+ *               to 1; NaN and values below 0 count as 0, values above 1 as 1, and the final
+ *               draw resolves 2^-44
+ *   tokens, parents, uniforms  device [T]: token ids in [0, vocab), parents (request-relative,
+ *               parent < node; node 0's token and parent are not read), uniforms in [0, 1)
+ *               (node 0's draws the next token).  A token or parent outside its range is
+ *               recorded as IRM_ERR_DEVICE_BOUNDS and its node never accepted.
+ *   max_path    the walk stops (and draws the next token there) once it has max_path nodes
+ *   n_accept    device int32 [B]: nodes of the path, node 0 included (0 for an empty tree)
+ *   path        device int32 [B, max_path]: the accepted nodes, then -1
+ *   next_token  device int32 [B]; -1 for an empty tree or a row without probability
+ * vocab at most 2^20.  Workspace: IRM_WORKSPACE_HEADER bytes (status word).
+ */
+irm_status irm_tree_verify(const float* target_probs, const float* draft_probs, int64_t row_stride, int32_t vocab,
+                           const int32_t* tokens, const int32_t* parents, const float* uniforms,
+                           const int32_t* q_indptr_host, int B, int max_path, int32_t* n_accept, int32_t* path,
+                           int32_t* next_token, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Pages of a cache, kept on the device so that a step needs no host round trip.  The cache is
+ * bf16 [n_layers, n_pages, 64, 576]; all layers share one page table.
+ *   seq_len    device int32 [n_slots]: rows of each request; request s holds the pages
+ *              page_table[s, 0 .. ceil(seq_len[s] / 64) - 1], n_slots <= 8192
+ *   page_table device int32 [n_slots, max_pages]; entries given back become -1
+ *   refcount   device int32 [n_pages]: requests that hold each page, 0 = free (start with
+ *              zeros; a caller may hold pages of its own with counts of its own)
+ * All results are independent of scheduling: free pages are handed out lowest first, in
+ * request order.
+ * A device-side refusal (a status recorded in the workspace, read with irm_device_status) leaves
+ * what it concerns as it was:  IRM_ERR_DEVICE_BOUNDS for a length outside [0, 64 max_pages],
+ * a page index outside [0, n_pages) or a page released more often than held;
+ * IRM_ERR_OUT_OF_PAGES when the free pages do not suffice (then no request of the call grows,
+ * or none is forked); IRM_ERR_SHARED_PAGE for a request that would grow while its last,
+ * partly filled page is held by others too (fork it instead: a fork has its own copy of it).
+ * Workspace: irm_pages_workspace_size bytes.
+ */
+irm_status irm_pages_workspace_size(int n_slots, size_t* bytes);
+/* Every request s to new_len[s] rows (device int32 [n_slots]): allocates, trims or, with 0, frees.
+ * Releases take effect before allocations.  seq_len becomes new_len where it was granted. */
+irm_status irm_pages_resize(const int32_t* new_len, int32_t* seq_len, int n_slots, int32_t* page_table,
+                            int max_pages, int32_t* refcount, int64_t n_pages, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+/* Forks request src_host[f] into the empty slot dst_host[f] (host int32 [n_forks], n_forks <=
+ * 1024; destinations distinct and not sources): full pages are shared, the rows of a partly filled last
+ * page are copied to a fresh page in every layer, so both may grow.  A destination whose
+ * seq_len is not 0 is recorded as IRM_ERR_DEVICE_BOUNDS and left alone. */
+irm_status irm_pages_fork(const int32_t* src_host, const int32_t* dst_host, int n_forks, void* kv, int n_layers,
+                          int32_t* seq_len, int n_slots, int32_t* page_table, int max_pages, int32_t* refcount,
+                          int64_t n_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Moves the rows of an accepted path up: row base[s] + path[s, k] to row base[s] + k, for k <
+ * n_accept[s], in every layer (base, n_accept device int32 [n_slots], path device int32 [n_slots,
+ * max_path], as irm_tree_verify writes them; paths increase strictly).  Lengths and pages
+ * stay: resize to base + n_accept next.  The drafts' pages must be the request's own. */
+irm_status irm_pages_compact(void* kv, int n_layers, int64_t n_pages, const int32_t* page_table, int max_pages,
+                             int n_slots, const int32_t* base, const int32_t* path, int max_path,
+                             const int32_t* n_accept, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Copies pages src_host[i] -> dst_host[i] (host int32 [n]) in every layer; destinations distinct
+ * and not sources.  Tables and counts are the caller's to change. */
+irm_status irm_pages_copy(void* kv, int n_layers, int64_t n_pages, const int32_t* src_host, const int32_t* dst_host,
+                          int n, cudaStream_t stream);
 
 /*
  * Content-defined chunking of token streams, the step that cuts a request's unmatched tail

@@ -9,13 +9,16 @@ from .binding import (CDC_LOW_BITS, CDC_THRESHOLD, ROPE_INTERLEAVED, ROPE_NEOX, 
                       ChunkTable, IrmError, Registry, Rope, cdc_sizes, cdc_slot_base, irm_cdc_chunk,
                       assemble_kv_workspace_size, decode_noalloc_status, decode_workspace_size,
                       device_status, irm_assemble_kv, irm_mla_attn_decode,
-                      irm_mla_attn_decode_noalloc, irm_mla_attn_prefill, lib,
-                      new_workspace, prefill_workspace_size, selftest_wait_timeout,
-                      validate_chunks)
+                      irm_mla_attn_decode_noalloc, irm_mla_attn_prefill, irm_mla_attn_tree,
+                      irm_pages_compact, irm_pages_copy, irm_pages_fork, irm_pages_resize, irm_tree_verify,
+                      lib, new_workspace, pages_workspace_size, prefill_workspace_size,
+                      selftest_wait_timeout, tree_workspace_size, validate_chunks, WORKSPACE_HEADER)
 
 __all__ = ["Registry", "CDC_LOW_BITS", "CDC_THRESHOLD", "CdcParams", "cdc_sizes", "cdc_slot_base",
            "irm_cdc_chunk", "ROPE_INTERLEAVED", "ROPE_NEOX", "Rope", "ChunkTable", "IrmError",
            "assemble_kv_workspace_size", "decode_noalloc_status", "decode_workspace_size",
            "device_status", "irm_assemble_kv", "irm_mla_attn_decode", "irm_mla_attn_decode_noalloc",
-           "irm_mla_attn_prefill",
+           "irm_mla_attn_prefill", "irm_mla_attn_tree", "irm_pages_compact", "irm_pages_copy",
+           "irm_pages_fork", "irm_pages_resize", "irm_tree_verify", "pages_workspace_size",
+           "tree_workspace_size", "WORKSPACE_HEADER",
            "lib", "new_workspace", "prefill_workspace_size", "selftest_wait_timeout", "validate_chunks"]

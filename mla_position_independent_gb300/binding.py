@@ -27,7 +27,9 @@ EXPORTS = ["irm_status_string", "irm_last_error", "irm_version", "irm_validate_c
            "irm_mla_attn_decode_rope", "irm_mla_attn_decode_noalloc", "irm_decode_noalloc_status",
            "irm_mla_attn_prefill_workspace_size", "irm_mla_attn_prefill", "irm_mla_attn_prefill_rope",
            "irm_cdc_sizes", "irm_cdc_chunk", "irm_registry_create", "irm_registry_stats",
-           "irm_registry_assemble", "irm_selftest_wait_timeout"]
+           "irm_registry_assemble", "irm_selftest_wait_timeout", "irm_mla_attn_tree_workspace_size",
+           "irm_mla_attn_tree", "irm_tree_verify", "irm_pages_workspace_size", "irm_pages_resize",
+           "irm_pages_fork", "irm_pages_compact", "irm_pages_copy"]
 
 ROPE_NEOX, ROPE_INTERLEAVED = 0, 1
 
@@ -104,6 +106,14 @@ def lib():
         L.irm_registry_stats.argtypes = [P, P, P]
         L.irm_registry_assemble.argtypes = [P, P, I64, I64, I64, P, P, P, ctypes.c_int32, ctypes.c_int32,
                                             ctypes.c_uint64, P, P, ctypes.c_int32, P]
+        L.irm_mla_attn_tree_workspace_size.argtypes = [P, P, I, I, P]
+        L.irm_mla_attn_tree.argtypes = [P, P, I, I, P, P, P, I64, P, I, P, I, ctypes.c_float, P, P, P, SZ, P]
+        L.irm_tree_verify.argtypes = [P, P, I64, ctypes.c_int32, P, P, P, P, I, I, P, P, P, P, SZ, P]
+        L.irm_pages_workspace_size.argtypes = [I, P]
+        L.irm_pages_resize.argtypes = [P, P, I, P, I, P, I64, P, SZ, P]
+        L.irm_pages_fork.argtypes = [P, P, I, P, I, P, I, P, I, P, I64, P, SZ, P]
+        L.irm_pages_compact.argtypes = [P, I, I64, P, I, I, P, P, I, P, P, SZ, P]
+        L.irm_pages_copy.argtypes = [P, I, I64, P, P, I, P]
         for name in EXPORTS:
             if name not in ("irm_status_string", "irm_last_error", "irm_version"):
                 getattr(L, name).restype = I
@@ -363,6 +373,215 @@ def irm_cdc_chunk(tokens: torch.Tensor, offsets: np.ndarray, gear: torch.Tensor 
                                int(vocab), pp, _ptr(n_chunks), _ptr(c_start), _ptr(c_len),
                                _ptr(c_hash), _ptr(workspace), workspace.numel(), _stream(stream)))
     return n_chunks, c_start, c_len, c_hash, workspace
+
+
+def _host_i32(x, name):
+    a = np.asarray(x)
+    if a.ndim != 1 or a.dtype.kind not in "iu":
+        raise ValueError(f"{name} must be a 1-d integer array in host memory")
+    if a.itemsize > 4 and a.size and (a.max() > 2**31 - 1 or a.min() < -2**31):
+        raise ValueError(f"{name} has values outside int32")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
+def _need_shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _one_device(*tensors):
+    """The tensors' device; a call's launches and its default stream belong to it."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return new_workspace(nbytes, device)
+    _need(workspace, torch.uint8, "workspace", 1)
+    return workspace
+
+
+def tree_workspace_size(ctx: np.ndarray, q_indptr: np.ndarray, H: int) -> int:
+    """Workspace bytes of irm_mla_attn_tree for these lengths."""
+    ctx, q_indptr = _host_i32(ctx, "ctx"), _host_i32(q_indptr, "q_indptr")
+    if len(q_indptr) != len(ctx) + 1:
+        raise ValueError("q_indptr must have one entry more than ctx")
+    n = ctypes.c_size_t(0)
+    _check(lib().irm_mla_attn_tree_workspace_size(_ptr(ctx), _ptr(q_indptr), len(ctx), int(H), ctypes.byref(n)))
+    return n.value
+
+
+def irm_mla_attn_tree(q_lat, q_rope, ctx, q_indptr, paged_kv, page_table, tree_mask, softmax_scale=DEFAULT_SCALE,
+                      out=None, lse=None, workspace=None, stream=None):
+    """Attention of drafted trees over the paged cache: q_lat [T, H, 512] / q_rope [T, H, 64] bf16 of
+    all nodes end to end, ctx [B] and q_indptr [B + 1] integers in host memory, paged_kv [n_pages, 64,
+    576] bf16, page_table [B, max_pages] int32, tree_mask [T, words] int32 (bit k of a row: the node
+    sees draft k).  Returns (out [T, H, 512] bf16, lse or None, workspace)."""
+    ctx, q_indptr = _host_i32(ctx, "ctx"), _host_i32(q_indptr, "q_indptr")
+    if len(ctx) < 1 or len(q_indptr) != len(ctx) + 1:
+        raise ValueError("q_indptr must have one entry more than ctx")
+    _need(q_lat, torch.bfloat16, "q_lat", 3)
+    _need(q_rope, torch.bfloat16, "q_rope", 3)
+    _need(paged_kv, torch.bfloat16, "paged_kv", 3)
+    _need(page_table, torch.int32, "page_table", 2)
+    _need(tree_mask, torch.int32, "tree_mask", 2)
+    B, T, H = len(ctx), int(q_indptr[-1]), int(q_lat.shape[1])
+    _need_shape(q_lat, (T, H, 512), "q_lat")
+    _need_shape(q_rope, (T, H, 64), "q_rope")
+    _need_shape(paged_kv, (paged_kv.shape[0], 64, 576), "paged_kv")
+    _need_shape(page_table, (B, page_table.shape[1]), "page_table")
+    _need_shape(tree_mask, (T, tree_mask.shape[1]), "tree_mask")
+    if out is None:
+        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q_lat.device)
+    _need(out, torch.bfloat16, "out")
+    _need_shape(out, (T, H, 512), "out")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        _need_shape(lse, (T, H), "lse")
+    if workspace is None:
+        workspace = new_workspace(tree_workspace_size(ctx, q_indptr, H), q_lat.device)
+    _need(workspace, torch.uint8, "workspace", 1)
+    if T == 0:
+        return out, lse, workspace
+    with _one_device(q_lat, q_rope, paged_kv, page_table, tree_mask, out, lse, workspace):
+        _check(lib().irm_mla_attn_tree(
+            _ptr(q_lat), _ptr(q_rope), B, H, _ptr(ctx), _ptr(q_indptr), _ptr(paged_kv), int(paged_kv.shape[0]),
+            _ptr(page_table), int(page_table.shape[1]), _ptr(tree_mask), int(tree_mask.shape[1]),
+            float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out, lse, workspace
+
+
+def irm_tree_verify(target_probs, tokens, parents, uniforms, q_indptr, draft_probs=None, max_path=None, out=None,
+                    workspace=None, stream=None):
+    """Verification of drafted trees: target_probs (and draft_probs) [T, vocab] fp32, rows may be
+    strided; tokens, parents int32 [T], uniforms fp32 [T]; q_indptr [B + 1] integers in host
+    memory.  Returns (n_accept [B], path [B, max_path], next_token [B], workspace), int32."""
+    q_indptr = _host_i32(q_indptr, "q_indptr")
+    if len(q_indptr) < 2:
+        raise ValueError("q_indptr must have at least two entries")
+    B, T = len(q_indptr) - 1, int(q_indptr[-1])
+    _need(tokens, torch.int32, "tokens", 1)
+    _need(parents, torch.int32, "parents", 1)
+    _need(uniforms, torch.float32, "uniforms", 1)
+    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is None and name == "draft_probs":
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 or not t.is_cuda:
+            raise ValueError(f"{name} must be a 2-d torch.float32 tensor on the GPU")
+        if t.shape[1] < 1 or t.stride(1) != 1 and t.shape[1] > 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    V = int(target_probs.shape[1])
+    ld = int(target_probs.stride(0)) if T > 1 else V
+    _need_shape(target_probs, (T, V), "target_probs")
+    if draft_probs is not None:
+        _need_shape(draft_probs, (T, V), "draft_probs")
+        if T > 1 and draft_probs.stride(0) != ld:
+            raise ValueError("draft_probs must have target_probs' row stride")
+    for t, name in ((tokens, "tokens"), (parents, "parents"), (uniforms, "uniforms")):
+        _need_shape(t, (T,), name)
+    if max_path is None:
+        max_path = max(1, int(np.diff(q_indptr).max())) if out is None else int(out[1].shape[1])
+    dev = tokens.device
+    if out is None:
+        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty((B, max_path), dtype=torch.int32, device=dev),
+               torch.empty(B, dtype=torch.int32, device=dev))
+    n_accept, path, next_token = out
+    for t, shape, name in ((n_accept, (B,), "n_accept"), (path, (B, max_path), "path"), (next_token, (B,), "next_token")):
+        _need(t, torch.int32, name)
+        _need_shape(t, shape, name)
+    workspace = _workspace(workspace, WORKSPACE_HEADER, dev)
+    with _one_device(tokens, parents, uniforms, target_probs, draft_probs, n_accept, path, next_token, workspace):
+        _check(lib().irm_tree_verify(
+            _ptr(target_probs), _ptr(draft_probs), ld, V, _ptr(tokens), _ptr(parents), _ptr(uniforms), _ptr(q_indptr), B,
+            int(max_path), _ptr(n_accept), _ptr(path), _ptr(next_token), _ptr(workspace), workspace.numel(),
+            _stream(stream)))
+    return n_accept, path, next_token, workspace
+
+
+def pages_workspace_size(n_slots: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().irm_pages_workspace_size(int(n_slots), ctypes.byref(n)))
+    return n.value
+
+
+def _need_pages(seq_len, page_table, refcount):
+    _need(seq_len, torch.int32, "seq_len", 1)
+    _need(page_table, torch.int32, "page_table", 2)
+    _need(refcount, torch.int32, "refcount", 1)
+    _need_shape(page_table, (seq_len.shape[0], page_table.shape[1]), "page_table")
+
+
+def _need_cache(kv, n_pages=None):
+    """[n_layers, n_pages, 64, 576] bf16, or one layer's [n_pages, 64, 576]: (layers, pages)."""
+    _need(kv, torch.bfloat16, "kv")
+    if kv.dim() not in (3, 4) or tuple(kv.shape[-2:]) != (64, 576):
+        raise ValueError("kv must be [n_layers, n_pages, 64, 576] or [n_pages, 64, 576]")
+    if n_pages is not None and kv.shape[-3] != n_pages:
+        raise ValueError(f"kv must have refcount's {n_pages} pages, not {kv.shape[-3]}")
+    return (int(kv.shape[0]) if kv.dim() == 4 else 1), int(kv.shape[-3])
+
+
+def irm_pages_resize(new_len, seq_len, page_table, refcount, workspace=None, stream=None):
+    """Every request to new_len [n_slots] rows (device int32): allocates, trims or, with 0, frees its pages.
+    seq_len [n_slots], page_table [n_slots, max_pages] and refcount [n_pages] (int32) are updated."""
+    _need_pages(seq_len, page_table, refcount)
+    _need(new_len, torch.int32, "new_len", 1)
+    _need_shape(new_len, seq_len.shape, "new_len")
+    n_slots = int(seq_len.shape[0])
+    workspace = _workspace(workspace, pages_workspace_size(n_slots) if workspace is None else 0, seq_len.device)
+    with _one_device(seq_len, new_len, page_table, refcount, workspace):
+        _check(lib().irm_pages_resize(_ptr(new_len), _ptr(seq_len), n_slots, _ptr(page_table), int(page_table.shape[1]),
+                                      _ptr(refcount), int(refcount.shape[0]), _ptr(workspace), workspace.numel(),
+                                      _stream(stream)))
+    return workspace
+
+
+def irm_pages_fork(src, dst, kv, seq_len, page_table, refcount, workspace=None, stream=None):
+    """Forks requests src into the empty slots dst (integers in host memory): full pages are shared, the
+    partly filled last page is copied in every layer of kv ([n_layers, n_pages, 64, 576] bf16)."""
+    src, dst = _host_i32(src, "src"), _host_i32(dst, "dst")
+    if len(src) != len(dst):
+        raise ValueError("src and dst must have the same length")
+    _need_pages(seq_len, page_table, refcount)
+    layers, n_pages = _need_cache(kv, int(refcount.shape[0]))
+    n_slots = int(seq_len.shape[0])
+    workspace = _workspace(workspace, pages_workspace_size(n_slots) if workspace is None else 0, seq_len.device)
+    with _one_device(seq_len, kv, page_table, refcount, workspace):
+        _check(lib().irm_pages_fork(_ptr(src), _ptr(dst), len(src), _ptr(kv), layers, _ptr(seq_len), n_slots,
+                                    _ptr(page_table), int(page_table.shape[1]), _ptr(refcount), n_pages,
+                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+    return workspace
+
+
+def irm_pages_compact(kv, page_table, base, path, n_accept, workspace=None, stream=None):
+    """Moves accepted drafts' rows base + path[:, k] to base + k, k < n_accept, in every layer of kv; base,
+    n_accept [n_slots] and path [n_slots, max_path] int32 on the device (irm_tree_verify's outputs)."""
+    layers, n_pages = _need_cache(kv)
+    _need(page_table, torch.int32, "page_table", 2)
+    n_slots = int(page_table.shape[0])
+    for t, ndim, name in ((base, 1, "base"), (path, 2, "path"), (n_accept, 1, "n_accept")):
+        _need(t, torch.int32, name, ndim)
+        _need_shape(t, (n_slots, *t.shape[1:]), name)
+    workspace = _workspace(workspace, WORKSPACE_HEADER, kv.device)
+    with _one_device(kv, page_table, base, path, n_accept, workspace):
+        _check(lib().irm_pages_compact(_ptr(kv), layers, n_pages, _ptr(page_table), int(page_table.shape[1]), n_slots,
+                                       _ptr(base), _ptr(path), int(path.shape[1]), _ptr(n_accept), _ptr(workspace),
+                                       workspace.numel(), _stream(stream)))
+    return workspace
+
+
+def irm_pages_copy(kv, src, dst, stream=None):
+    """Copies pages src[i] -> dst[i] (integers in host memory) in every layer of kv."""
+    src, dst = _host_i32(src, "src"), _host_i32(dst, "dst")
+    if len(src) != len(dst):
+        raise ValueError("src and dst must have the same length")
+    layers, n_pages = _need_cache(kv)
+    with _one_device(kv):
+        _check(lib().irm_pages_copy(_ptr(kv), layers, n_pages, _ptr(src), _ptr(dst), len(src), _stream(stream)))
 
 
 ASSEMBLE_S1 = 1

@@ -635,6 +635,8 @@ const char* irm_status_string(int status) {
     case IRM_ERR_DEVICE_TIMEOUT: return "device pipeline wait timed out";
     case IRM_ERR_DEVICE_BOUNDS: return "device saw a source row or page outside its buffer";
     case IRM_ERR_WORKSPACE: return "workspace missing or too small";
+    case IRM_ERR_OUT_OF_PAGES: return "too few free pages";
+    case IRM_ERR_SHARED_PAGE: return "growth inside a shared page";
     default: return "unknown status";
   }
 }
@@ -665,6 +667,8 @@ irm_status irm_device_status(void* workspace, cudaStream_t stream) {
   }
   if (word & 1) return fail(IRM_ERR_DEVICE_TIMEOUT, "a device pipeline wait exceeded its limit");
   if (word & 2) return fail(IRM_ERR_DEVICE_BOUNDS, "a kernel met a source row or page outside its buffer");
+  if (word & 8) return fail(IRM_ERR_SHARED_PAGE, "a request would grow inside a page that it shares");
+  if (word & 4) return fail(IRM_ERR_OUT_OF_PAGES, "too few free pages for a resize or fork");
   return IRM_OK;
 }
 

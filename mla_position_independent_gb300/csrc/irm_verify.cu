@@ -1,0 +1,409 @@
+// Verification of drafted tokens against the target model's probabilities, from given uniform
+// numbers (speculative sampling over a tree; the emitted tokens follow the target's
+// distribution exactly, whatever was drafted).
+//
+// Per request, with node 0 the last committed token, p_u the target's and q_u the draft
+// model's row at node u, and w, S the residual distribution (unnormalised) and its sum:
+//   u = 0, w = p_0, S = 1.  For the children i of u in index order, x = token_i:
+//     accept when r_i q_u(x) S < w(x): u = i, w = p_i, S = 1;
+//     else w <- max(w - S q_u, 0), S <- sum w.
+//   When no child is left: next token = the lowest v with cumsum(w)(v) > r_0 sum(w).
+// Without draft probabilities the drafts are taken as chosen without chance (q one-hot at the
+// child's token): a rejection takes w(x) out of w and S.
+// A node's children come after it, so one pass over the nodes in index order is the walk.
+//
+// Arithmetic.  Sums over the vocabulary decide which token comes out, so they must not depend
+// on the order of addition or on the split: every probability becomes a 44-bit fixed-point
+// integer (resolution 5.7e-14) and sums are 64-bit integers, exact in any order (2^20 entries
+// of 1.0 fit).  fp32 sums would shift the boundaries of a flat 100k-entry row by more than
+// some of its entries are wide; fp64 adds run at ~1/60 of the integer rate here.
+// The acceptance tests run in fp64 on the fp32 inputs, in the order written above.
+//
+// What bounds it: one row of V fp32 (two with draft probabilities) per request for the final
+// draw, read twice (sum, then locate: the second read is one warp's segment).  A cluster of C CTAs
+// shares a request's row in contiguous warp segments; the CTA totals travel through
+// distributed shared memory.  The children's probabilities are gathered in one round of loads,
+// all nodes at once, before the walk, which then runs in shared memory.
+#include <cuda_runtime.h>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "irm_common.cuh"
+#include "irm_host_util.h"
+
+namespace irm {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBatch = 1024;  // requests per launch (their offsets travel in the parameters)
+constexpr uint32_t kFull = 0xffffffffu;
+
+struct VerifyArgs {
+  const float* target;
+  const float* draft;
+  int64_t ld;  // elements between rows
+  int V, b0, max_path;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* uniforms;
+  int32_t* n_accept;
+  int32_t* path;
+  int32_t* next_token;
+  int* status;
+  int32_t indptr[kBatch + 1];
+};
+static_assert(sizeof(VerifyArgs) <= 32764, "kernel parameter block");
+
+// Probability in units of 2^-44; NaN and negative values are 0, values above 1 are 1.
+__device__ __forceinline__ uint64_t fixed44(float p) {
+  return __float2ull_rn(fminf(fmaxf(p, 0.f), 1.f) * 17592186044416.f);
+}
+__device__ __forceinline__ double from44(uint64_t s) { return (double)s * 0x1p-44; }
+
+struct Shared {
+  int32_t par[IRM_MAX_TREE], tok[IRM_MAX_TREE], path[IRM_MAX_TREE];
+  float r[IRM_MAX_TREE], p[IRM_MAX_TREE], q[IRM_MAX_TREE];
+  uint64_t s_fix[IRM_MAX_TREE];  // draft mode: S before rejection t at the current node
+  int32_t rej[IRM_MAX_TREE];     // target-only mode: distinct tokens rejected at the current node
+  uint64_t wsum[kWarps];
+  uint64_t ctot[2][kMaxCluster];
+  uint64_t tot_out, before_out;
+  int32_t u, k, next_i, depth, need_sum, pass;
+};
+
+// Residual of one vocabulary entry after k rejections, in fixed point.
+__device__ __forceinline__ uint64_t residual(uint64_t w, uint64_t q, const uint64_t* s_fix, int k) {
+  for (int t = 0; t < k; ++t) {
+    const uint64_t sub = __umul64hi(q << 19, s_fix[t] << 1);  // q S / 2^44
+    w = w > sub ? w - sub : 0ull;
+  }
+  return w;
+}
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// Four consecutive entries of a row as fixed-point residuals (zero past the end).
+template <bool VEC>
+__device__ __forceinline__ void load4(const float* p, const float* q, int v, int end, float4& a, float4& b) {
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
+  b = a;
+  if (VEC) {
+    if (v < end) {  // segments, rows and the vocabulary's end are whole vectors here
+      a = __ldg(reinterpret_cast<const float4*>(p + v));
+      if (q != nullptr) b = __ldg(reinterpret_cast<const float4*>(q + v));
+    }
+  } else {
+    float* ap = reinterpret_cast<float*>(&a);
+    float* bp = reinterpret_cast<float*>(&b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v + e < end) {
+        ap[e] = __ldg(p + v + e);
+        if (q != nullptr) bp[e] = __ldg(q + v + e);
+      }
+  }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t C;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+  const uint32_t rank = cluster_ctarank();
+  const int b = (int)(blockIdx.x / C);
+  const int lo = a.indptr[b], n = a.indptr[b + 1] - lo;
+  const int64_t gb = (int64_t)a.b0 + b;
+  if (n == 0) {  // the same in every CTA of the cluster
+    if (rank == 0) {
+      for (int k = tid; k < a.max_path; k += kThreads) a.path[gb * a.max_path + k] = -1;
+      if (tid == 0) {
+        a.n_accept[gb] = 0;
+        a.next_token[gb] = -1;
+      }
+    }
+    return;
+  }
+  cluster_arrive();  // waited for before the first store into a peer's shared memory
+  // ---- the tree and its tokens' probabilities at their parents, one round of loads ------
+  bool bad = false;
+  for (int i = tid; i < n; i += kThreads) {
+    const int par = a.parents[lo + i], tok = a.tokens[lo + i];
+    const bool child = i > 0 && par >= 0 && par < i, in = tok >= 0 && tok < a.V;
+    float p = 0.f, q = 0.f;
+    if (child && in) {
+      p = __ldg(a.target + (int64_t)(lo + par) * a.ld + tok);
+      if (a.draft != nullptr) q = __ldg(a.draft + (int64_t)(lo + par) * a.ld + tok);
+    }
+    bad |= i > 0 && !(child && in);
+    sh.par[i] = child ? par : -1;
+    sh.tok[i] = in ? tok : -1;
+    sh.p[i] = fminf(fmaxf(p, 0.f), 1.f);
+    sh.q[i] = fminf(fmaxf(q, 0.f), 1.f);
+    sh.r[i] = a.uniforms[lo + i];
+  }
+  if (bad && rank == 0) set_status(a.status, kDevErrBounds);
+  if (tid == 0) {
+    sh.u = 0;
+    sh.k = 0;
+    sh.next_i = 1;
+    sh.depth = 1;
+    sh.path[0] = 0;
+    sh.pass = 0;
+    sh.s_fix[0] = 1ull << 44;
+  }
+  __syncthreads();
+  cluster_wait();
+
+  const int segs = (int)C * kWarps;
+  const int seg = ((a.V + segs - 1) / segs + 3) / 4 * 4;
+  const int v0 = min(a.V, ((int)rank * kWarps + warp) * seg), v1 = min(a.V, v0 + seg);
+
+  // Sum of the residual after k rejections at node u over the vocabulary: sh.tot_out, and what
+  // lies before this CTA's slice: sh.before_out; sh.wsum keeps this CTA's warp sums.
+  auto vocab_sum = [&](int u, int k) {
+    const float* p = a.target + (int64_t)(lo + u) * a.ld;
+    const float* q = (a.draft != nullptr && k > 0) ? a.draft + (int64_t)(lo + u) * a.ld : nullptr;
+    uint64_t s = 0;
+    for (int v = v0 + 4 * lane; v < v1; v += 128 * 4) {
+      float4 x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) load4<VEC>(p, q, v + 128 * e, v1, x[e], y[e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          s += q != nullptr ? residual(fixed44(xs[f]), fixed44(ys[f]), sh.s_fix, k) : fixed44(xs[f]);
+      }
+    }
+    s = warp_sum(s);
+    if (lane == 0) sh.wsum[warp] = s;
+    __syncthreads();
+    if (a.draft == nullptr)  // the rejected tokens leave the row
+      for (int t = tid; t < k; t += kThreads) {
+        const int w = sh.rej[t] / seg - (int)rank * kWarps;
+        if (w >= 0 && w < kWarps)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&sh.wsum[w]),
+                    (unsigned long long)(0ull - fixed44(__ldg(p + sh.rej[t]))));
+      }
+    __syncthreads();
+    const int slot = sh.pass & 1;
+    if (warp == 0) {
+      const uint64_t mine = warp_sum(lane < kWarps ? sh.wsum[lane] : 0ull);
+      if (lane < (int)C) st_cluster_u64(mapa_shared(smem_u32(&sh.ctot[slot][rank]), (uint32_t)lane), mine);
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (tid == 0) {
+      uint64_t t = 0, before = 0;
+      for (int c = 0; c < (int)C; ++c) {
+        if (c == (int)rank) before = t;
+        t += sh.ctot[slot][c];
+      }
+      sh.tot_out = t;
+      sh.before_out = before;
+      ++sh.pass;
+    }
+    __syncthreads();
+  };
+
+  // ---- the walk: warp 0 until a residual sum is needed (draft mode) or no child is left ----
+  for (;;) {
+    if (warp == 0) {
+      int u = sh.u, k = sh.k, i = sh.next_i, depth = sh.depth, need = 0;
+      double S = a.draft != nullptr ? from44(sh.s_fix[k]) : 1.0;
+      while (depth < a.max_path) {
+        // next child of u, 32 nodes at a time
+        int found = -1;
+        for (int base = i; base < n; base += 32) {
+          const unsigned m = __ballot_sync(kFull, base + lane < n && sh.par[base + lane] == u);
+          if (m) {
+            found = base + __ffs((int)m) - 1;
+            break;
+          }
+        }
+        if (found < 0) break;
+        i = found + 1;
+        const int x = sh.tok[found];
+        const double p = (double)sh.p[found], r = (double)sh.r[found];
+        double w = p;
+        bool take;
+        if (a.draft != nullptr) {
+          const double q = (double)sh.q[found];
+          for (int t = 0; t < k; ++t) w = fmax(w - q * from44(sh.s_fix[t]), 0.0);
+          take = x >= 0 && r * q * S < w;
+        } else {
+          bool again = false;  // already rejected at this node
+          for (int t = lane; t < k; t += 32) again |= sh.rej[t] == x;
+          if (__any_sync(kFull, again)) w = 0.0;
+          take = x >= 0 && r * S < w;
+        }
+        if (take) {
+          u = found;
+          k = 0;
+          S = 1.0;
+          if (lane == 0) sh.path[depth] = found;
+          ++depth;
+        } else if (x >= 0) {
+          if (a.draft != nullptr) {
+            ++k;
+            // the new sum only matters when another child is left to test
+            bool more = false;
+            for (int t = i + lane; t < n; t += 32) more |= sh.par[t] == u;
+            need = __any_sync(kFull, more) ? 1 : 0;
+            if (need) break;
+          } else if (w > 0.0) {
+            if (lane == 0) sh.rej[k] = x;
+            __syncwarp();
+            ++k;
+            S -= w;
+          }
+        }
+      }
+      if (lane == 0) {
+        sh.u = u;
+        sh.k = k;
+        sh.next_i = i;
+        sh.depth = depth;
+        sh.need_sum = need;
+      }
+    }
+    __syncthreads();
+    if (!sh.need_sum) break;
+    const int u = sh.u, k = sh.k;
+    vocab_sum(u, k);
+    if (tid == 0) sh.s_fix[k] = sh.tot_out;
+    __syncthreads();
+  }
+
+  // ---- the next token: inverse of the residual's running sum --------------------------
+  const int u = sh.u;
+  int k = sh.k;
+  vocab_sum(u, k);
+  if (sh.tot_out == 0 && k > 0) {  // nothing is left but rounding: draw from the target's row
+    k = 0;
+    vocab_sum(u, 0);
+  }
+  const uint64_t total = sh.tot_out;
+  if (rank == 0) {
+    for (int t = tid; t < a.max_path; t += kThreads) a.path[gb * a.max_path + t] = t < sh.depth ? sh.path[t] : -1;
+    if (tid == 0) a.n_accept[gb] = sh.depth;
+    if (tid == 0 && total == 0) a.next_token[gb] = -1;
+  }
+  if (total == 0) return;
+  const double rf = (double)fminf(fmaxf(sh.r[0], 0.f), 1.f);
+  uint64_t thr = (uint64_t)(rf * (double)total);
+  if (thr >= total) thr = total - 1;
+  // the warp whose segment holds the threshold
+  uint64_t before = sh.before_out;
+  for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+  if (thr < before || thr >= before + sh.wsum[warp]) return;
+  const float* p = a.target + (int64_t)(lo + u) * a.ld;
+  const float* q = (a.draft != nullptr && k > 0) ? a.draft + (int64_t)(lo + u) * a.ld : nullptr;
+  for (int vb = v0; vb < v1; vb += 128) {
+    const int v = vb + 4 * lane;
+    float4 x, y;
+    load4<VEC>(p, q, v, v1, x, y);
+    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    uint64_t w4[4], mine = 0;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      uint64_t w = fixed44(xs[f]);
+      if (a.draft != nullptr) {
+        if (k > 0) w = residual(w, fixed44(ys[f]), sh.s_fix, k);
+      } else {
+        for (int t = 0; t < k; ++t)
+          if (sh.rej[t] == v + f) w = 0;
+      }
+      w4[f] = w;
+      mine += w;
+    }
+    uint64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t t = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const uint64_t all = __shfl_sync(kFull, incl, 31);
+    if (thr < before + all) {
+      uint64_t at = before + incl - mine;
+      if (thr >= at && thr < at + mine) {
+        int f = 0;
+        while (thr >= at + w4[f]) at += w4[f++];
+        a.next_token[gb] = v + f;
+      }
+      return;
+    }
+    before += all;
+  }
+}
+
+}  // namespace
+}  // namespace irm
+
+extern "C" irm_status irm_tree_verify(const float* target_probs, const float* draft_probs, int64_t row_stride,
+                                      int32_t vocab, const int32_t* tokens, const int32_t* parents,
+                                      const float* uniforms, const int32_t* q_indptr_host, int B, int max_path,
+                                      int32_t* n_accept, int32_t* path, int32_t* next_token, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+  using namespace irm;
+  int most = 0;
+  irm_status st = check_trees(q_indptr_host, B, &most);
+  if (st != IRM_OK) return st;
+  if (vocab < 1 || vocab > (1 << 20)) return fail(IRM_ERR_UNSUPPORTED, "vocab %d outside [1, 2^20]", vocab);
+  if (row_stride < vocab) return fail(IRM_ERR_INVALID_ARG, "row_stride is smaller than vocab");
+  if (max_path < 1) return fail(IRM_ERR_INVALID_ARG, "max_path must be positive");
+  if (!n_accept || !path || !next_token || (most > 0 && (!target_probs || !tokens || !parents || !uniforms)))
+    return fail(IRM_ERR_INVALID_ARG, "null device pointer");
+  for (const void* p : {(const void*)target_probs, (const void*)draft_probs, (const void*)tokens, (const void*)parents,
+                        (const void*)uniforms, (const void*)n_accept, (const void*)path, (const void*)next_token})
+    if (!aligned(p, 4)) return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < IRM_WORKSPACE_HEADER)
+    return fail(IRM_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %d bytes", IRM_WORKSPACE_HEADER);
+  VerifyArgs a{};
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.ld = row_stride;
+  a.V = vocab;
+  a.max_path = max_path;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.uniforms = uniforms;
+  a.n_accept = n_accept;
+  a.path = path;
+  a.next_token = next_token;
+  a.status = static_cast<int*>(workspace);
+  const bool vec = vocab % 4 == 0 && row_stride % 4 == 0 && aligned(target_probs, 16) && aligned(draft_probs, 16);
+  for (int b0 = 0; b0 < B; b0 += kBatch) {
+    const int nb = B - b0 < kBatch ? B - b0 : kBatch;
+    a.b0 = b0;
+    std::memcpy(a.indptr, q_indptr_host + b0, (size_t)(nb + 1) * sizeof(int32_t));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nb * kMaxCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, tree_verify_kernel<true>, a)
+                              : cudaLaunchKernelEx(&cfg, tree_verify_kernel<false>, a);
+    if (e != cudaSuccess) return cuda_fail(e, "tree verification launch");
+  }
+  return IRM_OK;
+}
