@@ -4,102 +4,689 @@
 //   s_t = scale * (q_lat . cKV_t + q_rope . k_r,t) over the rows t < ctx and the drafts' rows
 //   ctx + k whose bit k is set in node i's mask;  O = softmax(s) . cKV, lse = ln sum exp(s).
 //
-// One block per query row: a warp computes one key's score at a time, the block keeps a
-// running maximum and sum over tiles of 64 keys (one page) and four output columns a thread.
+// Work unit: 128 query rows (of a request's n H rows, node-major) x a run of pages, on a pair
+// of CTAs (a cluster of 2, one CTA per SM); a page (64 rows) is one tile.
+//   - The contraction of Q K^T and the columns of O are split over the pair: CTA r loads, with
+//     TMA, cKV columns [256 r, 256 r + 256) and k_r columns [32 r, 32 r + 32) of each page, so
+//     each row is read once by the pair, and 36 KiB a tile leave room for four tiles in flight.
+//     128 rows x 512 fp32 columns of O alone would fill one SM's TMEM.
+//   - The softmax is split by rows: CTA r owns query rows [64 r, 64 r + 64).  Each CTA sends the
+//     other its fp32 partial scores of the other's rows (16 KiB a tile, st.async), adds what it
+//     receives to its own partials, and after the exponentials writes its rows of P into both
+//     CTAs' shared memory (8 KiB a tile).  Nothing is computed twice, and no partial score is
+//     rounded on the way.
+//   - O accumulates in TMEM (256 columns), P V reads P and the page's cKV from shared memory;
+//     Q K^T reads Q's cKV columns from TMEM (128 columns) into one of two score buffers (64 each).
+//   - Two sets of four warps take even and odd tiles, a thread a row: of each set the two warps
+//     of the CTA's own rows run the softmax, the other two ship scores.  While one set is in its
+//     exponentials the other is in its exchange; all that passes from tile to tile is the running
+//     maximum (in shared memory, one mbarrier per 32 rows).
+//   - The maximum moves only when a tile exceeds it by 2^8 (P stays <= 256, and the final sum uses
+//     the same maximum, so the result is exact); then the owner's factor per row, which travels
+//     with P, rescales O in both CTAs.  l is summed in fp32 before P is rounded to bf16 for
+//     the tensor cores (the rounding of P, half a step of bf16 a key, is of the output's own size).
+//   - Rows that no node of the unit sees (masked drafts, rows behind the last one) may hold NaN:
+//     a warp clears them in shared memory before the page is used.
+// Warps: 0-7 scores, 8 TMA, 9 Q K^T issue and TMEM, 10 P V issue, 11 the clearing.
+// Long contexts are cut into pieces of equal length (the rest last, so that the short ones fill the
+// gaps); their normalised fp32 partials are merged by a second kernel.
+// Every wait is bounded (2 s) and reports a timeout in the status word.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "irm_common.cuh"
 #include "irm_host_util.h"
+#include "irm_pipeline.cuh"
+#include "irm_tma.cuh"
 
 namespace irm {
 namespace {
 
-constexpr int kBatch = 1024;  // requests per launch (their lengths travel in the parameters)
-constexpr int kThreads = 128;
+constexpr int kBatch = 256;  // requests per launch (their lengths travel in the parameters)
+constexpr int kBM = 128;     // query rows of a unit
+constexpr int kHalf = 64;    // of which a CTA owns
+constexpr int kScoreWarps = 8;
+constexpr int kTmaWarp = 8, kSWarp = 9, kPvWarp = 10;  // and 11, the clearing
+constexpr int kThreads = 12 * 32;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Shared memory: barriers and small arrays, then 1024-byte aligned tiles.
+constexpr int kStages = 4;
+constexpr uint32_t kSlab = 64 * 128;                  // 64 rows x 64 columns
+constexpr uint32_t kStage = 4 * kSlab + 64 * 64;      // + 64 rows x 32 k_r columns
+constexpr uint32_t kXBytes = kHalf * kPage * 4;       // received scores of one tile
+constexpr uint32_t kPBytes = kBM * 128;               // P of one tile
+constexpr uint32_t kOffBars = 0;
+constexpr uint32_t kOffTmem = 256;
+constexpr uint32_t kOffAbort = 260;
+constexpr uint32_t kOffMax = 512;                     // float [64]: running maximum of the own rows
+constexpr uint32_t kOffCorr = kOffMax + 64 * 4;       // float [2][64]: the peer rows' factors
+constexpr uint32_t kOffSum = kOffCorr + 2 * 64 * 4;   // float2 [2][64]: (maximum, sum) of each set
+constexpr uint32_t kOffInv = kOffSum + 2 * 64 * 8;    // float [128]: 1 / l of every row
+constexpr uint32_t kOffQr = 3072;                     // 128 rows x 64 B (swizzled)
+constexpr uint32_t kOffX = kOffQr + 128 * 64;         // [2] 16-byte words [16][64 rows]
+constexpr uint32_t kOffP = kOffX + 2 * kXBytes;
+constexpr uint32_t kOffKv = kOffP + 2 * kPBytes;
+constexpr uint32_t kSmem = kOffKv + kStages * kStage + 1024;  // room to align the base
+static_assert(kOffInv + 128 * 4 <= kOffQr && kOffQr % 1024 == 0 && kOffX % 1024 == 0 && kOffKv % 1024 == 0, "layout");
+static_assert(kSmem <= 232448, "shared memory");
+
+enum : int {
+  BAR_LANDED = 0,                    // [stage] TMA bytes of the page (1 + tx)
+  BAR_CLEAR = BAR_LANDED + kStages,  // [stage] unseen rows cleared (pages with drafts only)
+  BAR_FREE = BAR_CLEAR + kStages,    // [stage] P V of the page done, and the clearing warp past it (2)
+  BAR_S_FULL = BAR_FREE + kStages,   // [2] Q K^T done
+  BAR_S_FREE = BAR_S_FULL + 2,       // [2] the set's live warps read the score buffer
+  BAR_X_FULL = BAR_S_FREE + 2,       // [2] the peer's partial scores arrived (1 + tx)
+  BAR_X_FREE = BAR_X_FULL + 2,       // [2] the peer's warps have read what was sent
+  BAR_PR_FULL = BAR_X_FREE + 2,      // [2] the peer's rows of P and factors arrived (1 + tx)
+  BAR_P_FREE = BAR_PR_FULL + 2,      // [2] P V of the buffer done in both CTAs (2)
+  BAR_GO = BAR_P_FREE + 2,           // [2] P complete and O rescaled: the set's live warps
+  BAR_PV = BAR_GO + 2,               // P V of a tile done in this CTA
+  BAR_MAX = BAR_PV + 1,              // [2] running maximum of 32 own rows published
+  BAR_Q = BAR_MAX + 2,               // Q stored (8 warps)
+  BAR_DRAIN = BAR_Q + 1,             // [2] all UMMAs of an issuer done
+  NUM_BARS = BAR_DRAIN + 2,
+};
+static_assert(NUM_BARS * 8 <= kOffTmem, "barrier area");
+
+constexpr uint32_t kTmemO = 0, kTmemQ = 256, kTmemS = 384, kTmemCols = 512;
+constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kPage, 0, 0);
+constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, 256, 0, 1);
 
 struct TreeArgs {
+  CUtensorMap map_lat, map_rope;  // [rows, 576]: boxes of 64 x 64 and 64 rows x 32 columns
   const __nv_bfloat16* q_lat;
   const __nv_bfloat16* q_rope;
-  const __nv_bfloat16* kv;
   const int32_t* page_table;
   const uint32_t* mask;
   int64_t n_pages;
   int B, b0, H, max_pages, mask_words;
-  float scale;
+  int piece;   // pages of a piece
+  int n_long;  // units of full pieces; the requests' rests follow
+  float scale_log2;
   __nv_bfloat16* out;
   float* lse;
+  float* opart;    // fp32 [partial][128][512]
+  float* lsepart;  // fp32 [partial][128], log2 units
   int* status;
   int32_t ctx[kBatch], indptr[kBatch + 1];
+  int32_t long_base[kBatch + 1], rest_base[kBatch + 1], part_base[kBatch + 1];
 };
 static_assert(sizeof(TreeArgs) <= 32764, "kernel parameter block");
 
-__global__ void __launch_bounds__(kThreads) tree_attn_kernel(const __grid_constant__ TreeArgs a) {
-  __shared__ float score[kPage];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = (int64_t)blockIdx.x;  // node of this launch * H + head
-  const int node = (int)(row / a.H) + a.indptr[0];
-  int lo = 0, hi = a.B;
+__host__ __device__ inline int row_tiles(int n, int H) { return (n * H + kBM - 1) / kBM; }
+__host__ __device__ inline int page_count(int ctx, int n) { return n > 0 ? (ctx + n + kPage - 1) / kPage : 0; }
+
+// Last b in [0, B) with base[b] <= u: the owner of u among entries with a positive share.
+__device__ __forceinline__ int owner_of(const int32_t* base, int B, int u) {
+  int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.indptr[mid] <= node) lo = mid; else hi = mid;
+    if (base[mid] <= u) lo = mid; else hi = mid;
   }
-  const int b = lo, ctx = a.ctx[b], n = a.indptr[b + 1] - a.indptr[b];
-  const int64_t grow = (int64_t)a.indptr[0] * a.H + row;
-  const uint32_t* mask = a.mask + (int64_t)node * a.mask_words;
-  const int32_t* ptab = a.page_table + (int64_t)(a.b0 + b) * a.max_pages;
-  float q[18];
+  return lo;
+}
+
+// 64 mask bits from bit `first` (>= 0) of a node's mask on; bits from n on are clear.
+__device__ __forceinline__ uint64_t mask_window(const uint32_t* mask, int words, int first, int n) {
+  if (first >= n) return 0;
+  const int w = first >> 5, s = first & 31;
+  const uint64_t lo = mask[w], mid = w + 1 < words ? mask[w + 1] : 0u, hi = w + 2 < words ? mask[w + 2] : 0u;
+  uint64_t v = (lo | mid << 32) >> s;
+  if (s != 0) v |= hi << (64 - s);
+  return n - first < 64 ? v & ((1ull << (n - first)) - 1) : v;
+}
+
+// Which of the rows T .. T + 63 of its request a node sees.
+__device__ __forceinline__ uint64_t seen_rows(const uint32_t* mask, int words, int T, int ctx, int n) {
+  const int off = T - ctx;
+  if (off >= 0) return mask_window(mask, words, off, n);
+  if (off <= -64) return ~0ull;
+  return ((1ull << -off) - 1) | mask_window(mask, words, 0, n) << -off;
+}
+
+// Paired fp32 arithmetic of sm_100 and later; each half rounds as the scalar form.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// O columns of this warp's 32 lanes times each lane's factor.
+__device__ __forceinline__ void rescale_o(uint32_t tO, float corr) {
+#pragma unroll 1
+  for (int c = 0; c < 256; c += 32) {
+    uint32_t r[32];
+    tmem_ld32(tO + c, r);
+    tmem_ld_wait();
 #pragma unroll
-  for (int e = 0; e < 16; ++e) q[e] = __bfloat162float(a.q_lat[grow * kDLat + 32 * e + lane]);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) q[16 + e] = __bfloat162float(a.q_rope[grow * kDRope + 32 * e + lane]);
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int T = 0; T < ctx + n; T += kPage) {
-    const int page = ptab[T / kPage];
-    const bool in = page >= 0 && page < a.n_pages;
-    if (!in && tid == 0) set_status(a.status, kDevErrBounds);
-    const __nv_bfloat16* rows = a.kv + (int64_t)(in ? page : 0) * kPage * kDRow;
-    for (int r = warp; r < kPage; r += kThreads / 32) {
-      const int t = T + r, k = t - ctx;
-      const bool see = t < ctx || (k < n && (mask[k >> 5] >> (k & 31) & 1u));
-      float s = 0.f;
-      if (see && in) {
-#pragma unroll
-        for (int e = 0; e < 18; ++e) s += q[e] * __bfloat162float(rows[r * kDRow + 32 * e + lane]);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-      if (lane == 0) score[r] = see ? s * a.scale : -INFINITY;
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
+    tmem_st32(tO + c, r);
+  }
+  tmem_st_wait();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TreeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // alike in both CTAs
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const uint32_t peer = (uint32_t)rank ^ 1u;
+
+  // ---- the unit -------------------------------------------------------------------------
+  const int unit = (int)(blockIdx.x >> 1);
+  const bool is_rest = unit >= a.n_long;
+  const int at = is_rest ? unit - a.n_long : unit;
+  const int b = owner_of(is_rest ? a.rest_base : a.long_base, a.B, at);
+  const int first_node = a.indptr[b], n = a.indptr[b + 1] - first_node, ctx = a.ctx[b];
+  const int mtiles = row_tiles(n, a.H), tiles_all = page_count(ctx, n);
+  const int in_b = at - (is_rest ? a.rest_base[b] : a.long_base[b]);
+  const int piece = is_rest ? tiles_all / a.piece : in_b / mtiles;
+  const int mtile = is_rest ? in_b : in_b % mtiles;
+  const int kb = piece * a.piece;
+  const int ntiles = min(a.piece, tiles_all - kb);
+  const int pieces = (tiles_all + a.piece - 1) / a.piece;
+  const int row0 = mtile * kBM, rows_valid = min(kBM, n * a.H - row0);
+  const int64_t grow0 = (int64_t)first_node * a.H + row0;  // row of the batch's T H
+  const int tail = max(0, ctx / kPage - kb);               // first tile of the unit with drafts
+
+  auto bar = [&](int i) -> uint32_t { return sb + kOffBars + 8u * (uint32_t)i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffAbort);
+  // quadrants of 32 rows that hold valid rows, of the own and of the peer's 64
+  auto live_of = [&](int r) -> int { return max(0, min(2, (rows_valid - kHalf * r + 31) / 32)); };
+  const int live_own = live_of(rank), live_peer = live_of((int)peer);
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(BAR_LANDED + s), 1);
+      mbar_init(bar(BAR_CLEAR + s), 1);
+      mbar_init(bar(BAR_FREE + s), 2);
     }
-    __syncthreads();
-    float mx = m;
-    for (int r = 0; r < kPage; ++r) mx = fmaxf(mx, score[r]);
-    if (mx != -INFINITY) {
-      const float corr = expf(m - mx);
-      m = mx;
-      l *= corr;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(BAR_S_FULL + s), 1);
+      mbar_init(bar(BAR_S_FREE + s), live_own + live_peer);
+      mbar_init(bar(BAR_X_FULL + s), 1);
+      mbar_init(bar(BAR_X_FREE + s), max(1, live_peer));
+      mbar_init(bar(BAR_PR_FULL + s), 1);
+      mbar_init(bar(BAR_P_FREE + s), 2);
+      mbar_init(bar(BAR_GO + s), live_own + live_peer);
+      mbar_init(bar(BAR_MAX + s), 1);
+      mbar_init(bar(BAR_DRAIN + s), 1);
+      // the first two tiles' bytes (a barrier that nothing is sent to is not waited for either)
+      if (live_own) mbar_arrive_expect_tx(bar(BAR_X_FULL + s), (uint32_t)live_own * (kXBytes / 2));
+      if (live_peer) mbar_arrive_expect_tx(bar(BAR_PR_FULL + s), (uint32_t)live_peer * (kPBytes / 4 + 128));
+    }
+    mbar_init(bar(BAR_PV), 1);
+    mbar_init(bar(BAR_Q), kScoreWarps);
+    *abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(sb + kOffTmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();  // every warp waits for it before its first remote access, or at its end
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
+  bool ok = true;
+
+  if (warp < kScoreWarps) {
+    const int set = warp >> 2, quad = warp & 3;
+    const bool own = (quad >> 1) == rank;
+    const bool live = quad * 32 < rows_valid;
+    const int m = quad * 32 + lane;   // row of the unit = TMEM lane
+    const int mh = m & (kHalf - 1);   // and of its owner's half
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + kTmemS + 64u * (uint32_t)set + lanes;
+    const uint32_t tO = tmem + kTmemO + lanes;
+    const bool valid = m < rows_valid;
+    // ---- Q: set h stores cKV slabs 2h, 2h + 1 of this CTA's columns, set 0 also q_rope ------
+    if (live) {
+      const int64_t row = grow0 + (valid ? m : 0);
+      const uint4* q = reinterpret_cast<const uint4*>(a.q_lat + row * kDLat + 256 * rank + 128 * set);
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] *= corr;
-      for (int r = 0; r < kPage; ++r) {
-        if (score[r] == -INFINITY) continue;
-        const float p = expf(score[r] - mx);
-        l += p;
-        if (in) {
+      for (int slab = 0; slab < 2; ++slab) {
+        uint32_t r[32];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] += p * __bfloat162float(rows[r * kDRow + 128 * e + tid]);
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = valid ? __ldg(q + slab * 8 + i) : zero;
+          r[4 * i] = v.x;
+          r[4 * i + 1] = v.y;
+          r[4 * i + 2] = v.z;
+          r[4 * i + 3] = v.w;
+        }
+        tmem_st32(tmem + kTmemQ + 32u * (uint32_t)(2 * set + slab) + lanes, r);
+      }
+      if (set == 0) {
+        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + row * kDRope + 32 * rank);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(sb + kOffQr + sw64_offset((uint32_t)m, (uint32_t)i), valid ? __ldg(qr + i) : zero);
+      }
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(BAR_Q));
+    __syncwarp();
+    cluster_wait();
+    const uint32_t buf = (uint32_t)set;  // a set's tiles all use the buffers of its number
+    const uint32_t remX = mapa_shared(sb + kOffX + buf * kXBytes, peer);
+    const uint32_t remXfull = mapa_shared(bar(BAR_X_FULL + set), peer);
+    const uint32_t remXfree = mapa_shared(bar(BAR_X_FREE + set), peer);
+    const uint32_t remP = mapa_shared(sb + kOffP + buf * kPBytes, peer);
+    const uint32_t remPfull = mapa_shared(bar(BAR_PR_FULL + set), peer);
+    const uint32_t remCorr = mapa_shared(sb + kOffCorr + buf * 256u + 4u * (uint32_t)mh, peer);
+    const uint4* X = reinterpret_cast<const uint4*>(smem + kOffX + buf * kXBytes);
+    float* max_sh = reinterpret_cast<float*>(smem + kOffMax);
+    const float* corr_sh = reinterpret_cast<const float*>(smem + kOffCorr + buf * 256u);
+    const uint32_t* mask = a.mask + (int64_t)(first_node + (row0 + (valid ? m : 0)) / a.H) * a.mask_words;
+    const bool first_quad = (quad & 1) == 0;  // arms the byte counts
+    float m_l = -INFINITY, l = 0.f;           // this set's sum, relative to m_l
+
+    for (int j = set; live && j < ntiles; j += 2) {  // warps without valid rows have no part in it
+      const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+      uint32_t s[64];
+      if (!(ok = warp_wait(bar(BAR_S_FULL + set), ph, abort_flag))) break;
+      tc_fence_after();
+      tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+      tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
+      float corr = 1.f;
+      if (own) {
+        // ================= softmax of a row =================
+        if (!(ok = warp_wait_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
+        float v[64];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = X[i * kHalf + mh];
+          v[4 * i] = __uint_as_float(s[4 * i]) + __uint_as_float(x.x);
+          v[4 * i + 1] = __uint_as_float(s[4 * i + 1]) + __uint_as_float(x.y);
+          v[4 * i + 2] = __uint_as_float(s[4 * i + 2]) + __uint_as_float(x.z);
+          v[4 * i + 3] = __uint_as_float(s[4 * i + 3]) + __uint_as_float(x.w);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (first_quad && j + 2 < ntiles) mbar_arrive_expect_tx(bar(BAR_X_FULL + set), (uint32_t)live_own * (kXBytes / 2));
+          mbar_arrive_remote_relaxed(remXfree);  // the values are in registers
+        }
+        if (j >= tail) {
+          const uint64_t see = valid ? seen_rows(mask, a.mask_words, (kb + j) * kPage, ctx, n) : 0ull;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!(see >> i & 1)) v[i] = -INFINITY;
+        }
+        float t[21];
+#pragma unroll
+        for (int i = 0; i < 21; ++i) t[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+#pragma unroll
+        for (int i = 0; i < 7; ++i) t[i] = fmax3(t[3 * i], t[3 * i + 1], t[3 * i + 2]);
+        const float top = fmaxf(fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), t[6]), v[63]) * a.scale_log2;
+        if (j > 0 && !(ok = warp_wait(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+        const float before = j > 0 ? max_sh[mh] : -INFINITY;
+        const bool up = top > before + 8.f;
+        const float now = up ? top : before;
+        max_sh[mh] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_MAX + (quad & 1)));
+        if (up) corr = fast_exp2(before - now);
+        if (now != m_l) l *= fast_exp2(m_l - now);  // m_l = -inf: l is 0
+        m_l = now;
+        const float use = now == -INFINITY ? 0.f : now;
+        const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2), m2 = f2_pack(-use, -use);
+        uint64_t sum[2] = {0ull, 0ull};
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 x = f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), c2, m2));
+          const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+          sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+          pk[i] = pack_bf16(p0, p1);
+        }
+        const float2 part = f2_unpack(f2_add(sum[0], sum[1]));
+        l += part.x + part.y;
+        if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          const uint32_t off = sw128_offset((uint32_t)m, (uint32_t)i);
+          st_async_v4_b32(remP + off, w, remPfull);
+          st_shared_v4(sb + kOffP + buf * kPBytes + off, w);
+        }
+        st_async_b32(remCorr, __float_as_uint(corr), remPfull);
+      } else {
+        // ================= partial scores of the peer's rows =================
+        if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
+                          remXfull);
+        if (!(ok = warp_wait_cluster(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
+        if (lane == 0 && first_quad && j + 2 < ntiles)
+          mbar_arrive_expect_tx(bar(BAR_PR_FULL + set), (uint32_t)live_peer * (kPBytes / 4 + 128));
+        corr = corr_sh[mh];
+      }
+      if (j > 0 && __any_sync(kFull, corr != 1.f)) {
+        if (!(ok = warp_wait(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+        tc_fence_after();
+        rescale_o(tO, corr);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_GO + set));
+    }
+    if (own) reinterpret_cast<float2*>(smem + kOffSum)[set * kHalf + mh] = make_float2(m_l, l);
+  } else if (warp == kTmaWarp) {
+    // ================= pages in =================
+    const int32_t* ptab = a.page_table + (int64_t)(a.b0 + b) * a.max_pages + kb;
+    if (lane == 0) {
+      tma_prefetch_map(&a.map_lat);
+      tma_prefetch_map(&a.map_rope);
+    }
+    int page = 0, sent = 0;
+    for (int j = 0; j < ntiles; ++j) {
+      if ((j & 31) == 0) {
+        page = j + lane < ntiles ? ptab[j + lane] : 0;
+        if (page < 0 || page >= a.n_pages) {
+          set_status(a.status, kDevErrBounds);
+          page = (int)a.n_pages;  // behind the tensor: zeros
+        }
+      }
+      const int y = __shfl_sync(kFull, page, j & 31) * kPage;
+      const int s = j % kStages;
+      if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
+      if (lane == 0) {
+        const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
+        mbar_arrive_expect_tx(bar(BAR_LANDED + s), kStage);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tma_load_2d(st + c * kSlab, &a.map_lat, 256 * rank + 64 * c, y, bar(BAR_LANDED + s));
+        tma_load_2d(st + 4 * kSlab, &a.map_rope, kDLat + 32 * rank, y, bar(BAR_LANDED + s));
+      }
+      sent = j + 1;
+    }
+    // the copies in flight land before the CTA ends, whatever became of the others
+    for (int j = max(0, sent - kStages); j < sent; ++j)
+      ok = warp_wait(bar(BAR_LANDED + j % kStages), (uint32_t)(j / kStages) & 1u, nullptr) && ok;
+    __syncwarp();
+    cluster_wait();
+  } else if (warp == kSWarp) {
+    // ================= Q K^T (one thread) =================
+    if (lane == 0) {
+      ok = mbar_wait(bar(BAR_Q), 0, abort_flag);
+      tc_fence_after();
+      const uint64_t aq = sdesc_sw64(sb + kOffQr, 512);
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int s = j % kStages, set = j & 1;
+        if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+        if (j >= tail && !(ok = mbar_wait(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = mbar_wait(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+        tc_fence_after();
+        fence_proxy_async_smem();  // Q's and the cleared rows' plain stores
+        const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
+        const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(st + 4 * kSlab, 512);
+        const uint32_t d = tmem + kTmemS + 64u * (uint32_t)set;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, sdesc_add(bd, c * kSlab + kk * 32), kIdescS, (c | kk) ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) umma_bf16(d, sdesc_add(aq, kk * 32), sdesc_add(bk, kk * 32), kIdescS, 1u);
+        umma_commit(bar(BAR_S_FULL + set));
+      }
+      umma_commit(bar(BAR_DRAIN));
+      ok = mbar_wait(bar(BAR_DRAIN), 0, nullptr) && ok;
+    }
+    __syncwarp();
+    cluster_wait();
+  } else if (warp == kPvWarp) {
+    // ================= P V (one thread) =================
+    if (lane == 0) {
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int s = j % kStages, set = j & 1;
+        if (!(ok = mbar_wait(bar(BAR_GO + set), (uint32_t)(j >> 1) & 1u, abort_flag))) break;
+        tc_fence_after();
+        fence_proxy_async_smem();  // P, written by both CTAs' threads
+        const uint64_t ad = sdesc_sw128(sb + kOffP + (uint32_t)set * kPBytes, 16, 1024);
+        const uint64_t bd = sdesc_sw128(sb + kOffKv + (uint32_t)s * kStage, kSlab, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(tmem + kTmemO, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), kIdescPV, (j | kk) ? 1u : 0u);
+        umma_commit(bar(BAR_FREE + s));
+        umma_commit(bar(BAR_PV));
+        umma_commit_multicast(bar(BAR_P_FREE + set), (uint16_t)3);
+      }
+      umma_commit(bar(BAR_DRAIN + 1));
+      ok = mbar_wait(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
+    }
+    __syncwarp();
+    cluster_wait();
+  } else {
+    // ================= rows that no node of the unit sees become zeros =================
+    const int node0 = row0 / a.H, node1 = (row0 + rows_valid - 1) / a.H;
+    for (int j = 0; j < ntiles; ++j) {
+      const int s = j % kStages;
+      uint32_t lo = 0, hi = 0;
+      if (j >= tail) {
+        uint64_t see = 0;
+        for (int i = node0 + lane; i <= node1; i += 32)
+          see |= seen_rows(a.mask + (int64_t)(first_node + i) * a.mask_words, a.mask_words, (kb + j) * kPage, ctx, n);
+        lo = __reduce_or_sync(kFull, (uint32_t)see);
+        hi = __reduce_or_sync(kFull, (uint32_t)(see >> 32));
+      }
+      if (!(ok = warp_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+      if (j >= tail) {
+        const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (uint64_t gone = ~((uint64_t)hi << 32 | lo); gone != 0; gone &= gone - 1) {
+          const uint32_t r = (uint32_t)__ffsll((long long)gone) - 1u;
+          st_shared_v4(st + (uint32_t)(lane >> 3) * kSlab + sw128_offset(r, (uint32_t)lane & 7u), zero);
+          if (lane < 4) st_shared_v4(st + 4 * kSlab + sw64_offset(r, (uint32_t)lane), zero);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_CLEAR + s));
+      }
+      // every page is waited for, and given back, so that no phase is missed
+      if (lane == 0) mbar_arrive(bar(BAR_FREE + s));
+    }
+    __syncwarp();
+    cluster_wait();
+  }
+  if (!ok) {
+    *abort_flag = 1;
+    set_status(a.status, kDevErrTimeout);
+  }
+  // ---- sums of the rows, to both CTAs ----------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const bool split = pieces > 1;
+  const int64_t part = split ? (int64_t)a.part_base[b] + (int64_t)mtile * pieces + piece : 0;
+  float* inv_sh = reinterpret_cast<float*>(smem + kOffInv);
+  if (tid < kHalf) {
+    const int m = kHalf * rank + tid;
+    const float2 x = reinterpret_cast<const float2*>(smem + kOffSum)[tid];
+    const float2 y = reinterpret_cast<const float2*>(smem + kOffSum)[kHalf + tid];
+    const float mx = fmaxf(x.x, y.x);
+    float l = 0.f;
+    if (mx != -INFINITY) l = x.y * fast_exp2(x.x - mx) + y.y * fast_exp2(y.x - mx);
+    const bool some = m < rows_valid && *abort_flag == 0 && l > 0.f;
+    const float inv = some ? 1.f / l : 0.f, lse2 = some ? mx + __log2f(l) : -INFINITY;
+    // both sets' sums are relative to the last maximum they saw; O is relative to the last one
+    // of all, which is the larger
+    inv_sh[m] = inv;
+    st_cluster_f32(mapa_shared(sb + kOffInv + 4u * (uint32_t)m, peer), inv);
+    if (m < rows_valid) {
+      if (split) a.lsepart[part * kBM + m] = lse2;
+      else if (a.lse != nullptr) a.lse[grow0 + m] = lse2 * kLn2;
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  // ---- O / l: 32 columns of a quadrant at a time, three warps to a quadrant ------------------
+  {
+    const int quad = warp & 3, m = quad * 32 + lane;
+    if (quad * 32 < rows_valid) {
+      const float inv = inv_sh[m];
+      const bool write = m < rows_valid;
+      for (int c = warp >> 2; c < 8; c += 3) {
+        uint32_t r[32];
+        tmem_ld32(tmem + kTmemO + ((uint32_t)(quad * 32) << 16) + 32u * c, r);
+        tmem_ld_wait();
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = inv > 0.f ? __uint_as_float(r[i]) * inv : 0.f;
+        if (!write) continue;
+        const int col = 256 * rank + 32 * c;
+        if (split) {
+          float4* o = reinterpret_cast<float4*>(a.opart + (part * kBM + m) * kDLat + col);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(a.out + (grow0 + m) * kDLat + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
         }
       }
     }
-    __syncthreads();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) a.out[grow * kDLat + 128 * e + tid] = __float2bfloat16_rn(acc[e] * inv);
-  if (a.lse != nullptr && tid == 0) a.lse[grow] = l > 0.f ? m + logf(l) : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
+
+// Rows whose context was cut into pieces: O = sum 2^(lse_p - max) O_p / sum 2^(lse_p - max).  A
+// block a row, 4 columns a thread; rows of uncut requests have nothing to do.
+constexpr int kMergeThreads = kDLat / 4;
+
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  const int node = a.indptr[0] + (int)(blockIdx.x / a.H);
+  const int b = owner_of(a.indptr, a.B, node);
+  const int n = a.indptr[b + 1] - a.indptr[b], tiles = page_count(a.ctx[b], n);
+  const int pieces = (tiles + a.piece - 1) / a.piece;
+  if (pieces <= 1) return;
+  const int row = (node - a.indptr[b]) * a.H + (int)(blockIdx.x % a.H);
+  const int64_t part = (int64_t)a.part_base[b] + (int64_t)(row / kBM) * pieces;
+  const float* lse = a.lsepart + part * kBM + row % kBM;
+  const float* o = a.opart + (part * kBM + row % kBM) * kDLat + 4 * threadIdx.x;
+  float mx = -INFINITY;
+  for (int p = 0; p < pieces; ++p) mx = fmaxf(mx, lse[(int64_t)p * kBM]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  if (mx != -INFINITY) {
+    for (int p = 0; p < pieces; ++p) {
+      const float w = fast_exp2(lse[(int64_t)p * kBM] - mx);
+      const float4 v = *reinterpret_cast<const float4*>(o + (int64_t)p * kBM * kDLat);
+      sum += w;
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t grow = (int64_t)a.indptr[b] * a.H + row;
+  *reinterpret_cast<uint2*>(a.out + grow * kDLat + 4 * threadIdx.x) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse != nullptr && threadIdx.x == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------------- host
+
+// Cut of a batch's contexts: pages of a piece, and what follows from it.
+struct Plan {
+  int piece, n_long, n_rest;
+  int64_t parts;  // partial results (units of cut requests)
+};
+
+// The cut with the least estimated time, in tile times: waves of units over the pairs of SMs, each
+// unit its pages and ~10 tile times of start and end; partials cost a merge.
+Plan plan_batch(const int32_t* ctx, const int32_t* indptr, int B, int H, int pairs) {
+  struct Like {
+    int tiles, mt, count;  // neighbouring requests alike count as one
+  } like[kBatch];
+  int kinds = 0, most = 1;
+  for (int b = 0; b < B; ++b) {
+    const int n = indptr[b + 1] - indptr[b], tiles = page_count(ctx[b], n), mt = row_tiles(n, H);
+    if (n == 0) continue;
+    most = std::max(most, tiles);
+    if (kinds > 0 && like[kinds - 1].tiles == tiles && like[kinds - 1].mt == mt) ++like[kinds - 1].count;
+    else like[kinds++] = Like{tiles, mt, 1};
+  }
+  Plan best{most, 0, 0, 0};
+  double best_cost = 1e300;
+  static constexpr int kCuts[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 19, 22, 25, 30, 38, 50, 76};
+  for (const int cuts : kCuts) {
+    if (cuts > most) break;
+    Plan p{(most + cuts - 1) / cuts, 0, 0, 0};
+    for (int k = 0; k < kinds; ++k) {
+      const Like& g = like[k];
+      const int full = g.tiles / p.piece, rest = g.tiles % p.piece ? 1 : 0, units = g.mt * g.count;
+      p.n_long += units * full;
+      p.n_rest += units * rest;
+      if (full + rest > 1) p.parts += (int64_t)units * (full + rest);
+    }
+    const double units = (double)p.n_long + p.n_rest;
+    const double cost = std::ceil(units / pairs) * (p.piece + 10.0) + (p.parts ? 6.0 + 0.02 * (double)p.parts : 0.0);
+    if (cost < best_cost - 1e-9) {
+      best_cost = cost;
+      best = p;
+    }
+  }
+  return best;
+}
+
+int sm_pairs() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    sms = 152;
+  }
+  return std::max(1, sms / 2);
+}
+
+size_t opart_bytes(int64_t parts) { return align_up((size_t)parts * kBM * kDLat * sizeof(float), 256); }
+size_t lsepart_bytes(int64_t parts) { return align_up((size_t)parts * kBM * sizeof(float), 256); }
 
 irm_status check_lengths(const int32_t* ctx, const int32_t* indptr, int B, int H, int* most_nodes, int64_t* most_rows) {
   irm_status st = check_trees(indptr, B, most_nodes);
@@ -116,6 +703,56 @@ irm_status check_lengths(const int32_t* ctx, const int32_t* indptr, int B, int H
   return IRM_OK;
 }
 
+// Scratch of the largest launch (the launches follow one another on the stream).
+size_t scratch_bytes(const int32_t* ctx, const int32_t* indptr, int B, int H) {
+  const int pairs = sm_pairs();
+  int64_t parts = 0;
+  for (int b0 = 0; b0 < B; b0 += kBatch)
+    parts = std::max(parts, plan_batch(ctx + b0, indptr + b0, std::min(kBatch, B - b0), H, pairs).parts);
+  return opart_bytes(parts) + lsepart_bytes(parts);
+}
+
+// cuTensorMapEncodeTiled, looked up through the runtime (a host-only function of the driver).
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+irm_status encode_map(CUtensorMap* m, const void* kv, int64_t rows, uint32_t cols, CUtensorMapSwizzle swizzle) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return fail(IRM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {(cuuint64_t)kDRow, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)kDRow * 2};
+  const cuuint32_t box[2] = {cols, (cuuint32_t)kPage}, step[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(kv), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? IRM_OK : fail(IRM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+// The kernel's dynamic shared memory limit belongs to the device: raised once on each.
+cudaError_t raise_smem_limit() {
+  static std::mutex mu;
+  static bool done[128];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev >= 0 && dev < 128 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess && dev >= 0 && dev < 128) done[dev] = true;
+  return e;
+}
+
 }  // namespace
 }  // namespace irm
 
@@ -129,7 +766,7 @@ irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32
   int64_t rows = 0;
   const irm_status st = check_lengths(ctx_host, q_indptr_host, B, H, &nodes, &rows);
   if (st != IRM_OK) return st;
-  *bytes = IRM_WORKSPACE_HEADER;
+  *bytes = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H);
   return IRM_OK;
 }
 
@@ -156,33 +793,63 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     return fail(IRM_ERR_INVALID_ARG, "q_lat, q_rope, paged_kv and out must be 16-byte aligned");
   if (!aligned(page_table, 4) || !aligned(tree_mask, 4) || !aligned(lse, 4))
     return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < IRM_WORKSPACE_HEADER)
-    return fail(IRM_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %d bytes", IRM_WORKSPACE_HEADER);
+  const int pairs = sm_pairs();
+  const size_t need = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(IRM_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %zu bytes (got %zu)", need, workspace_bytes);
   if (q_indptr_host[B] == 0) return IRM_OK;
   TreeArgs a{};
+  if ((st = encode_map(&a.map_lat, paged_kv, n_pages * kPage, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != IRM_OK) return st;
+  if ((st = encode_map(&a.map_rope, paged_kv, n_pages * kPage, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != IRM_OK) return st;
+  cudaError_t e = raise_smem_limit();
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention set-up");
   a.q_lat = static_cast<const __nv_bfloat16*>(q_lat);
   a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
-  a.kv = static_cast<const __nv_bfloat16*>(paged_kv);
   a.page_table = page_table;
   a.mask = tree_mask;
   a.n_pages = n_pages;
   a.H = H;
   a.max_pages = max_pages;
   a.mask_words = mask_words;
-  a.scale = softmax_scale;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.status = static_cast<int*>(workspace);
   for (int b0 = 0; b0 < B; b0 += kBatch) {
     a.b0 = b0;
-    a.B = B - b0 < kBatch ? B - b0 : kBatch;
+    a.B = std::min(kBatch, B - b0);
     std::memcpy(a.ctx, ctx_host + b0, (size_t)a.B * sizeof(int32_t));
     std::memcpy(a.indptr, q_indptr_host + b0, (size_t)(a.B + 1) * sizeof(int32_t));
-    const int64_t blocks = (int64_t)(a.indptr[a.B] - a.indptr[0]) * H;
-    if (blocks == 0) continue;
-    tree_attn_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    const Plan p = plan_batch(a.ctx, a.indptr, a.B, H, pairs);
+    const int units = p.n_long + p.n_rest;
+    if (units == 0) continue;
+    a.piece = p.piece;
+    a.n_long = p.n_long;
+    int nl = 0, nr = 0;
+    int64_t np = 0;
+    for (int b = 0; b < a.B; ++b) {
+      const int n = a.indptr[b + 1] - a.indptr[b], tiles = page_count(a.ctx[b], n), mt = row_tiles(n, H);
+      a.long_base[b] = nl;
+      a.rest_base[b] = nr;
+      a.part_base[b] = (int32_t)np;
+      nl += mt * (tiles / p.piece);
+      nr += tiles % p.piece ? mt : 0;
+      const int pieces = (tiles + p.piece - 1) / p.piece;
+      if (pieces > 1) np += (int64_t)mt * pieces;
+    }
+    a.long_base[a.B] = nl;
+    a.rest_base[a.B] = nr;
+    a.part_base[a.B] = (int32_t)np;
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + IRM_WORKSPACE_HEADER;
+    a.opart = reinterpret_cast<float*>(ws);
+    a.lsepart = reinterpret_cast<float*>(ws + opart_bytes(p.parts));
+    tree_attn_kernel<<<2 * units, kThreads, kSmem, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    if (p.parts) {
+      const int64_t merge = (int64_t)(a.indptr[a.B] - a.indptr[0]) * H;
+      tree_merge_kernel<<<(unsigned)merge, kMergeThreads, 0, stream>>>(a);
+      if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tree attention merge launch");
+    }
   }
   return IRM_OK;
 }
