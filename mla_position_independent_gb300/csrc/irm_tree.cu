@@ -63,13 +63,15 @@ constexpr uint32_t kStage = 4 * kSlab + 64 * 64;      // + 64 rows x 32 k_r colu
 constexpr uint32_t kXBytes = kHalf * kPage * 4;       // received scores of one tile
 constexpr uint32_t kPBytes = kBM * 128;               // P of one tile
 constexpr uint32_t kOffBars = 0;
-constexpr uint32_t kOffTmem = 256;
-constexpr uint32_t kOffAbort = 260;
+constexpr uint32_t kOffTmem = 384;
+constexpr uint32_t kOffAbort = 388;
 constexpr uint32_t kOffMax = 512;                     // float [64]: running maximum of the own rows
-constexpr uint32_t kOffCorr = kOffMax + 64 * 4;       // float [2][64]: the peer rows' factors
-constexpr uint32_t kOffSum = kOffCorr + 2 * 64 * 4;   // float2 [2][64]: (maximum, sum) of each set
+constexpr uint32_t kOffCorr = kOffMax + 64 * 4;       // float [4 tiles][64]: the peer rows' factors
+constexpr uint32_t kOffFlag = 400;                    // int [2 sets][2 warps]: some factor is not 1
+constexpr uint32_t kOffSum = kOffCorr + 4 * 64 * 4;   // float2 [2][64]: (maximum, sum) of each set
 constexpr uint32_t kOffInv = kOffSum + 2 * 64 * 8;    // float [128]: 1 / l of every row
-constexpr uint32_t kOffQr = 3072;                     // 128 rows x 64 B (swizzled)
+constexpr uint32_t kPrBytes = kPBytes / 4 + 128 + 4;  // what a warp sends of P: 32 rows, factors, flag
+constexpr uint32_t kOffQr = 4096;                     // 128 rows x 64 B (swizzled)
 constexpr uint32_t kOffX = kOffQr + 128 * 64;         // [2] 16-byte words [16][64 rows]
 constexpr uint32_t kOffP = kOffX + 2 * kXBytes;
 constexpr uint32_t kOffKv = kOffP + 2 * kPBytes;
@@ -85,10 +87,11 @@ enum : int {
   BAR_S_FREE = BAR_S_FULL + 2,       // [2] the set's live warps read the score buffer
   BAR_X_FULL = BAR_S_FREE + 2,       // [2] the peer's partial scores arrived (1 + tx)
   BAR_X_FREE = BAR_X_FULL + 2,       // [2] the peer's warps have read what was sent
-  BAR_PR_FULL = BAR_X_FREE + 2,      // [2] the peer's rows of P and factors arrived (1 + tx)
+  BAR_PR_FULL = BAR_X_FREE + 2,      // [2] the peer's rows of P and factors arrived (its live warps + tx)
   BAR_P_FREE = BAR_PR_FULL + 2,      // [2] P V of the buffer done in both CTAs (2)
-  BAR_GO = BAR_P_FREE + 2,           // [2] P complete and O rescaled: the set's live warps
-  BAR_PV = BAR_GO + 2,               // P V of a tile done in this CTA
+  BAR_GO = BAR_P_FREE + 2,           // [2] the own rows' P written and O rescaled: live warps
+  BAR_RESC = BAR_GO + 2,             // [2] O rescaled for the peer's rows: live warps
+  BAR_PV = BAR_RESC + 2,               // P V of a tile done in this CTA
   BAR_MAX = BAR_PV + 1,              // [2] running maximum of 32 own rows published
   BAR_Q = BAR_MAX + 2,               // Q stored (8 warps)
   BAR_DRAIN = BAR_Q + 1,             // [2] all UMMAs of an issuer done
@@ -235,14 +238,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(BAR_S_FREE + s), live_own + live_peer);
       mbar_init(bar(BAR_X_FULL + s), 1);
       mbar_init(bar(BAR_X_FREE + s), max(1, live_peer));
-      mbar_init(bar(BAR_PR_FULL + s), 1);
+      mbar_init(bar(BAR_PR_FULL + s), max(1, live_peer));
       mbar_init(bar(BAR_P_FREE + s), 2);
-      mbar_init(bar(BAR_GO + s), live_own + live_peer);
+      mbar_init(bar(BAR_GO + s), max(1, live_own));
+      mbar_init(bar(BAR_RESC + s), max(1, live_peer));
       mbar_init(bar(BAR_MAX + s), 1);
       mbar_init(bar(BAR_DRAIN + s), 1);
       // the first two tiles' bytes (a barrier that nothing is sent to is not waited for either)
       if (live_own) mbar_arrive_expect_tx(bar(BAR_X_FULL + s), (uint32_t)live_own * (kXBytes / 2));
-      if (live_peer) mbar_arrive_expect_tx(bar(BAR_PR_FULL + s), (uint32_t)live_peer * (kPBytes / 4 + 128));
+      for (int k = 0; k < live_peer; ++k) mbar_arrive_expect_tx(bar(BAR_PR_FULL + s), kPrBytes);
     }
     mbar_init(bar(BAR_PV), 1);
     mbar_init(bar(BAR_Q), kScoreWarps);
@@ -307,15 +311,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t remXfree = mapa_shared(bar(BAR_X_FREE + set), peer);
     const uint32_t remP = mapa_shared(sb + kOffP + buf * kPBytes, peer);
     const uint32_t remPfull = mapa_shared(bar(BAR_PR_FULL + set), peer);
-    const uint32_t remCorr = mapa_shared(sb + kOffCorr + buf * 256u + 4u * (uint32_t)mh, peer);
+    const uint32_t remCorr = mapa_shared(sb + kOffCorr + 4u * (uint32_t)mh, peer);
+    const uint32_t remFlag = mapa_shared(sb + kOffFlag + 8u * buf + 4u * (uint32_t)(quad & 1), peer);
     const uint4* X = reinterpret_cast<const uint4*>(smem + kOffX + buf * kXBytes);
     float* max_sh = reinterpret_cast<float*>(smem + kOffMax);
-    const float* corr_sh = reinterpret_cast<const float*>(smem + kOffCorr + buf * 256u);
+    const float* corr_sh = reinterpret_cast<const float*>(smem + kOffCorr);
     const uint32_t* mask = a.mask + (int64_t)(first_node + (row0 + (valid ? m : 0)) / a.H) * a.mask_words;
     const bool first_quad = (quad & 1) == 0;  // arms the byte counts
     float m_l = -INFINITY, l = 0.f;           // this set's sum, relative to m_l
 
-    for (int j = set; live && j < ntiles; j += 2) {  // warps without valid rows have no part in it
+    // The factors of the peer's rows at tile t, after its P has arrived.  A sender looks at them one
+    // turn late, after it has shipped the scores of tile t + 2, so that the peer never waits for it;
+    // P V waits for this only where a factor is not 1.
+    auto take_factors = [&](int t) -> bool {
+      if (!warp_wait_cluster(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
+      if (lane == 0 && t + 2 < ntiles) mbar_arrive_expect_tx(bar(BAR_PR_FULL + set), kPrBytes);
+      const float corr = corr_sh[(t & 3) * kHalf + mh];
+      if (t > 0 && __any_sync(kFull, corr != 1.f)) {
+        if (!warp_wait(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
+        tc_fence_after();
+        rescale_o(tO, corr);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_RESC + set));
+      return true;
+    };
+
+    int j = set;
+    for (; live && j < ntiles; j += 2) {  // warps without valid rows have no part in it
       const uint32_t ph = (uint32_t)(j >> 1) & 1u;
       uint32_t s[64];
       if (!(ok = warp_wait(bar(BAR_S_FULL + set), ph, abort_flag))) break;
@@ -326,8 +350,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
-      float corr = 1.f;
       if (own) {
+        float corr = 1.f;
         // ================= softmax of a row =================
         if (!(ok = warp_wait_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
         float v[64];
@@ -387,7 +411,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           st_async_v4_b32(remP + off, w, remPfull);
           st_shared_v4(sb + kOffP + buf * kPBytes + off, w);
         }
-        st_async_b32(remCorr, __float_as_uint(corr), remPfull);
+        const bool moved = __any_sync(kFull, corr != 1.f);
+        st_async_b32(remCorr + (uint32_t)(j & 3) * (kHalf * 4u), __float_as_uint(corr), remPfull);
+        if (lane == 0) st_async_b32(remFlag, moved ? 1u : 0u, remPfull);
+        if (j > 0 && moved) {
+          if (!(ok = warp_wait(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+          tc_fence_after();
+          rescale_o(tO, corr);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
         if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
@@ -395,20 +429,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 16; ++i)
           st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
                           remXfull);
-        if (!(ok = warp_wait_cluster(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
-        if (lane == 0 && first_quad && j + 2 < ntiles)
-          mbar_arrive_expect_tx(bar(BAR_PR_FULL + set), (uint32_t)live_peer * (kPBytes / 4 + 128));
-        corr = corr_sh[mh];
+        if (j >= 2 && !(ok = take_factors(j - 2))) break;
       }
-      if (j > 0 && __any_sync(kFull, corr != 1.f)) {
-        if (!(ok = warp_wait(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
-        tc_fence_after();
-        rescale_o(tO, corr);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_GO + set));
     }
+    if (ok && live && !own && j > set) ok = take_factors(j - 2);
     if (own) reinterpret_cast<float2*>(smem + kOffSum)[set * kHalf + mh] = make_float2(m_l, l);
   } else if (warp == kTmaWarp) {
     // ================= pages in =================
@@ -478,7 +502,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
-        if (!(ok = mbar_wait(bar(BAR_GO + set), (uint32_t)(j >> 1) & 1u, abort_flag))) break;
+        const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+        if (live_own && !(ok = mbar_wait(bar(BAR_GO + set), ph, abort_flag))) break;
+        if (live_peer) {
+          if (!(ok = mbar_wait_cluster(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
+          const volatile int* flag = reinterpret_cast<const volatile int*>(smem + kOffFlag) + 2 * set;
+          const bool moved = flag[0] != 0 || (live_peer > 1 && flag[1] != 0);
+          if (j > 0 && moved && !(ok = mbar_wait(bar(BAR_RESC + set), ph, abort_flag))) break;
+        }
         tc_fence_after();
         fence_proxy_async_smem();  // P, written by both CTAs' threads
         const uint64_t ad = sdesc_sw128(sb + kOffP + (uint32_t)set * kPBytes, 16, 1024);
