@@ -22,6 +22,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
+// The same box, into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
+}
+
 // Shared-memory matrix descriptor, 64-byte swizzle (layout type 4): rows 64 B apart, 8-row
 // groups `sbo` bytes apart.
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
@@ -44,6 +49,29 @@ __device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, 
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+// Bounded waits as mbar_wait / mbar_wait_cluster, for roles whose waits are short and many: the
+// clock is first read after a thousand polls (reading it costs more than the usual wait), so the
+// common wait is the poll alone.  False once kWaitLimitNs has passed or *abort_flag != 0.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 0) {
+      if (abort_flag != nullptr && *abort_flag) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_poll<false>(bar, parity, abort_flag));
+}
+__device__ __forceinline__ bool warp_poll_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_poll<true>(bar, parity, abort_flag));
 }
 
 // Arrive (once) on the mbarrier at this offset in every CTA of `mask` when all UMMAs issued so

@@ -75,7 +75,9 @@ constexpr uint32_t kOffQr = 4096;                     // 128 rows x 64 B (swizzl
 constexpr uint32_t kOffX = kOffQr + 128 * 64;         // [2] 16-byte words [16][64 rows]
 constexpr uint32_t kOffP = kOffX + 2 * kXBytes;
 constexpr uint32_t kOffKv = kOffP + 2 * kPBytes;
+constexpr uint32_t kOffQl = kOffKv + 2 * kStage;      // 4 slabs of Q's cKV columns at the start, in stages 2 and 3
 constexpr uint32_t kSmem = kOffKv + kStages * kStage + 1024;  // room to align the base
+static_assert(4 * kBM * 128 <= 2 * kStage && kStages == 4, "Q's place");
 static_assert(kOffInv + 128 * 4 <= kOffQr && kOffQr % 1024 == 0 && kOffX % 1024 == 0 && kOffKv % 1024 == 0, "layout");
 static_assert(kSmem <= 232448, "shared memory");
 
@@ -93,8 +95,10 @@ enum : int {
   BAR_RESC = BAR_GO + 2,             // [2] O rescaled for the peer's rows: live warps
   BAR_PV = BAR_RESC + 2,               // P V of a tile done in this CTA
   BAR_MAX = BAR_PV + 1,              // [2] running maximum of 32 own rows published
-  BAR_Q = BAR_MAX + 2,               // Q stored (8 warps)
-  BAR_DRAIN = BAR_Q + 1,             // [2] all UMMAs of an issuer done
+  BAR_QIN = BAR_MAX + 2,             // Q's TMA bytes (1 + tx)
+  BAR_Q = BAR_QIN + 1,               // Q's cKV columns copied to TMEM (8 warps)
+  BAR_INV = BAR_Q + 1,               // the peer rows' 1 / l arrived (1 + tx)
+  BAR_DRAIN = BAR_INV + 1,           // [2] all UMMAs of an issuer done
   NUM_BARS = BAR_DRAIN + 2,
 };
 static_assert(NUM_BARS * 8 <= kOffTmem, "barrier area");
@@ -104,9 +108,8 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kPage, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, 256, 0, 1);
 
 struct TreeArgs {
-  CUtensorMap map_lat, map_rope;  // [rows, 576]: boxes of 64 x 64 and 64 rows x 32 columns
-  const __nv_bfloat16* q_lat;
-  const __nv_bfloat16* q_rope;
+  CUtensorMap map_lat, map_rope;  // pages [rows, 576]: boxes of 64 x 64, and of 64 rows x 32 columns
+  CUtensorMap map_ql, map_qr;     // queries [T H, 512] and [T H, 64]: boxes of 32 rows x 64, and x 32 columns
   const int32_t* page_table;
   const uint32_t* mask;
   int64_t n_pages;
@@ -249,9 +252,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int k = 0; k < live_peer; ++k) mbar_arrive_expect_tx(bar(BAR_PR_FULL + s), kPrBytes);
     }
     mbar_init(bar(BAR_PV), 1);
+    mbar_init(bar(BAR_QIN), 1);
     mbar_init(bar(BAR_Q), kScoreWarps);
+    mbar_init(bar(BAR_INV), 1);
+    if (live_peer) mbar_arrive_expect_tx(bar(BAR_INV), (uint32_t)live_peer * 128u);
     *abort_flag = 0;
     fence_mbar_init_cluster();
+  }
+  // what the first copies need, on its way during the set-up
+  const int32_t* ptab = a.page_table + (int64_t)(a.b0 + b) * a.max_pages + kb;
+  int page0 = 0;
+  if (warp == kTmaWarp) {
+    if (lane < ntiles) page0 = ptab[lane];
+    if (lane == 0) {
+      tma_prefetch_map(&a.map_ql);
+      tma_prefetch_map(&a.map_qr);
+      tma_prefetch_map(&a.map_lat);
+      tma_prefetch_map(&a.map_rope);
+    }
   }
   if (warp == kSWarp) {
     tmem_alloc(sb + kOffTmem, kTmemCols);
@@ -274,29 +292,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + kTmemS + 64u * (uint32_t)set + lanes;
     const uint32_t tO = tmem + kTmemO + lanes;
     const bool valid = m < rows_valid;
-    // ---- Q: set h stores cKV slabs 2h, 2h + 1 of this CTA's columns, set 0 also q_rope ------
-    if (live) {
-      const int64_t row = grow0 + (valid ? m : 0);
-      const uint4* q = reinterpret_cast<const uint4*>(a.q_lat + row * kDLat + 256 * rank + 128 * set);
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    // ---- Q, this CTA's cKV columns: from shared memory (where TMA put it) to TMEM; set h takes
+    //      slabs 2h, 2h + 1
+    ok = warp_poll(bar(BAR_QIN), 0, abort_flag);
+    if (live && ok) {
 #pragma unroll
-      for (int slab = 0; slab < 2; ++slab) {
+      for (int slab = 2 * set; slab < 2 * set + 2; ++slab) {
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 v = valid ? __ldg(q + slab * 8 + i) : zero;
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffQl + slab * (kBM * 128) + sw128_offset((uint32_t)m, (uint32_t)i));
           r[4 * i] = v.x;
           r[4 * i + 1] = v.y;
           r[4 * i + 2] = v.z;
           r[4 * i + 3] = v.w;
         }
-        tmem_st32(tmem + kTmemQ + 32u * (uint32_t)(2 * set + slab) + lanes, r);
-      }
-      if (set == 0) {
-        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + row * kDRope + 32 * rank);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          st_shared_v4(sb + kOffQr + sw64_offset((uint32_t)m, (uint32_t)i), valid ? __ldg(qr + i) : zero);
+        tmem_st32(tmem + kTmemQ + 32u * (uint32_t)slab + lanes, r);
       }
       tmem_st_wait();
     }
@@ -324,11 +335,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // turn late, after it has shipped the scores of tile t + 2, so that the peer never waits for it;
     // P V waits for this only where a factor is not 1.
     auto take_factors = [&](int t) -> bool {
-      if (!warp_wait_cluster(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
+      if (!warp_poll_cluster(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
       if (lane == 0 && t + 2 < ntiles) mbar_arrive_expect_tx(bar(BAR_PR_FULL + set), kPrBytes);
       const float corr = corr_sh[(t & 3) * kHalf + mh];
       if (t > 0 && __any_sync(kFull, corr != 1.f)) {
-        if (!warp_wait(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
+        if (!warp_poll(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
         tc_fence_after();
         rescale_o(tO, corr);
       }
@@ -339,10 +350,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
 
     int j = set;
-    for (; live && j < ntiles; j += 2) {  // warps without valid rows have no part in it
+    for (; live && ok && j < ntiles; j += 2) {  // warps without valid rows have no part in it
       const uint32_t ph = (uint32_t)(j >> 1) & 1u;
       uint32_t s[64];
-      if (!(ok = warp_wait(bar(BAR_S_FULL + set), ph, abort_flag))) break;
+      if (!(ok = warp_poll(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
       tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
@@ -353,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (own) {
         float corr = 1.f;
         // ================= softmax of a row =================
-        if (!(ok = warp_wait_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
+        if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
         float v[64];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -380,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 7; ++i) t[i] = fmax3(t[3 * i], t[3 * i + 1], t[3 * i + 2]);
         const float top = fmaxf(fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), t[6]), v[63]) * a.scale_log2;
-        if (j > 0 && !(ok = warp_wait(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+        if (j > 0 && !(ok = warp_poll(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
         const float before = j > 0 ? max_sh[mh] : -INFINITY;
         const bool up = top > before + 8.f;
         const float now = up ? top : before;
@@ -403,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const float2 part = f2_unpack(f2_add(sum[0], sum[1]));
         l += part.x + part.y;
-        if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = warp_poll_cluster(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint4 w = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
@@ -415,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         st_async_b32(remCorr + (uint32_t)(j & 3) * (kHalf * 4u), __float_as_uint(corr), remPfull);
         if (lane == 0) st_async_b32(remFlag, moved ? 1u : 0u, remPfull);
         if (j > 0 && moved) {
-          if (!(ok = warp_wait(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+          if (!(ok = warp_poll(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
           tc_fence_after();
           rescale_o(tO, corr);
         }
@@ -424,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
-        if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
@@ -435,16 +446,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (ok && live && !own && j > set) ok = take_factors(j - 2);
     if (own) reinterpret_cast<float2*>(smem + kOffSum)[set * kHalf + mh] = make_float2(m_l, l);
   } else if (warp == kTmaWarp) {
-    // ================= pages in =================
-    const int32_t* ptab = a.page_table + (int64_t)(a.b0 + b) * a.max_pages + kb;
+    // ================= Q and pages in =================
     if (lane == 0) {
-      tma_prefetch_map(&a.map_lat);
-      tma_prefetch_map(&a.map_rope);
+      const int quads = (rows_valid + 31) / 32;
+      mbar_arrive_expect_tx(bar(BAR_QIN), (uint32_t)quads * 32u * (512u + 64u));
+      for (int q = 0; q < quads; ++q) {  // rows behind the request's last (another's, or zeros) are never looked at
+        const int y = (int)grow0 + 32 * q;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tma_load_2d(sb + kOffQl + c * (kBM * 128) + q * 4096, &a.map_ql, 256 * rank + 64 * c, y, bar(BAR_QIN));
+        tma_load_2d(sb + kOffQr + q * 2048, &a.map_qr, 32 * rank, y, bar(BAR_QIN));
+      }
     }
     int page = 0, sent = 0;
     for (int j = 0; j < ntiles; ++j) {
       if ((j & 31) == 0) {
-        page = j + lane < ntiles ? ptab[j + lane] : 0;
+        page = j == 0 ? page0 : j + lane < ntiles ? ptab[j + lane] : 0;
         if (page < 0 || page >= a.n_pages) {
           set_status(a.status, kDevErrBounds);
           page = (int)a.n_pages;  // behind the tensor: zeros
@@ -452,7 +469,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const int y = __shfl_sync(kFull, page, j & 31) * kPage;
       const int s = j % kStages;
-      if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
+      // stages 2 and 3 hold Q until it is in TMEM
+      if (j == 2 && !(ok = warp_poll(bar(BAR_Q), 0, abort_flag))) break;
+      if (j >= kStages && !(ok = warp_poll(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
         mbar_arrive_expect_tx(bar(BAR_LANDED + s), kStage);
@@ -463,23 +482,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sent = j + 1;
     }
     // the copies in flight land before the CTA ends, whatever became of the others
+    ok = warp_poll(bar(BAR_QIN), 0, nullptr) && ok;
     for (int j = max(0, sent - kStages); j < sent; ++j)
-      ok = warp_wait(bar(BAR_LANDED + j % kStages), (uint32_t)(j / kStages) & 1u, nullptr) && ok;
+      ok = warp_poll(bar(BAR_LANDED + j % kStages), (uint32_t)(j / kStages) & 1u, nullptr) && ok;
     __syncwarp();
     cluster_wait();
   } else if (warp == kSWarp) {
     // ================= Q K^T (one thread) =================
     if (lane == 0) {
-      ok = mbar_wait(bar(BAR_Q), 0, abort_flag);
+      ok = mbar_poll<false>(bar(BAR_QIN), 0, abort_flag) && mbar_poll<false>(bar(BAR_Q), 0, abort_flag);
       tc_fence_after();
       const uint64_t aq = sdesc_sw64(sb + kOffQr, 512);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
-        if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
-        if (j >= tail && !(ok = mbar_wait(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
-        if (j >= 2 && !(ok = mbar_wait(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+        if (!(ok = mbar_poll<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+        if (j >= tail && !(ok = mbar_poll<false>(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = mbar_poll<false>(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
-        fence_proxy_async_smem();  // Q's and the cleared rows' plain stores
+        fence_proxy_async_smem();  // the cleared rows' plain stores
         const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
         const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(st + 4 * kSlab, 512);
         const uint32_t d = tmem + kTmemS + 64u * (uint32_t)set;
@@ -493,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         umma_commit(bar(BAR_S_FULL + set));
       }
       umma_commit(bar(BAR_DRAIN));
-      ok = mbar_wait(bar(BAR_DRAIN), 0, nullptr) && ok;
+      ok = mbar_poll<false>(bar(BAR_DRAIN), 0, nullptr) && ok;
     }
     __syncwarp();
     cluster_wait();
@@ -503,12 +523,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
-        if (live_own && !(ok = mbar_wait(bar(BAR_GO + set), ph, abort_flag))) break;
+        if (live_own && !(ok = mbar_poll<false>(bar(BAR_GO + set), ph, abort_flag))) break;
         if (live_peer) {
-          if (!(ok = mbar_wait_cluster(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
+          if (!(ok = mbar_poll<true>(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
           const volatile int* flag = reinterpret_cast<const volatile int*>(smem + kOffFlag) + 2 * set;
           const bool moved = flag[0] != 0 || (live_peer > 1 && flag[1] != 0);
-          if (j > 0 && moved && !(ok = mbar_wait(bar(BAR_RESC + set), ph, abort_flag))) break;
+          if (j > 0 && moved && !(ok = mbar_poll<false>(bar(BAR_RESC + set), ph, abort_flag))) break;
         }
         tc_fence_after();
         fence_proxy_async_smem();  // P, written by both CTAs' threads
@@ -522,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         umma_commit_multicast(bar(BAR_P_FREE + set), (uint16_t)3);
       }
       umma_commit(bar(BAR_DRAIN + 1));
-      ok = mbar_wait(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
+      ok = mbar_poll<false>(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
     }
     __syncwarp();
     cluster_wait();
@@ -539,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         lo = __reduce_or_sync(kFull, (uint32_t)see);
         hi = __reduce_or_sync(kFull, (uint32_t)(see >> 32));
       }
-      if (!(ok = warp_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+      if (!(ok = warp_poll(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
       if (j >= tail) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -571,6 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   float* inv_sh = reinterpret_cast<float*>(smem + kOffInv);
   if (tid < kHalf) {
     const int m = kHalf * rank + tid;
+    // both sets' sums are relative to the last maximum they saw; O to the last one of all, the larger
     const float2 x = reinterpret_cast<const float2*>(smem + kOffSum)[tid];
     const float2 y = reinterpret_cast<const float2*>(smem + kOffSum)[kHalf + tid];
     const float mx = fmaxf(x.x, y.x);
@@ -578,46 +599,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (mx != -INFINITY) l = x.y * fast_exp2(x.x - mx) + y.y * fast_exp2(y.x - mx);
     const bool some = m < rows_valid && *abort_flag == 0 && l > 0.f;
     const float inv = some ? 1.f / l : 0.f, lse2 = some ? mx + __log2f(l) : -INFINITY;
-    // both sets' sums are relative to the last maximum they saw; O is relative to the last one
-    // of all, which is the larger
     inv_sh[m] = inv;
-    st_cluster_f32(mapa_shared(sb + kOffInv + 4u * (uint32_t)m, peer), inv);
+    if (tid < 32 * live_own)
+      st_async_b32(mapa_shared(sb + kOffInv + 4u * (uint32_t)m, peer), __float_as_uint(inv), mapa_shared(bar(BAR_INV), peer));
     if (m < rows_valid) {
       if (split) a.lsepart[part * kBM + m] = lse2;
       else if (a.lse != nullptr) a.lse[grow0 + m] = lse2 * kLn2;
     }
   }
-  cluster_arrive();
-  cluster_wait();
-  // ---- O / l: 32 columns of a quadrant at a time, three warps to a quadrant ------------------
-  {
+  __syncthreads();
+  cluster_arrive();  // waited for at the end: until then the peer may still send here
+  // ---- O / l: a warp takes 64 columns of its 32 rows at a time, through shared memory, so that
+  //      its stores are whole 128-byte lines --------------------------------------------------
+  if (warp < kScoreWarps) {
     const int quad = warp & 3, m = quad * 32 + lane;
     if (quad * 32 < rows_valid) {
+      if ((quad >> 1) != rank && !warp_poll_cluster(bar(BAR_INV), 0, abort_flag)) set_status(a.status, kDevErrTimeout);
       const float inv = inv_sh[m];
-      const bool write = m < rows_valid;
-      for (int c = warp >> 2; c < 8; c += 3) {
-        uint32_t r[32];
-        tmem_ld32(tmem + kTmemO + ((uint32_t)(quad * 32) << 16) + 32u * c, r);
+      uint8_t* stage = smem + kOffKv + warp * 8192;
+      for (int c = 128 * (warp >> 2); c < 128 * (warp >> 2) + 128; c += 64) {
+        uint32_t r[64];
+        const uint32_t tO = tmem + kTmemO + ((uint32_t)(quad * 32) << 16) + (uint32_t)c;
+        tmem_ld32(tO, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+        tmem_ld32(tO + 32u, reinterpret_cast<uint32_t(&)[32]>(r[32]));
         tmem_ld_wait();
-        float v[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = inv > 0.f ? __uint_as_float(r[i]) * inv : 0.f;
-        if (!write) continue;
-        const int col = 256 * rank + 32 * c;
-        if (split) {
-          float4* o = reinterpret_cast<float4*>(a.opart + (part * kBM + m) * kDLat + col);
+        for (int i = 0; i < 64; ++i) r[i] = inv > 0.f ? __float_as_uint(__uint_as_float(r[i]) * inv) : 0u;
+        const int col = 256 * rank + c;
+        __syncwarp();
+        if (split) {  // rows of 256 bytes, 16-byte pieces XOR-ed with the row
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint4*>(stage + lane * 256 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int row = 2 * i + (lane >> 4), q = lane & 15;
+            if (quad * 32 + row < rows_valid)
+              *reinterpret_cast<uint4*>(a.opart + (part * kBM + quad * 32 + row) * kDLat + col + 4 * q) =
+                  *reinterpret_cast<const uint4*>(stage + row * 256 + ((q ^ (row & 7)) << 4));
+          }
         } else {
-          uint4* o = reinterpret_cast<uint4*>(a.out + (grow0 + m) * kDLat + col);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack_bf16(__uint_as_float(r[8 * i + 2 * k]), __uint_as_float(r[8 * i + 2 * k + 1]));
+            *reinterpret_cast<uint4*>(stage + sw128_offset((uint32_t)lane, (uint32_t)i)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3), q = lane & 7;
+            if (quad * 32 + row < rows_valid)
+              *reinterpret_cast<uint4*>(a.out + (grow0 + quad * 32 + row) * kDLat + col + 8 * q) =
+                  *reinterpret_cast<const uint4*>(stage + sw128_offset((uint32_t)row, (uint32_t)q));
+          }
         }
       }
     }
   }
+  __syncwarp();
+  cluster_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kSWarp) {
@@ -759,14 +803,15 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-irm_status encode_map(CUtensorMap* m, const void* kv, int64_t rows, uint32_t cols, CUtensorMapSwizzle swizzle) {
+// Map of `rows` rows of `width` bf16: boxes of box_rows x box_cols, as wide as the swizzle.
+irm_status encode_map(CUtensorMap* m, const void* base, int64_t rows, int width, uint32_t box_rows, uint32_t box_cols) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return fail(IRM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t dims[2] = {(cuuint64_t)kDRow, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)kDRow * 2};
-  const cuuint32_t box[2] = {cols, (cuuint32_t)kPage}, step[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(kv), dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
+  const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? IRM_OK : fail(IRM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
@@ -819,6 +864,7 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     return fail(IRM_ERR_INVALID_ARG, "mask_words=%d does not cover %d nodes", mask_words, nodes);
   if (!std::isfinite(softmax_scale) || softmax_scale <= 0.f)
     return fail(IRM_ERR_INVALID_ARG, "softmax_scale must be finite and positive");
+  if ((int64_t)q_indptr_host[B] * H >= INT32_MAX) return fail(IRM_ERR_UNSUPPORTED, "too many query rows");
   if (!q_lat || !q_rope || !paged_kv || !page_table || !tree_mask || !out) return fail(IRM_ERR_INVALID_ARG, "null device pointer");
   if (!aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(paged_kv, 16) || !aligned(out, 16))
     return fail(IRM_ERR_INVALID_ARG, "q_lat, q_rope, paged_kv and out must be 16-byte aligned");
@@ -830,12 +876,13 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     return fail(IRM_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %zu bytes (got %zu)", need, workspace_bytes);
   if (q_indptr_host[B] == 0) return IRM_OK;
   TreeArgs a{};
-  if ((st = encode_map(&a.map_lat, paged_kv, n_pages * kPage, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != IRM_OK) return st;
-  if ((st = encode_map(&a.map_rope, paged_kv, n_pages * kPage, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != IRM_OK) return st;
+  const int64_t q_rows = (int64_t)q_indptr_host[B] * H;
+  if ((st = encode_map(&a.map_lat, paged_kv, n_pages * kPage, kDRow, kPage, 64)) != IRM_OK) return st;
+  if ((st = encode_map(&a.map_rope, paged_kv, n_pages * kPage, kDRow, kPage, 32)) != IRM_OK) return st;
+  if ((st = encode_map(&a.map_ql, q_lat, q_rows, kDLat, 32, 64)) != IRM_OK) return st;
+  if ((st = encode_map(&a.map_qr, q_rope, q_rows, kDRope, 32, 32)) != IRM_OK) return st;
   cudaError_t e = raise_smem_limit();
   if (e != cudaSuccess) return cuda_fail(e, "tree attention set-up");
-  a.q_lat = static_cast<const __nv_bfloat16*>(q_lat);
-  a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
   a.page_table = page_table;
   a.mask = tree_mask;
   a.n_pages = n_pages;
