@@ -376,33 +376,60 @@ def irm_cdc_chunk(tokens: torch.Tensor, offsets: np.ndarray, gear: torch.Tensor 
 
 
 def _host_i32(x, name):
+    if type(x) is np.ndarray and x.dtype == np.int32 and x.ndim == 1 and x.flags.c_contiguous:
+        return x
     a = np.asarray(x)
     if a.ndim != 1 or a.dtype.kind not in "iu":
         raise ValueError(f"{name} must be a 1-d integer array in host memory")
-    if a.itemsize > 4 and a.size and (a.max() > 2**31 - 1 or a.min() < -2**31):
+    if a.itemsize >= 4 and a.size and (a.max() > 2**31 - 1 or a.min() < -2**31):
         raise ValueError(f"{name} has values outside int32")
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
-def _need_shape(t, shape, name):
+def _size(t, dim, name):
+    """A size that a call takes from one of its tensors."""
+    if not isinstance(t, torch.Tensor) or t.dim() <= dim:
+        raise ValueError(f"{name} must be a tensor on the GPU with more than {dim} dimensions")
+    return t.shape[dim]
+
+
+def _take(t, dtype, shape, name, device):
+    """Address of a contiguous GPU tensor of this type, shape and device (a call takes several, so one
+    comparison each; what is wrong is only looked for when something is)."""
+    if (type(t) is torch.Tensor and t.get_device() == device.index and t.dtype is dtype and t.shape == shape
+            and t.is_cuda and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, dtype, name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    return t.data_ptr()
 
 
-def _one_device(*tensors):
-    """The tensors' device; a call's launches and its default stream belong to it."""
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return torch.cuda.device(dev)
-
-
-def _workspace(workspace, nbytes, device):
+def _take_workspace(workspace, nbytes, device):
+    """(workspace, its address, its bytes); a new one of nbytes() where the caller keeps none."""
     if workspace is None:
-        return new_workspace(nbytes, device)
-    _need(workspace, torch.uint8, "workspace", 1)
-    return workspace
+        workspace = new_workspace(nbytes(), device)
+    n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    return workspace, _take(workspace, torch.uint8, (n,), "workspace", device), n
+
+
+def _launch(fn, device, stream, *args):
+    """A library call on `device` (made current for it) and on `stream`, by default the device's current one."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
+        stream = stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
+    if st != 0:
+        _check(st)
 
 
 def tree_workspace_size(ctx: np.ndarray, q_indptr: np.ndarray, H: int) -> int:
@@ -411,7 +438,7 @@ def tree_workspace_size(ctx: np.ndarray, q_indptr: np.ndarray, H: int) -> int:
     if len(q_indptr) != len(ctx) + 1:
         raise ValueError("q_indptr must have one entry more than ctx")
     n = ctypes.c_size_t(0)
-    _check(lib().irm_mla_attn_tree_workspace_size(_ptr(ctx), _ptr(q_indptr), len(ctx), int(H), ctypes.byref(n)))
+    _check(lib().irm_mla_attn_tree_workspace_size(ctx.tobytes(), q_indptr.tobytes(), len(ctx), int(H), ctypes.byref(n)))
     return n.value
 
 
@@ -422,83 +449,79 @@ def irm_mla_attn_tree(q_lat, q_rope, ctx, q_indptr, paged_kv, page_table, tree_m
     576] bf16, page_table [B, max_pages] int32, tree_mask [T, words] int32 (bit k of a row: the node
     sees draft k).  Returns (out [T, H, 512] bf16, lse or None, workspace)."""
     ctx, q_indptr = _host_i32(ctx, "ctx"), _host_i32(q_indptr, "q_indptr")
-    if len(ctx) < 1 or len(q_indptr) != len(ctx) + 1:
+    B = len(ctx)
+    if B < 1 or len(q_indptr) != B + 1:
         raise ValueError("q_indptr must have one entry more than ctx")
-    _need(q_lat, torch.bfloat16, "q_lat", 3)
-    _need(q_rope, torch.bfloat16, "q_rope", 3)
-    _need(paged_kv, torch.bfloat16, "paged_kv", 3)
-    _need(page_table, torch.int32, "page_table", 2)
-    _need(tree_mask, torch.int32, "tree_mask", 2)
-    B, T, H = len(ctx), int(q_indptr[-1]), int(q_lat.shape[1])
-    _need_shape(q_lat, (T, H, 512), "q_lat")
-    _need_shape(q_rope, (T, H, 64), "q_rope")
-    _need_shape(paged_kv, (paged_kv.shape[0], 64, 576), "paged_kv")
-    _need_shape(page_table, (B, page_table.shape[1]), "page_table")
-    _need_shape(tree_mask, (T, tree_mask.shape[1]), "tree_mask")
+    if not isinstance(q_lat, torch.Tensor) or q_lat.dim() != 3:
+        _need(q_lat, torch.bfloat16, "q_lat", 3)
+    dev, T, H = q_lat.device, int(q_indptr[B]), q_lat.shape[1]
+    ql = _take(q_lat, torch.bfloat16, (T, H, 512), "q_lat", dev)
+    n_pages, max_pages, words = _size(paged_kv, 0, "paged_kv"), _size(page_table, 1, "page_table"), _size(tree_mask, 1, "tree_mask")
+    qr = _take(q_rope, torch.bfloat16, (T, H, 64), "q_rope", dev)
+    kv = _take(paged_kv, torch.bfloat16, (n_pages, 64, 576), "paged_kv", dev)
+    pt = _take(page_table, torch.int32, (B, max_pages), "page_table", dev)
+    tm = _take(tree_mask, torch.int32, (T, words), "tree_mask", dev)
     if out is None:
-        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q_lat.device)
-    _need(out, torch.bfloat16, "out")
-    _need_shape(out, (T, H, 512), "out")
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        _need_shape(lse, (T, H), "lse")
-    if workspace is None:
-        workspace = new_workspace(tree_workspace_size(ctx, q_indptr, H), q_lat.device)
-    _need(workspace, torch.uint8, "workspace", 1)
-    if T == 0:
-        return out, lse, workspace
-    with _one_device(q_lat, q_rope, paged_kv, page_table, tree_mask, out, lse, workspace):
-        _check(lib().irm_mla_attn_tree(
-            _ptr(q_lat), _ptr(q_rope), B, H, _ptr(ctx), _ptr(q_indptr), _ptr(paged_kv), int(paged_kv.shape[0]),
-            _ptr(page_table), int(page_table.shape[1]), _ptr(tree_mask), int(tree_mask.shape[1]),
-            float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
+    o = _take(out, torch.bfloat16, (T, H, 512), "out", dev)
+    ls = None if lse is None else _take(lse, torch.float32, (T, H), "lse", dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: tree_workspace_size(ctx, q_indptr, H), dev)
+    if T > 0:
+        _launch(lib().irm_mla_attn_tree, dev, stream, ql, qr, B, H, ctx.tobytes(), q_indptr.tobytes(), kv, n_pages, pt, max_pages,
+                tm, words, softmax_scale, o, ls, ws, ws_bytes)
     return out, lse, workspace
+
+
+def _take_probs(t, shape, name, device):
+    """Address and row stride of fp32 rows that may lie in a wider buffer."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-d torch.float32 tensor on the GPU")
+    if t.shape != shape or t.device != device:
+        _take(t, torch.float32, shape, name, device)
+    rows, vocab = shape
+    ld = t.stride(0) if rows > 1 else vocab
+    if ld < vocab or (vocab > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), ld
 
 
 def irm_tree_verify(target_probs, tokens, parents, uniforms, q_indptr, draft_probs=None, max_path=None, out=None,
                     workspace=None, stream=None):
     """Verification of drafted trees: target_probs (and draft_probs) [T, vocab] fp32, rows may be
     strided; tokens, parents int32 [T], uniforms fp32 [T]; q_indptr [B + 1] integers in host
-    memory.  Returns (n_accept [B], path [B, max_path], next_token [B], workspace), int32."""
+    memory.  Returns (n_accept [B], path [B, max_path], next_token [B], workspace), int32; max_path is
+    the largest tree unless given (or taken from out, a tuple of the three)."""
     q_indptr = _host_i32(q_indptr, "q_indptr")
-    if len(q_indptr) < 2:
+    B = len(q_indptr) - 1
+    if B < 1:
         raise ValueError("q_indptr must have at least two entries")
-    B, T = len(q_indptr) - 1, int(q_indptr[-1])
-    _need(tokens, torch.int32, "tokens", 1)
-    _need(parents, torch.int32, "parents", 1)
-    _need(uniforms, torch.float32, "uniforms", 1)
-    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
-        if t is None and name == "draft_probs":
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 or not t.is_cuda:
-            raise ValueError(f"{name} must be a 2-d torch.float32 tensor on the GPU")
-        if t.shape[1] < 1 or t.stride(1) != 1 and t.shape[1] > 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    V = int(target_probs.shape[1])
-    ld = int(target_probs.stride(0)) if T > 1 else V
-    _need_shape(target_probs, (T, V), "target_probs")
+    T = int(q_indptr[B])
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
+        raise ValueError("target_probs must be a 2-d torch.float32 tensor on the GPU")
+    dev, V = target_probs.device, target_probs.shape[1]
+    tp, ld = _take_probs(target_probs, (T, V), "target_probs", dev)
+    dp = None
     if draft_probs is not None:
-        _need_shape(draft_probs, (T, V), "draft_probs")
-        if T > 1 and draft_probs.stride(0) != ld:
+        dp, draft_ld = _take_probs(draft_probs, (T, V), "draft_probs", dev)
+        if draft_ld != ld:
             raise ValueError("draft_probs must have target_probs' row stride")
-    for t, name in ((tokens, "tokens"), (parents, "parents"), (uniforms, "uniforms")):
-        _need_shape(t, (T,), name)
-    if max_path is None:
-        max_path = max(1, int(np.diff(q_indptr).max())) if out is None else int(out[1].shape[1])
-    dev = tokens.device
+    tk = _take(tokens, torch.int32, (T,), "tokens", dev)
+    pr = _take(parents, torch.int32, (T,), "parents", dev)
+    un = _take(uniforms, torch.float32, (T,), "uniforms", dev)
     if out is None:
+        if max_path is None:
+            max_path = max(1, int((q_indptr[1:] - q_indptr[:-1]).max())) if B > 1 else max(1, T)
         out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty((B, max_path), dtype=torch.int32, device=dev),
                torch.empty(B, dtype=torch.int32, device=dev))
     n_accept, path, next_token = out
-    for t, shape, name in ((n_accept, (B,), "n_accept"), (path, (B, max_path), "path"), (next_token, (B,), "next_token")):
-        _need(t, torch.int32, name)
-        _need_shape(t, shape, name)
-    workspace = _workspace(workspace, WORKSPACE_HEADER, dev)
-    with _one_device(tokens, parents, uniforms, target_probs, draft_probs, n_accept, path, next_token, workspace):
-        _check(lib().irm_tree_verify(
-            _ptr(target_probs), _ptr(draft_probs), ld, V, _ptr(tokens), _ptr(parents), _ptr(uniforms), _ptr(q_indptr), B,
-            int(max_path), _ptr(n_accept), _ptr(path), _ptr(next_token), _ptr(workspace), workspace.numel(),
-            _stream(stream)))
+    if max_path is None:
+        max_path = path.shape[1]
+    na = _take(n_accept, torch.int32, (B,), "n_accept", dev)
+    pa = _take(path, torch.int32, (B, max_path), "path", dev)
+    nt = _take(next_token, torch.int32, (B,), "next_token", dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev)
+    _launch(lib().irm_tree_verify, dev, stream, tp, dp, ld, V, tk, pr, un, q_indptr.tobytes(), B, max_path, na, pa, nt, ws,
+            ws_bytes)
     return n_accept, path, next_token, workspace
 
 
@@ -508,35 +531,33 @@ def pages_workspace_size(n_slots: int) -> int:
     return n.value
 
 
-def _need_pages(seq_len, page_table, refcount):
-    _need(seq_len, torch.int32, "seq_len", 1)
-    _need(page_table, torch.int32, "page_table", 2)
-    _need(refcount, torch.int32, "refcount", 1)
-    _need_shape(page_table, (seq_len.shape[0], page_table.shape[1]), "page_table")
+def _take_pages(seq_len, page_table, refcount):
+    """Addresses and sizes of the page state: (device, n_slots, max_pages, n_pages, seq_len, page_table, refcount)."""
+    n_slots, max_pages, n_pages = _size(seq_len, 0, "seq_len"), _size(page_table, 1, "page_table"), _size(refcount, 0, "refcount")
+    dev = seq_len.device
+    return (dev, n_slots, max_pages, n_pages, _take(seq_len, torch.int32, (n_slots,), "seq_len", dev),
+            _take(page_table, torch.int32, (n_slots, max_pages), "page_table", dev),
+            _take(refcount, torch.int32, (n_pages,), "refcount", dev))
 
 
-def _need_cache(kv, n_pages=None):
-    """[n_layers, n_pages, 64, 576] bf16, or one layer's [n_pages, 64, 576]: (layers, pages)."""
-    _need(kv, torch.bfloat16, "kv")
-    if kv.dim() not in (3, 4) or tuple(kv.shape[-2:]) != (64, 576):
+def _take_cache(kv, device, n_pages=None):
+    """[n_layers, n_pages, 64, 576] bf16, or one layer's [n_pages, 64, 576]: (address, layers, pages)."""
+    if not isinstance(kv, torch.Tensor) or kv.dim() not in (3, 4):
         raise ValueError("kv must be [n_layers, n_pages, 64, 576] or [n_pages, 64, 576]")
-    if n_pages is not None and kv.shape[-3] != n_pages:
-        raise ValueError(f"kv must have refcount's {n_pages} pages, not {kv.shape[-3]}")
-    return (int(kv.shape[0]) if kv.dim() == 4 else 1), int(kv.shape[-3])
+    shape = kv.shape
+    pages = shape[-3] if n_pages is None else n_pages
+    layers = shape[0] if len(shape) == 4 else 1
+    want = (layers, pages, 64, 576) if len(shape) == 4 else (pages, 64, 576)
+    return _take(kv, torch.bfloat16, want, "kv", device), layers, pages
 
 
 def irm_pages_resize(new_len, seq_len, page_table, refcount, workspace=None, stream=None):
     """Every request to new_len [n_slots] rows (device int32): allocates, trims or, with 0, frees its pages.
     seq_len [n_slots], page_table [n_slots, max_pages] and refcount [n_pages] (int32) are updated."""
-    _need_pages(seq_len, page_table, refcount)
-    _need(new_len, torch.int32, "new_len", 1)
-    _need_shape(new_len, seq_len.shape, "new_len")
-    n_slots = int(seq_len.shape[0])
-    workspace = _workspace(workspace, pages_workspace_size(n_slots) if workspace is None else 0, seq_len.device)
-    with _one_device(seq_len, new_len, page_table, refcount, workspace):
-        _check(lib().irm_pages_resize(_ptr(new_len), _ptr(seq_len), n_slots, _ptr(page_table), int(page_table.shape[1]),
-                                      _ptr(refcount), int(refcount.shape[0]), _ptr(workspace), workspace.numel(),
-                                      _stream(stream)))
+    dev, n_slots, max_pages, n_pages, sl, pt, rc = _take_pages(seq_len, page_table, refcount)
+    nl = _take(new_len, torch.int32, (n_slots,), "new_len", dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev)
+    _launch(lib().irm_pages_resize, dev, stream, nl, sl, n_slots, pt, max_pages, rc, n_pages, ws, ws_bytes)
     return workspace
 
 
@@ -546,31 +567,27 @@ def irm_pages_fork(src, dst, kv, seq_len, page_table, refcount, workspace=None, 
     src, dst = _host_i32(src, "src"), _host_i32(dst, "dst")
     if len(src) != len(dst):
         raise ValueError("src and dst must have the same length")
-    _need_pages(seq_len, page_table, refcount)
-    layers, n_pages = _need_cache(kv, int(refcount.shape[0]))
-    n_slots = int(seq_len.shape[0])
-    workspace = _workspace(workspace, pages_workspace_size(n_slots) if workspace is None else 0, seq_len.device)
-    with _one_device(seq_len, kv, page_table, refcount, workspace):
-        _check(lib().irm_pages_fork(_ptr(src), _ptr(dst), len(src), _ptr(kv), layers, _ptr(seq_len), n_slots,
-                                    _ptr(page_table), int(page_table.shape[1]), _ptr(refcount), n_pages,
-                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+    dev, n_slots, max_pages, n_pages, sl, pt, rc = _take_pages(seq_len, page_table, refcount)
+    cache, layers, _ = _take_cache(kv, dev, n_pages)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev)
+    _launch(lib().irm_pages_fork, dev, stream, src.tobytes(), dst.tobytes(), len(src), cache, layers, sl, n_slots, pt, max_pages,
+            rc, n_pages, ws, ws_bytes)
     return workspace
 
 
 def irm_pages_compact(kv, page_table, base, path, n_accept, workspace=None, stream=None):
     """Moves accepted drafts' rows base + path[:, k] to base + k, k < n_accept, in every layer of kv; base,
     n_accept [n_slots] and path [n_slots, max_path] int32 on the device (irm_tree_verify's outputs)."""
-    layers, n_pages = _need_cache(kv)
-    _need(page_table, torch.int32, "page_table", 2)
-    n_slots = int(page_table.shape[0])
-    for t, ndim, name in ((base, 1, "base"), (path, 2, "path"), (n_accept, 1, "n_accept")):
-        _need(t, torch.int32, name, ndim)
-        _need_shape(t, (n_slots, *t.shape[1:]), name)
-    workspace = _workspace(workspace, WORKSPACE_HEADER, kv.device)
-    with _one_device(kv, page_table, base, path, n_accept, workspace):
-        _check(lib().irm_pages_compact(_ptr(kv), layers, n_pages, _ptr(page_table), int(page_table.shape[1]), n_slots,
-                                       _ptr(base), _ptr(path), int(path.shape[1]), _ptr(n_accept), _ptr(workspace),
-                                       workspace.numel(), _stream(stream)))
+    max_pages, max_path = _size(page_table, 1, "page_table"), _size(path, 1, "path")
+    dev, n_slots = page_table.device, page_table.shape[0]
+    cache, layers, n_pages = _take_cache(kv, dev)
+    pt = _take(page_table, torch.int32, (n_slots, max_pages), "page_table", dev)
+    ba = _take(base, torch.int32, (n_slots,), "base", dev)
+    pa = _take(path, torch.int32, (n_slots, max_path), "path", dev)
+    na = _take(n_accept, torch.int32, (n_slots,), "n_accept", dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev)
+    _launch(lib().irm_pages_compact, dev, stream, cache, layers, n_pages, pt, max_pages, n_slots, ba, pa, max_path, na, ws,
+            ws_bytes)
     return workspace
 
 
@@ -579,9 +596,10 @@ def irm_pages_copy(kv, src, dst, stream=None):
     src, dst = _host_i32(src, "src"), _host_i32(dst, "dst")
     if len(src) != len(dst):
         raise ValueError("src and dst must have the same length")
-    layers, n_pages = _need_cache(kv)
-    with _one_device(kv):
-        _check(lib().irm_pages_copy(_ptr(kv), layers, n_pages, _ptr(src), _ptr(dst), len(src), _stream(stream)))
+    if not isinstance(kv, torch.Tensor):
+        raise ValueError("kv must be [n_layers, n_pages, 64, 576] or [n_pages, 64, 576]")
+    cache, layers, n_pages = _take_cache(kv, kv.device)
+    _launch(lib().irm_pages_copy, kv.device, stream, cache, layers, n_pages, src.tobytes(), dst.tobytes(), len(src))
 
 
 ASSEMBLE_S1 = 1
