@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstring>
 #include <exception>
+#include <mutex>
 #include <vector>
 
 #include "irm_common.cuh"
@@ -78,25 +79,29 @@ __device__ __forceinline__ unsigned free_bits(const int32_t* refcount, int64_t p
 }
 
 // The lowest `want` free pages, in index order: take(rank, page) for each.  Returns false, having
-// taken none, when there are fewer.  Called by the whole block.
+// taken none, when there are fewer.  Called by the whole block; a thread's ranks increase.
 template <class Take>
 __device__ __forceinline__ bool take_free(const int32_t* refcount, int64_t n_pages, int want, int* part, Take take) {
   if (want == 0) return true;
   const bool vec = (reinterpret_cast<uintptr_t>(refcount) & 15u) == 0;
   constexpr int64_t kRound = (int64_t)kThreads * kScanPages;
-  int found = 0, n = 0;
+  int found = 0, n = 0, rank = 0, rounds = 0;
+  unsigned m = 0;
   for (int64_t p0 = 0; p0 < n_pages && found < want; p0 += kRound) {
-    const unsigned m = free_bits(refcount, p0 + (int64_t)threadIdx.x * kScanPages, n_pages, vec);
-    block_exclusive(__popc(m), part, &n);
+    m = free_bits(refcount, p0 + (int64_t)threadIdx.x * kScanPages, n_pages, vec);
+    rank = block_exclusive(__popc(m), part, &n);
     found += n;
+    ++rounds;
   }
   if (found < want) return false;
   int rank0 = 0;
   for (int64_t p0 = 0; p0 < n_pages && rank0 < want; p0 += kRound) {
     const int64_t p = p0 + (int64_t)threadIdx.x * kScanPages;
-    unsigned m = free_bits(refcount, p, n_pages, vec);
-    int r = rank0 + block_exclusive(__popc(m), part, &n);
-    for (; m != 0 && r < want; m &= m - 1, ++r) take(r, (int)(p + __ffs((int)m) - 1));
+    if (rounds > 1) {  // the bits at hand are the last round's
+      m = free_bits(refcount, p, n_pages, vec);
+      rank = rank0 + block_exclusive(__popc(m), part, &n);
+    }
+    for (int r = rank; m != 0 && r < want; m &= m - 1, ++r) take(r, (int)(p + __ffs((int)m) - 1));
     rank0 += n;
   }
   return true;
@@ -112,6 +117,12 @@ __device__ __forceinline__ int owner_of(const int* pre, int n, int r) {
   }
   return lo;
 }
+// The same for increasing ranks: starts at the owner of the rank before (-1: none yet).
+__device__ __forceinline__ int next_owner(const int* pre, int n, int r, int s) {
+  if (s < 0) return owner_of(pre, n, r);
+  while (pre[s + 1] <= r) ++s;
+  return s;
+}
 
 struct ResizeArgs {
   const int32_t* new_len;
@@ -123,74 +134,94 @@ struct ResizeArgs {
   int* status;
 };
 
+// All requests' pages form one list for each phase (released, then wanted), which the threads share
+// evenly whatever the requests' lengths: a position's request is found in the list's exclusive sums.
 __global__ void __launch_bounds__(kThreads) pages_resize_kernel(const ResizeArgs a) {
-  extern __shared__ int pre[];  // [n_slots + 1]: pages wanted, then their exclusive sums
+  extern __shared__ int pre[];          // [n_slots + 1]: exclusive sums of the phase's pages
+  int* held = pre + a.n_slots + 1;      // [n_slots]: pages held before, -1 for a refused request
   __shared__ int part[32];
-  __shared__ uint32_t refused[kMaxSlots / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int most = a.max_pages * kPage;
-  for (int i = tid; i < (a.n_slots + 31) / 32; i += kThreads) refused[i] = 0;
-  __syncthreads();
-  // ---- releases: a warp per request -------------------------------------------------------
-  for (int s = warp; s < a.n_slots; s += kWarps) {
-    const int old = a.seq_len[s], now = a.new_len[s];
-    if (old < 0 || old > most || now < 0 || now > most) {
-      if (lane == 0) {
-        set_status(a.status, kDevErrBounds);
-        atomicOr(&refused[s >> 5], 1u << (s & 31));
-      }
-      continue;
-    }
-    int32_t* row = a.table + (int64_t)s * a.max_pages;
-    for (int i = pages_of(now) + lane; i < pages_of(old); i += 32) {
-      const int p = row[i];
-      row[i] = -1;
-      bool ok = p >= 0 && p < a.n_pages;
-      if (ok && atomicSub(&a.refcount[p], 1) <= 0) {
-        atomicAdd(&a.refcount[p], 1);
-        ok = false;
-      }
+  // ---- releases -----------------------------------------------------------------------------
+  int total = 0, n;
+  for (int s0 = 0; s0 < a.n_slots; s0 += kThreads) {
+    const int s = s0 + tid;
+    int gone = 0;
+    if (s < a.n_slots) {
+      const int old = a.seq_len[s], now = a.new_len[s];
+      const bool ok = old >= 0 && old <= most && now >= 0 && now <= most;
       if (!ok) set_status(a.status, kDevErrBounds);
+      held[s] = ok ? pages_of(old) : -1;
+      gone = ok ? max(0, pages_of(old) - pages_of(now)) : 0;
     }
+    const int at = block_exclusive(gone, part, &n);
+    if (s < a.n_slots) pre[s] = total + at;
+    total += n;
+  }
+  if (tid == 0) pre[a.n_slots] = total;
+  __syncthreads();
+  constexpr int kBatch = 4;  // pages a thread has in flight
+  for (int r0 = tid; r0 < total; r0 += kBatch * kThreads) {
+    int page[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * kThreads;
+      if (r < total) {
+        const int s = owner_of(pre, a.n_slots, r);
+        int32_t* e = a.table + (int64_t)s * a.max_pages + held[s] - pre[s + 1] + r;
+        page[k] = *e;
+        *e = -1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (r0 + k * kThreads < total) {
+        bool ok = page[k] >= 0 && page[k] < a.n_pages;
+        if (ok && atomicSub(&a.refcount[page[k]], 1) <= 0) {
+          atomicAdd(&a.refcount[page[k]], 1);
+          ok = false;
+        }
+        if (!ok) set_status(a.status, kDevErrBounds);
+      }
   }
   __syncthreads();
-  // ---- what each request wants -----------------------------------------------------------
-  int total = 0;
+  // ---- what each request wants -----------------------------------------------------------------
+  total = 0;
   for (int s0 = 0; s0 < a.n_slots; s0 += kThreads) {
     const int s = s0 + tid;
     int need = 0;
-    if (s < a.n_slots && !(refused[s >> 5] >> (s & 31) & 1u)) {
+    if (s < a.n_slots && held[s] >= 0) {
       const int old = a.seq_len[s], now = a.new_len[s];
       if (now > old) {
-        need = pages_of(now) - pages_of(old);
+        need = pages_of(now) - held[s];
         if (old % kPage != 0) {  // it would write into its last page: that must be its own
           const int p = a.table[(int64_t)s * a.max_pages + old / kPage];
           const bool in = p >= 0 && p < a.n_pages;
           if (!in || a.refcount[p] > 1) {
             set_status(a.status, in ? kDevErrShared : kDevErrBounds);
-            atomicOr(&refused[s >> 5], 1u << (s & 31));
+            held[s] = -1;
             need = 0;
           }
         }
       }
     }
-    int n;
     const int at = block_exclusive(need, part, &n);
     if (s < a.n_slots) pre[s] = total + at;
     total += n;
   }
   if (tid == 0) pre[a.n_slots] = total;
   __syncthreads();
-  // ---- allocations -----------------------------------------------------------------------
+  // ---- allocations -----------------------------------------------------------------------------
+  int s_of = -1;
   const bool enough = take_free(a.refcount, a.n_pages, total, part, [&](int r, int page) {
-    const int s = owner_of(pre, a.n_slots, r);
-    a.table[(int64_t)s * a.max_pages + pages_of(a.seq_len[s]) + (r - pre[s])] = page;
+    s_of = next_owner(pre, a.n_slots, r, s_of);
+    a.table[(int64_t)s_of * a.max_pages + held[s_of] + (r - pre[s_of])] = page;
     a.refcount[page] = 1;  // each count is read before the block barrier that precedes this write
   });
   __syncthreads();
   if (!enough && tid == 0) set_status(a.status, kDevErrNoPages);
   for (int s = tid; s < a.n_slots; s += kThreads)
-    if (!(refused[s >> 5] >> (s & 31) & 1u)) {
+    if (held[s] >= 0) {
       const int now = a.new_len[s];
       if (enough || now <= a.seq_len[s]) a.seq_len[s] = now;
     }
@@ -214,58 +245,67 @@ struct ForkArgs {
 static_assert(sizeof(ForkArgs) <= 32764, "kernel parameter block");
 
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_constant__ ForkArgs a) {
-  __shared__ int part[32], len[kMaxForks], pre[kMaxForks + 1], fresh[kMaxForks];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int part[32], len[kMaxForks], first[kMaxForks + 1], pre[kMaxForks + 1], fresh[kMaxForks];
+  __shared__ int src[kMaxForks], dst[kMaxForks];  // lanes that read parameters at their own place would take turns
+  const int f = threadIdx.x;  // a thread a fork where forks are looked at one by one
   const int most = a.max_pages * kPage;
-  // ---- sources and destinations: len = rows to fork, or -1 for a refused one ---------------
-  for (int f = warp; f < a.n_forks; f += kWarps) {
-    const int rows = a.seq_len[a.src[f]];
-    bool ok = rows >= 0 && rows <= most && a.seq_len[a.dst[f]] == 0;
-    if (ok) {
-      const int32_t* row = a.table + (int64_t)a.src[f] * a.max_pages;
-      for (int i = lane; i < pages_of(rows); i += 32) ok &= row[i] >= 0 && row[i] < a.n_pages;
+  // ---- sources and destinations: len = rows to fork, or -1 for a refused one; the sources' pages
+  //      form one list, shared evenly by the threads --------------------------------------------
+  int rows = -1;
+  if (f < a.n_forks) {
+    src[f] = a.src[f];
+    dst[f] = a.dst[f];
+    rows = a.seq_len[src[f]];
+    if (rows < 0 || rows > most || a.seq_len[dst[f]] != 0) {
+      rows = -1;
+      set_status(a.status, kDevErrBounds);
     }
-    ok = __all_sync(kFull, ok);
-    if (lane == 0) {
-      len[f] = ok ? rows : -1;
-      if (!ok) set_status(a.status, kDevErrBounds);
+    len[f] = rows;
+  }
+  int pages;
+  const int at0 = block_exclusive(rows > 0 ? pages_of(rows) : 0, part, &pages);
+  if (f < a.n_forks) first[f] = at0;
+  if (f == 0) first[a.n_forks] = pages;
+  __syncthreads();
+  int g = -1;
+  for (int r = threadIdx.x; r < pages; r += kThreads) {
+    g = next_owner(first, a.n_forks, r, g);
+    const int p = a.table[(int64_t)src[g] * a.max_pages + (r - first[g])];
+    if (p < 0 || p >= a.n_pages) {
+      set_status(a.status, kDevErrBounds);
+      len[g] = -1;
     }
   }
   __syncthreads();
   int total;
-  const int need = tid < a.n_forks && len[tid] > 0 && len[tid] % kPage != 0 ? 1 : 0;
+  const int need = f < a.n_forks && len[f] > 0 && len[f] % kPage != 0 ? 1 : 0;
   const int at = block_exclusive(need, part, &total);
-  if (tid < a.n_forks) pre[tid] = at;
+  if (f < a.n_forks) pre[f] = at;
+  if (f == 0) pre[a.n_forks] = total;
   __syncthreads();
   const bool enough = take_free(a.refcount, a.n_pages, total, part, [&](int r, int page) {
     fresh[owner_of(pre, a.n_forks, r)] = page;
   });
   __syncthreads();
-  if (!enough && tid == 0) set_status(a.status, kDevErrNoPages);
-  for (int f = warp; f < a.n_forks; f += kWarps) {
-    const int rows = len[f];
-    if (!enough || rows < 0) {
-      if (lane == 0) a.jobs[f] = CopyJob{0, 0, 0, 0};
-      continue;
-    }
-    const int full = rows / kPage;
-    const int32_t* from = a.table + (int64_t)a.src[f] * a.max_pages;
-    int32_t* to = a.table + (int64_t)a.dst[f] * a.max_pages;
-    for (int i = lane; i < full; i += 32) {
-      const int p = from[i];
-      to[i] = p;
+  if (!enough && f == 0) set_status(a.status, kDevErrNoPages);
+  // ---- the destinations' tables: full pages shared, a fresh one for the partly filled last ------
+  g = -1;
+  for (int r = threadIdx.x; enough && r < pages; r += kThreads) {
+    g = next_owner(first, a.n_forks, r, g);
+    if (len[g] < 0) continue;
+    const int i = r - first[g], p = a.table[(int64_t)src[g] * a.max_pages + i];
+    const bool full = i < len[g] / kPage;
+    a.table[(int64_t)dst[g] * a.max_pages + i] = full ? p : fresh[g];
+    if (full) {
       atomicAdd(&a.refcount[p], 1);
+    } else {
+      a.refcount[fresh[g]] = 1;
+      a.jobs[g] = CopyJob{p, fresh[g], len[g] % kPage, 0};
     }
-    if (lane == 0) {
-      CopyJob j{0, 0, 0, 0};
-      if (rows % kPage != 0) {
-        j = CopyJob{from[full], fresh[f], rows % kPage, 0};
-        to[full] = fresh[f];
-        a.refcount[fresh[f]] = 1;
-      }
-      a.jobs[f] = j;
-      a.seq_len[a.dst[f]] = rows;
-    }
+  }
+  if (f < a.n_forks) {
+    if (enough && len[f] >= 0) a.seq_len[dst[f]] = len[f];
+    if (!enough || len[f] <= 0 || len[f] % kPage == 0) a.jobs[f] = CopyJob{0, 0, 0, 0};
   }
 }
 
@@ -415,6 +455,22 @@ irm_status check_pairs(const int32_t* src, const int32_t* dst, int m, int64_t n,
   return st;
 }
 
+// The resize kernel's dynamic shared memory limit belongs to the device: raised once on each, for
+// more slots than fit by default.
+cudaError_t raise_resize_smem() {
+  static std::mutex mu;
+  static bool done[128];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev >= 0 && dev < 128 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(pages_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)((2 * kMaxSlots + 1) * sizeof(int)));
+  if (e == cudaSuccess && dev >= 0 && dev < 128) done[dev] = true;
+  return e;
+}
+
 size_t workspace_need() { return IRM_WORKSPACE_HEADER + kMaxForks * sizeof(CopyJob); }
 
 // Shares of a page that make a few thousand blocks where there are few pages to copy (16 at most,
@@ -449,8 +505,11 @@ irm_status irm_pages_resize(const int32_t* new_len, int32_t* seq_len, int n_slot
     return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
   if ((st = check_workspace(workspace, workspace_bytes, workspace_need())) != IRM_OK) return st;
   const ResizeArgs a{new_len, seq_len, n_slots, max_pages, page_table, refcount, n_pages, static_cast<int*>(workspace)};
-  pages_resize_kernel<<<1, kThreads, (size_t)(n_slots + 1) * sizeof(int), stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const size_t smem = (size_t)(2 * n_slots + 1) * sizeof(int);
+  cudaError_t e = smem > 40960 ? raise_resize_smem() : cudaSuccess;
+  if (e != cudaSuccess) return cuda_fail(e, "page resize set-up");
+  pages_resize_kernel<<<1, kThreads, smem, stream>>>(a);
+  e = cudaGetLastError();
   return e == cudaSuccess ? IRM_OK : cuda_fail(e, "page resize launch");
 }
 

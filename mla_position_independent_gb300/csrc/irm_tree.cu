@@ -51,7 +51,7 @@ constexpr int kBatch = 256;  // requests per launch (their lengths travel in the
 constexpr int kBM = 128;     // query rows of a unit
 constexpr int kHalf = 64;    // of which a CTA owns
 constexpr int kScoreWarps = 8;
-constexpr int kTmaWarp = 8, kSWarp = 9, kPvWarp = 10;  // and 11, the clearing
+constexpr int kTmaWarp = 8, kSWarp = 9, kPvWarp = 10, kClearWarp = 11;
 constexpr int kThreads = 12 * 32;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -107,6 +107,12 @@ constexpr uint32_t kTmemO = 0, kTmemQ = 256, kTmemS = 384, kTmemCols = 512;
 constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kPage, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, 256, 0, 1);
 
+// A request: its first node (of the batch's T) and nodes, its rows before them, and how many units of
+// full pieces, units of rests and partials come before its own.
+struct Request {
+  int32_t first, n, ctx, long_base, rest_base, part_base, pad[2];
+};
+
 struct TreeArgs {
   CUtensorMap map_lat, map_rope;  // pages [rows, 576]: boxes of 64 x 64, and of 64 rows x 32 columns
   CUtensorMap map_ql, map_qr;     // queries [T H, 512] and [T H, 64]: boxes of 32 rows x 64, and x 32 columns
@@ -122,20 +128,20 @@ struct TreeArgs {
   float* opart;    // fp32 [partial][128][512]
   float* lsepart;  // fp32 [partial][128], log2 units
   int* status;
-  int32_t ctx[kBatch], indptr[kBatch + 1];
-  int32_t long_base[kBatch + 1], rest_base[kBatch + 1], part_base[kBatch + 1];
+  Request req[kBatch];
 };
 static_assert(sizeof(TreeArgs) <= 32764, "kernel parameter block");
 
 __host__ __device__ inline int row_tiles(int n, int H) { return (n * H + kBM - 1) / kBM; }
 __host__ __device__ inline int page_count(int ctx, int n) { return n > 0 ? (ctx + n + kPage - 1) / kPage : 0; }
 
-// Last b in [0, B) with base[b] <= u: the owner of u among entries with a positive share.
-__device__ __forceinline__ int owner_of(const int32_t* base, int B, int u) {
-  int lo = 0, hi = B;
+// Last b in [0, B) with req[b].*base <= u: the owner of u among requests with a positive share.
+template <int32_t Request::*base>
+__device__ __forceinline__ int owner_of(const TreeArgs& a, int u) {
+  int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (base[mid] <= u) lo = mid; else hi = mid;
+    if (a.req[mid].*base <= u) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -211,10 +217,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int unit = (int)(blockIdx.x >> 1);
   const bool is_rest = unit >= a.n_long;
   const int at = is_rest ? unit - a.n_long : unit;
-  const int b = owner_of(is_rest ? a.rest_base : a.long_base, a.B, at);
-  const int first_node = a.indptr[b], n = a.indptr[b + 1] - first_node, ctx = a.ctx[b];
+  const int b = is_rest ? owner_of<&Request::rest_base>(a, at) : owner_of<&Request::long_base>(a, at);
+  const Request req = a.req[b];
+  const int first_node = req.first, n = req.n, ctx = req.ctx;
   const int mtiles = row_tiles(n, a.H), tiles_all = page_count(ctx, n);
-  const int in_b = at - (is_rest ? a.rest_base[b] : a.long_base[b]);
+  const int in_b = at - (is_rest ? req.rest_base : req.long_base);
   const int piece = is_rest ? tiles_all / a.piece : in_b / mtiles;
   const int mtile = is_rest ? in_b : in_b % mtiles;
   const int kb = piece * a.piece;
@@ -265,11 +272,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp) {
     if (lane < ntiles) page0 = ptab[lane];
     if (lane == 0) {
-      tma_prefetch_map(&a.map_ql);
-      tma_prefetch_map(&a.map_qr);
       tma_prefetch_map(&a.map_lat);
       tma_prefetch_map(&a.map_rope);
     }
+  } else if (warp == kClearWarp && lane == 0) {
+    tma_prefetch_map(&a.map_ql);
+    tma_prefetch_map(&a.map_qr);
   }
   if (warp == kSWarp) {
     tmem_alloc(sb + kOffTmem, kTmemCols);
@@ -446,18 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (ok && live && !own && j > set) ok = take_factors(j - 2);
     if (own) reinterpret_cast<float2*>(smem + kOffSum)[set * kHalf + mh] = make_float2(m_l, l);
   } else if (warp == kTmaWarp) {
-    // ================= Q and pages in =================
-    if (lane == 0) {
-      const int quads = (rows_valid + 31) / 32;
-      mbar_arrive_expect_tx(bar(BAR_QIN), (uint32_t)quads * 32u * (512u + 64u));
-      for (int q = 0; q < quads; ++q) {  // rows behind the request's last (another's, or zeros) are never looked at
-        const int y = (int)grow0 + 32 * q;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tma_load_2d(sb + kOffQl + c * (kBM * 128) + q * 4096, &a.map_ql, 256 * rank + 64 * c, y, bar(BAR_QIN));
-        tma_load_2d(sb + kOffQr + q * 2048, &a.map_qr, 32 * rank, y, bar(BAR_QIN));
-      }
-    }
+    // ================= pages in =================
     int page = 0, sent = 0;
     for (int j = 0; j < ntiles; ++j) {
       if ((j & 31) == 0) {
@@ -546,7 +543,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_wait();
-  } else {
+  } else if (warp == kClearWarp) {
+    // ================= Q in =================
+    if (lane == 0) {
+      const int quads = (rows_valid + 31) / 32;
+      mbar_arrive_expect_tx(bar(BAR_QIN), (uint32_t)quads * 32u * (512u + 64u));
+      for (int q = 0; q < quads; ++q) {  // rows behind the request's last (another's, or zeros) are never looked at
+        const int y = (int)grow0 + 32 * q;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tma_load_2d(sb + kOffQl + c * (kBM * 128) + q * 4096, &a.map_ql, 256 * rank + 64 * c, y, bar(BAR_QIN));
+        tma_load_2d(sb + kOffQr + q * 2048, &a.map_qr, 32 * rank, y, bar(BAR_QIN));
+      }
+    }
+    __syncwarp();
     // ================= rows that no node of the unit sees become zeros =================
     const int node0 = row0 / a.H, node1 = (row0 + rows_valid - 1) / a.H;
     for (int j = 0; j < ntiles; ++j) {
@@ -587,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const bool split = pieces > 1;
-  const int64_t part = split ? (int64_t)a.part_base[b] + (int64_t)mtile * pieces + piece : 0;
+  const int64_t part = split ? (int64_t)req.part_base + (int64_t)mtile * pieces + piece : 0;
   float* inv_sh = reinterpret_cast<float*>(smem + kOffInv);
   if (tid < kHalf) {
     const int m = kHalf * rank + tid;
@@ -675,13 +685,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr int kMergeThreads = kDLat / 4;
 
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  const int node = a.indptr[0] + (int)(blockIdx.x / a.H);
-  const int b = owner_of(a.indptr, a.B, node);
-  const int n = a.indptr[b + 1] - a.indptr[b], tiles = page_count(a.ctx[b], n);
-  const int pieces = (tiles + a.piece - 1) / a.piece;
+  const int node = a.req[0].first + (int)(blockIdx.x / a.H);
+  const Request req = a.req[owner_of<&Request::first>(a, node)];
+  const int tiles = page_count(req.ctx, req.n), pieces = (tiles + a.piece - 1) / a.piece;
   if (pieces <= 1) return;
-  const int row = (node - a.indptr[b]) * a.H + (int)(blockIdx.x % a.H);
-  const int64_t part = (int64_t)a.part_base[b] + (int64_t)(row / kBM) * pieces;
+  const int row = (node - req.first) * a.H + (int)(blockIdx.x % a.H);
+  const int64_t part = (int64_t)req.part_base + (int64_t)(row / kBM) * pieces;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the units' kernel has ended
   const float* lse = a.lsepart + part * kBM + row % kBM;
   const float* o = a.opart + (part * kBM + row % kBM) * kDLat + 4 * threadIdx.x;
   float mx = -INFINITY;
@@ -700,7 +710,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const int64_t grow = (int64_t)a.indptr[b] * a.H + row;
+  const int64_t grow = (int64_t)req.first * a.H + row;
   *reinterpret_cast<uint2*>(a.out + grow * kDLat + 4 * threadIdx.x) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   if (a.lse != nullptr && threadIdx.x == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
@@ -714,39 +724,70 @@ struct Plan {
   int64_t parts;  // partial results (units of cut requests)
 };
 
-// The cut with the least estimated time, in tile times: waves of units over the pairs of SMs, each
-// unit its pages and ~10 tile times of start and end; partials cost a merge.
+// Time until the last of a batch's units ends, in tile times: n_long units of `piece` pages each and
+// then n_rest of `rest` (their mean), each with a start and end of `unit` tiles, are taken in this
+// order by `pairs` pairs of SMs as they come free.
+double makespan(int64_t n_long, double piece, int64_t n_rest, double rest, double unit, int pairs) {
+  const double tl = piece + unit, tr = rest + unit;
+  const int64_t waves = n_long / pairs, over = n_long % pairs;  // `over` pairs run one long unit more
+  const double t0 = (double)waves * tl, t1 = t0 + tl;
+  if (n_rest == 0) return over ? t1 : t0;
+  // k rests on each of the pairs that come free first, until the others come free too
+  const int64_t early = over ? pairs - over : 0;
+  const int64_t fit = (int64_t)((t1 - t0) / tr + 0.999) * early;  // those started before t1
+  if (over && n_rest <= fit) return std::max(t1, t0 + std::ceil((double)n_rest / (double)early) * tr);
+  const double from = over ? t1 : t0;
+  const int64_t left = over ? n_rest - (int64_t)((t1 - t0) / tr) * early : n_rest;
+  return from + std::ceil((double)left / pairs) * tr;
+}
+
+// The cut with the least estimated time.  In tile times, measured: a unit's start and end take ~8 (12
+// where units have at most 64 rows and a tile takes ~0.9 instead of ~1.2 us), a cut batch's merge 5
+// and a tenth for each partial.  With 8 for few rows a batch of 8 x 8192, 16 heads, one node, got
+// 80 units for the 76 pairs: 32.2 against 25.4 us.
+constexpr double kMergeCost = 5.0, kPartCost = 0.1;
 Plan plan_batch(const int32_t* ctx, const int32_t* indptr, int B, int H, int pairs) {
   struct Like {
     int tiles, mt, count;  // neighbouring requests alike count as one
   } like[kBatch];
-  int kinds = 0, most = 1;
+  int kinds = 0, most = 1, rows = 0;
   for (int b = 0; b < B; ++b) {
     const int n = indptr[b + 1] - indptr[b], tiles = page_count(ctx[b], n), mt = row_tiles(n, H);
     if (n == 0) continue;
     most = std::max(most, tiles);
+    rows = std::max(rows, n * H);
     if (kinds > 0 && like[kinds - 1].tiles == tiles && like[kinds - 1].mt == mt) ++like[kinds - 1].count;
     else like[kinds++] = Like{tiles, mt, 1};
   }
   Plan best{most, 0, 0, 0};
   double best_cost = 1e300;
-  static constexpr int kCuts[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 19, 22, 25, 30, 38, 50, 76};
-  for (const int cuts : kCuts) {
-    if (cuts > most) break;
-    Plan p{(most + cuts - 1) / cuts, 0, 0, 0};
-    for (int k = 0; k < kinds; ++k) {
-      const Like& g = like[k];
-      const int full = g.tiles / p.piece, rest = g.tiles % p.piece ? 1 : 0, units = g.mt * g.count;
-      p.n_long += units * full;
-      p.n_rest += units * rest;
-      if (full + rest > 1) p.parts += (int64_t)units * (full + rest);
+  // pieces from the longest context down, by steps of a few percent (fewer steps where every
+  // request is of another length)
+  const double unit = rows <= kHalf ? 12.0 : 8.0;
+  const double step = kinds <= 8 ? 0.97 : 0.88;
+  int last = 0;
+  for (double f = 1.0;; f *= step) {
+    const int piece = std::max(1, (int)std::ceil((double)most * f));
+    if (piece != last) {
+      Plan p{piece, 0, 0, 0};
+      double rests = 0.0;
+      for (int k = 0; k < kinds; ++k) {
+        const Like& g = like[k];
+        const int full = g.tiles / piece, rest = g.tiles - full * piece, units = g.mt * g.count;
+        p.n_long += units * full;
+        if (rest) p.n_rest += units;
+        rests += (double)units * rest;
+        if (full + (rest ? 1 : 0) > 1) p.parts += (int64_t)units * (full + (rest ? 1 : 0));
+      }
+      const double cost = makespan(p.n_long, piece, p.n_rest, p.n_rest ? rests / p.n_rest : 0.0, unit, pairs) +
+                          (p.parts ? kMergeCost + kPartCost * (double)p.parts : 0.0);
+      if (cost < best_cost - 1e-9) {
+        best_cost = cost;
+        best = p;
+      }
+      last = piece;
     }
-    const double units = (double)p.n_long + p.n_rest;
-    const double cost = std::ceil(units / pairs) * (p.piece + 10.0) + (p.parts ? 6.0 + 0.02 * (double)p.parts : 0.0);
-    if (cost < best_cost - 1e-9) {
-      best_cost = cost;
-      best = p;
-    }
+    if (piece == 1 || f * most < 3.0) break;
   }
   return best;
 }
@@ -896,9 +937,8 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
   for (int b0 = 0; b0 < B; b0 += kBatch) {
     a.b0 = b0;
     a.B = std::min(kBatch, B - b0);
-    std::memcpy(a.ctx, ctx_host + b0, (size_t)a.B * sizeof(int32_t));
-    std::memcpy(a.indptr, q_indptr_host + b0, (size_t)(a.B + 1) * sizeof(int32_t));
-    const Plan p = plan_batch(a.ctx, a.indptr, a.B, H, pairs);
+    const int32_t *ctx = ctx_host + b0, *indptr = q_indptr_host + b0;
+    const Plan p = plan_batch(ctx, indptr, a.B, H, pairs);
     const int units = p.n_long + p.n_rest;
     if (units == 0) continue;
     a.piece = p.piece;
@@ -906,27 +946,30 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     int nl = 0, nr = 0;
     int64_t np = 0;
     for (int b = 0; b < a.B; ++b) {
-      const int n = a.indptr[b + 1] - a.indptr[b], tiles = page_count(a.ctx[b], n), mt = row_tiles(n, H);
-      a.long_base[b] = nl;
-      a.rest_base[b] = nr;
-      a.part_base[b] = (int32_t)np;
-      nl += mt * (tiles / p.piece);
-      nr += tiles % p.piece ? mt : 0;
-      const int pieces = (tiles + p.piece - 1) / p.piece;
-      if (pieces > 1) np += (int64_t)mt * pieces;
+      const int n = indptr[b + 1] - indptr[b], tiles = page_count(ctx[b], n), mt = row_tiles(n, H);
+      const int full = tiles / p.piece, rest = tiles % p.piece ? 1 : 0;
+      a.req[b] = Request{indptr[b], n, ctx[b], nl, nr, (int32_t)np, {0, 0}};
+      nl += mt * full;
+      nr += mt * rest;
+      if (full + rest > 1) np += (int64_t)mt * (full + rest);
     }
-    a.long_base[a.B] = nl;
-    a.rest_base[a.B] = nr;
-    a.part_base[a.B] = (int32_t)np;
     uint8_t* ws = static_cast<uint8_t*>(workspace) + IRM_WORKSPACE_HEADER;
     a.opart = reinterpret_cast<float*>(ws);
     a.lsepart = reinterpret_cast<float*>(ws + opart_bytes(p.parts));
     tree_attn_kernel<<<2 * units, kThreads, kSmem, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tree attention launch");
     if (p.parts) {
-      const int64_t merge = (int64_t)(a.indptr[a.B] - a.indptr[0]) * H;
-      tree_merge_kernel<<<(unsigned)merge, kMergeThreads, 0, stream>>>(a);
-      if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tree attention merge launch");
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)((int64_t)(indptr[a.B] - indptr[0]) * H));
+      cfg.blockDim = dim3(kMergeThreads);
+      cfg.stream = stream;
+      cudaLaunchAttribute early[1];
+      early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      early[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = early;
+      cfg.numAttrs = 1;
+      if ((e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, a)) != cudaSuccess)
+        return cuda_fail(e, "tree attention merge launch");
     }
   }
   return IRM_OK;
