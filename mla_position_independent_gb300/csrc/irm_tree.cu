@@ -597,6 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const bool split = pieces > 1;
+  if (split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for the rest of it
   const int64_t part = split ? (int64_t)req.part_base + (int64_t)mtile * pieces + piece : 0;
   float* inv_sh = reinterpret_cast<float*>(smem + kOffInv);
   if (tid < kHalf) {
@@ -680,11 +681,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Rows whose context was cut into pieces: O = sum 2^(lse_p - max) O_p / sum 2^(lse_p - max).  A
-// block a row, 4 columns a thread; rows of uncut requests have nothing to do.
-constexpr int kMergeThreads = kDLat / 4;
+// Rows whose context was cut into pieces: O = sum 2^(lse_p - max) O_p / sum 2^(lse_p - max).  Rows
+// of uncut requests have nothing to do.
+//
+// Few pieces (and so, as a rule, many rows): a warp a row, 16 columns a lane, no barrier.
+constexpr int kMergeFew = 8;
+constexpr int kMergeRows = 4;  // rows of a block
+__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_few_kernel(const __grid_constant__ TreeArgs a, int64_t rows) {
+  const int64_t r = (int64_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int lane = threadIdx.x & 31;
+  const int node = a.req[0].first + (int)(r / a.H);
+  const Request req = a.req[owner_of<&Request::first>(a, node)];
+  const int tiles = page_count(req.ctx, req.n), pieces = (tiles + a.piece - 1) / a.piece;
+  if (pieces <= 1) return;
+  const int row = (node - req.first) * a.H + (int)(r % a.H);
+  const int64_t part = (int64_t)req.part_base + (int64_t)(row / kBM) * pieces;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the units' kernel has ended
+  const float* lse = a.lsepart + part * kBM + row % kBM;
+  const float4* o = reinterpret_cast<const float4*>(a.opart + (part * kBM + row % kBM) * kDLat) + lane;
+  const float mine = lane < pieces ? lse[(int64_t)lane * kBM] : -INFINITY;
+  float mx = mine;
+#pragma unroll
+  for (int k = 4; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, k));  // kMergeFew lanes
+  mx = __shfl_sync(kFull, mx, 0);
+  const float w = mx == -INFINITY ? 0.f : fast_exp2(mine - mx);
+  float4 acc[4] = {};
+  float sum = 0.f;
+#pragma unroll 2
+  for (int p = 0; p < pieces; ++p) {
+    const float wp = __shfl_sync(kFull, w, p);
+    sum += wp;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 v = __ldcs(o + (int64_t)p * kBM * (kDLat / 4) + 32 * c);
+      acc[c].x += wp * v.x;
+      acc[c].y += wp * v.y;
+      acc[c].z += wp * v.z;
+      acc[c].w += wp * v.w;
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t grow = (int64_t)req.first * a.H + row;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint2*>(a.out + grow * kDLat + 128 * c + 4 * lane) =
+        make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
+  if (a.lse != nullptr && lane == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+}
 
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+// Many pieces (few rows): a block a row; groups of 128 threads (4 columns a thread) share the row's
+// pieces, eight loads of a thread in flight, and add up in shared memory.
+constexpr int kMergeGroup = kDLat / 4;
+constexpr int kMergeGroups = 4;
+constexpr int kMergeWeights = 128;
+
+__global__ void __launch_bounds__(kMergeGroup * kMergeGroups) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ float weight[kMergeWeights], top[16];
+  __shared__ float4 sums[kMergeGroups][kMergeGroup];
+  const int tid = threadIdx.x, group = tid / kMergeGroup;
+  constexpr int groups = kMergeGroups;
   const int node = a.req[0].first + (int)(blockIdx.x / a.H);
   const Request req = a.req[owner_of<&Request::first>(a, node)];
   const int tiles = page_count(req.ctx, req.n), pieces = (tiles + a.piece - 1) / a.piece;
@@ -693,27 +749,54 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   const int64_t part = (int64_t)req.part_base + (int64_t)(row / kBM) * pieces;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the units' kernel has ended
   const float* lse = a.lsepart + part * kBM + row % kBM;
-  const float* o = a.opart + (part * kBM + row % kBM) * kDLat + 4 * threadIdx.x;
+  const float* o = a.opart + (part * kBM + row % kBM) * kDLat + 4 * (tid % kMergeGroup);
   float mx = -INFINITY;
-  for (int p = 0; p < pieces; ++p) mx = fmaxf(mx, lse[(int64_t)p * kBM]);
+  for (int p = tid; p < pieces; p += blockDim.x) mx = fmaxf(mx, lse[(int64_t)p * kBM]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, k));
+  if ((tid & 31) == 0) top[tid >> 5] = mx;
+  __syncthreads();
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) mx = fmaxf(mx, top[w]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  if (mx != -INFINITY) {
-    for (int p = 0; p < pieces; ++p) {
-      const float w = fast_exp2(lse[(int64_t)p * kBM] - mx);
-      const float4 v = *reinterpret_cast<const float4*>(o + (int64_t)p * kBM * kDLat);
-      sum += w;
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
+  for (int p0 = 0; p0 < pieces && mx != -INFINITY; p0 += kMergeWeights) {
+    const int n = min(kMergeWeights, pieces - p0);
+    if (tid < n) weight[tid] = fast_exp2(lse[(int64_t)(p0 + tid) * kBM] - mx);
+    __syncthreads();
+    for (int k = 0; k < n; ++k) sum += weight[k];
+    constexpr int kUnroll = 8;
+    for (int k0 = group; k0 < n; k0 += kUnroll * groups) {
+      float4 v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (k0 + u * groups < n) v[u] = __ldcs(reinterpret_cast<const float4*>(o + (int64_t)(p0 + k0 + u * groups) * kBM * kDLat));
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (k0 + u * groups < n) {
+          const float w = weight[k0 + u * groups];
+          acc.x += w * v[u].x;
+          acc.y += w * v[u].y;
+          acc.z += w * v[u].z;
+          acc.w += w * v[u].w;
+        }
     }
+    __syncthreads();
+  }
+  sums[group][tid % kMergeGroup] = acc;
+  __syncthreads();
+  if (group > 0) return;
+  for (int g = 1; g < groups; ++g) {
+    const float4 v = sums[g][tid];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int64_t grow = (int64_t)req.first * a.H + row;
-  *reinterpret_cast<uint2*>(a.out + grow * kDLat + 4 * threadIdx.x) =
+  *reinterpret_cast<uint2*>(a.out + grow * kDLat + 4 * tid) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse != nullptr && threadIdx.x == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+  if (a.lse != nullptr && tid == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------------- host
@@ -943,7 +1026,7 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     if (units == 0) continue;
     a.piece = p.piece;
     a.n_long = p.n_long;
-    int nl = 0, nr = 0;
+    int nl = 0, nr = 0, most_pieces = 0;
     int64_t np = 0;
     for (int b = 0; b < a.B; ++b) {
       const int n = indptr[b + 1] - indptr[b], tiles = page_count(ctx[b], n), mt = row_tiles(n, H);
@@ -951,6 +1034,7 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
       a.req[b] = Request{indptr[b], n, ctx[b], nl, nr, (int32_t)np, {0, 0}};
       nl += mt * full;
       nr += mt * rest;
+      most_pieces = std::max(most_pieces, full + rest);
       if (full + rest > 1) np += (int64_t)mt * (full + rest);
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace) + IRM_WORKSPACE_HEADER;
@@ -960,16 +1044,18 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tree attention launch");
     if (p.parts) {
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)((int64_t)(indptr[a.B] - indptr[0]) * H));
-      cfg.blockDim = dim3(kMergeThreads);
+      const int64_t merge_rows = (int64_t)(indptr[a.B] - indptr[0]) * H;
+      const bool few = most_pieces <= kMergeFew;
+      cfg.gridDim = dim3((unsigned)(few ? (merge_rows + kMergeRows - 1) / kMergeRows : merge_rows));
+      cfg.blockDim = dim3(few ? 32 * kMergeRows : kMergeGroup * kMergeGroups);
       cfg.stream = stream;
       cudaLaunchAttribute early[1];
       early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       early[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = early;
       cfg.numAttrs = 1;
-      if ((e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, a)) != cudaSuccess)
-        return cuda_fail(e, "tree attention merge launch");
+      e = few ? cudaLaunchKernelEx(&cfg, tree_merge_few_kernel, a, merge_rows) : cudaLaunchKernelEx(&cfg, tree_merge_kernel, a);
+      if (e != cudaSuccess) return cuda_fail(e, "tree attention merge launch");
     }
   }
   return IRM_OK;
