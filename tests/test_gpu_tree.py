@@ -171,6 +171,15 @@ def test_long_context_many_heads():
     check(c, out, lse, heads=[0, 64, 127])
 
 
+@pytest.mark.parametrize("nodes", [1, 5])
+def test_many_pieces(nodes):
+    """One long context on the whole GPU: dozens of pieces of one row tile, each with a maximum of its own."""
+    c = make([50000], [nodes], 2, seed=25, q_std=0.6)
+    out, lse, ws = call(c)
+    irm.device_status(ws)
+    check(c, out, lse)
+
+
 @pytest.mark.parametrize("q_std", [0.0, 1.0, 6.0])
 def test_score_sizes(q_std):
     """Flat scores, and scores in the tens, where one row takes nearly all and the running maximum moves."""
@@ -267,6 +276,19 @@ def test_one_workspace_for_calls_of_different_sizes():
         out, lse, _ = call(c, workspace=ws)
         irm.device_status(ws)
         check(c, out, lse, heads=[0, 15])
+
+
+def test_workspace_is_checked():
+    c = make([9000, 4000], [3, 2], 16, seed=26)
+    need = irm.tree_workspace_size(c["ctx"], c["indptr"], 16)
+    assert need > 256  # the contexts are cut
+    ws = irm.new_workspace(need)
+    with pytest.raises(irm.IrmError) as e:
+        call(c, workspace=ws[:need - 256])
+    assert e.value.status == -8
+    out, lse, _ = call(c, workspace=ws)
+    irm.device_status(ws)
+    check(c, out, lse, heads=[0, 15])
 
 
 def test_two_streams_and_a_replayed_graph():

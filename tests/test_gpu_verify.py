@@ -87,6 +87,28 @@ def test_tree_shapes(draft, par):
     assert max(depth) > 1 or draft
 
 
+@pytest.mark.parametrize("B", [1, 39, 77, 160, 400])
+@pytest.mark.parametrize("draft", [False, True])
+def test_batch_sizes(B, draft):
+    """A request's row spread over 8, 4, 2 and 1 blocks."""
+    run_and_check(batch([5] * B, 1200, draft, seed=B))
+
+
+@pytest.mark.parametrize("B", [1, 50])
+def test_largest_vocabulary(B):
+    """2^20 entries: a flat row, where every entry counts, with borders next to the uniform numbers."""
+    V, rng = 1 << 20, np.random.default_rng(B)
+    target = torch.rand((B, V), device="cuda") + 0.5
+    target /= target.sum(1, keepdim=True)
+    c = dict(indptr=np.arange(B + 1, dtype=np.int32), target=target.cpu().numpy(), draft=None, tokens=np.zeros(B, np.int32),
+             parents=np.full(B, -1, np.int32), r=rng.random(B).astype(np.float32))
+    if B == 1:
+        c["r"][0] = np.nextafter(np.float32(1), np.float32(0))
+    n, path, token, ws = call(c)
+    irm.device_status(ws)
+    check(c, n, path, token)
+
+
 def test_largest_tree():
     run_and_check(batch([1024], 50, False, seed=5))
 
