@@ -803,9 +803,13 @@ __global__ void __launch_bounds__(kMergeGroup * kMergeGroups) tree_merge_kernel(
 
 // Cut of a batch's contexts: pages of a piece, and what follows from it.
 struct Plan {
-  int piece, n_long, n_rest;
+  int piece;
+  int64_t n_long, n_rest;
   int64_t parts;  // partial results (units of cut requests)
 };
+// Bounds of a cut; without one a batch has at most kBatch * 1024 units and no partials.
+constexpr int64_t kMaxUnits = int64_t(1) << 29;
+constexpr int64_t kMaxParts = 8192;  // 2.1 GB of workspace; 100 x 131072 rows, 512 query rows each, take 1200
 
 // Time until the last of a batch's units ends, in tile times: n_long units of `piece` pages each and
 // then n_rest of `rest` (their mean), each with a start and end of `unit` tiles, are taken in this
@@ -856,7 +860,8 @@ Plan plan_batch(const int32_t* ctx, const int32_t* indptr, int B, int H, int pai
       double rests = 0.0;
       for (int k = 0; k < kinds; ++k) {
         const Like& g = like[k];
-        const int full = g.tiles / piece, rest = g.tiles - full * piece, units = g.mt * g.count;
+        const int full = g.tiles / piece, rest = g.tiles - full * piece;
+        const int64_t units = (int64_t)g.mt * g.count;
         p.n_long += units * full;
         if (rest) p.n_rest += units;
         rests += (double)units * rest;
@@ -864,7 +869,8 @@ Plan plan_batch(const int32_t* ctx, const int32_t* indptr, int B, int H, int pai
       }
       const double cost = makespan(p.n_long, piece, p.n_rest, p.n_rest ? rests / p.n_rest : 0.0, unit, pairs) +
                           (p.parts ? kMergeCost + kPartCost * (double)p.parts : 0.0);
-      if (cost < best_cost - 1e-9) {
+      if (p.n_long + p.n_rest > kMaxUnits) break;  // shorter pieces make more of them
+      if (p.parts <= kMaxParts && cost < best_cost - 1e-9) {
         best_cost = cost;
         best = p;
       }
@@ -1022,10 +1028,10 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     a.B = std::min(kBatch, B - b0);
     const int32_t *ctx = ctx_host + b0, *indptr = q_indptr_host + b0;
     const Plan p = plan_batch(ctx, indptr, a.B, H, pairs);
-    const int units = p.n_long + p.n_rest;
+    const int units = (int)(p.n_long + p.n_rest);
     if (units == 0) continue;
     a.piece = p.piece;
-    a.n_long = p.n_long;
+    a.n_long = (int)p.n_long;
     int nl = 0, nr = 0, most_pieces = 0;
     int64_t np = 0;
     for (int b = 0; b < a.B; ++b) {

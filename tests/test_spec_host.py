@@ -58,6 +58,14 @@ def test_tree_attention_null_tables(irm):
     assert irm.tree_workspace_size(i32(100), p, 16) >= 256
 
 
+@pytest.mark.parametrize("B,ctx,nodes", [(256, 20_000_000, 1024), (256, 2_000_000_000, 1024), (300, 2_000_000_000, 1),
+                                         (1, 2_000_000_000, 1024), (1, 2_000_000_000, 1)])
+def test_tree_attention_workspace_of_the_largest_batches(irm, B, ctx, nodes):
+    # at most 8192 partials of 128 rows of 512 + 1 fp32, however many pieces and row tiles there are
+    size = irm.tree_workspace_size(np.full(B, ctx), np.arange(B + 1) * nodes, 128)
+    assert 256 <= size <= 256 + 8192 * 128 * 513 * 4 + 512
+
+
 def test_tree_attention_no_nodes_is_no_launch(irm):
     keep, args = tree_args(indptr=(0, 0, 0))
     assert irm.lib().irm_mla_attn_tree(*args) == 0
