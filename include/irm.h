@@ -154,7 +154,8 @@ irm_status irm_validate_chunks(const irm_chunk* chunks_host, const int32_t* indp
 
 /*
  * Reads and clears the device status word of a workspace (synchronizes `stream`).
- * Returns IRM_OK, IRM_ERR_DEVICE_TIMEOUT, IRM_ERR_DEVICE_BOUNDS or IRM_ERR_CUDA.
+ * Returns IRM_OK, IRM_ERR_CUDA, or the first of IRM_ERR_DEVICE_TIMEOUT, IRM_ERR_DEVICE_BOUNDS,
+ * IRM_ERR_SHARED_PAGE and IRM_ERR_OUT_OF_PAGES that was recorded since the last call.
  */
 irm_status irm_device_status(void* workspace, cudaStream_t stream);
 
@@ -309,6 +310,9 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  * b owns nodes [q_indptr_host[b], q_indptr_host[b + 1]), at most IRM_MAX_TREE, possibly none.
  * Host arrays of these calls travel in the launch parameters: the caller may reuse them as
  * soon as the call returns, and a captured graph replays the lengths as they were given.
+ * These calls leave scratch of their own in a workspace and expect none: they may share one, one
+ * after another.  A workspace that they have used is zeroed again before a decode or prefill call
+ * gets it, since those keep counters there.
  */
 
 /*
@@ -327,7 +331,7 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  *           rows are read as zeros
  *   tree_mask device uint32 [T, mask_words], bit k of a row in word k / 32; 32 * mask_words
  *           must cover the largest tree
- *   softmax_scale  finite and positive
+ *   softmax_scale  positive, finite also when multiplied by log2(e)
  *   out     device bf16 [T, H, 512];  lse device fp32 [T, H] or NULL
  * Rows of the last page behind ctx_b + n_b - 1, and rows of drafts that no node of the request
  * sees, may hold anything (NaN included).  A NaN or infinity in any other row may spread to
@@ -377,17 +381,19 @@ irm_status irm_tree_verify(const float* target_probs, const float* draft_probs, 
  * bf16 [n_layers, n_pages, 64, 576]; all layers share one page table.
  *   seq_len    device int32 [n_slots]: rows of each request; request s holds the pages
  *              page_table[s, 0 .. ceil(seq_len[s] / 64) - 1], n_slots <= 8192
- *   page_table device int32 [n_slots, max_pages]; entries given back become -1
+ *   page_table device int32 [n_slots, max_pages], at most 2^30 entries; those given back become -1
  *   refcount   device int32 [n_pages]: requests that hold each page, 0 = free (start with
  *              zeros; a caller may hold pages of its own with counts of its own)
  * All results are independent of scheduling: free pages are handed out lowest first, in
  * request order.
  * A device-side refusal (a status recorded in the workspace, read with irm_device_status) leaves
- * what it concerns as it was:  IRM_ERR_DEVICE_BOUNDS for a length outside [0, 64 max_pages],
- * a page index outside [0, n_pages) or a page released more often than held;
+ * what it concerns as it was:  IRM_ERR_DEVICE_BOUNDS for a request with a length outside [0,
+ * 64 max_pages] or, where it is read to be kept, a page index outside [0, n_pages);
  * IRM_ERR_OUT_OF_PAGES when the free pages do not suffice (then no request of the call grows,
  * or none is forked); IRM_ERR_SHARED_PAGE for a request that would grow while its last,
  * partly filled page is held by others too (fork it instead: a fork has its own copy of it).
+ * A release of an index outside [0, n_pages), or of a page more often than it is held, is recorded
+ * as IRM_ERR_DEVICE_BOUNDS and changes no count; the request's table entry is cleared all the same.
  * Workspace: irm_pages_workspace_size bytes.
  */
 irm_status irm_pages_workspace_size(int n_slots, size_t* bytes);

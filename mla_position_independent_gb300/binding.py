@@ -407,10 +407,20 @@ def _take(t, dtype, shape, name, device):
     return t.data_ptr()
 
 
-def _take_workspace(workspace, nbytes, device):
+def _make(new, device, stream):
+    """new(): tensors that a call makes for itself, allocated (and zeroed) on the stream that the call runs on."""
+    if stream is None:
+        return new()
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
+    with torch.cuda.stream(stream):
+        return new()
+
+
+def _take_workspace(workspace, nbytes, device, stream):
     """(workspace, its address, its bytes); a new one of nbytes() where the caller keeps none."""
     if workspace is None:
-        workspace = new_workspace(nbytes(), device)
+        workspace = _make(lambda: new_workspace(nbytes(), device), device, stream)
     n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
     return workspace, _take(workspace, torch.uint8, (n,), "workspace", device), n
 
@@ -462,10 +472,10 @@ def irm_mla_attn_tree(q_lat, q_rope, ctx, q_indptr, paged_kv, page_table, tree_m
     pt = _take(page_table, torch.int32, (B, max_pages), "page_table", dev)
     tm = _take(tree_mask, torch.int32, (T, words), "tree_mask", dev)
     if out is None:
-        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
+        out = _make(lambda: torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev), dev, stream)
     o = _take(out, torch.bfloat16, (T, H, 512), "out", dev)
     ls = None if lse is None else _take(lse, torch.float32, (T, H), "lse", dev)
-    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: tree_workspace_size(ctx, q_indptr, H), dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: tree_workspace_size(ctx, q_indptr, H), dev, stream)
     if T > 0:
         _launch(lib().irm_mla_attn_tree, dev, stream, ql, qr, B, H, ctx.tobytes(), q_indptr.tobytes(), kv, n_pages, pt, max_pages,
                 tm, words, softmax_scale, o, ls, ws, ws_bytes)
@@ -511,15 +521,16 @@ def irm_tree_verify(target_probs, tokens, parents, uniforms, q_indptr, draft_pro
     if out is None:
         if max_path is None:
             max_path = max(1, int((q_indptr[1:] - q_indptr[:-1]).max())) if B > 1 else max(1, T)
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty((B, max_path), dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev))
+        out = _make(lambda: (torch.empty(B, dtype=torch.int32, device=dev),
+                             torch.empty((B, max_path), dtype=torch.int32, device=dev),
+                             torch.empty(B, dtype=torch.int32, device=dev)), dev, stream)
     n_accept, path, next_token = out
     if max_path is None:
         max_path = path.shape[1]
     na = _take(n_accept, torch.int32, (B,), "n_accept", dev)
     pa = _take(path, torch.int32, (B, max_path), "path", dev)
     nt = _take(next_token, torch.int32, (B,), "next_token", dev)
-    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
     _launch(lib().irm_tree_verify, dev, stream, tp, dp, ld, V, tk, pr, un, q_indptr.tobytes(), B, max_path, na, pa, nt, ws,
             ws_bytes)
     return n_accept, path, next_token, workspace
@@ -556,7 +567,7 @@ def irm_pages_resize(new_len, seq_len, page_table, refcount, workspace=None, str
     seq_len [n_slots], page_table [n_slots, max_pages] and refcount [n_pages] (int32) are updated."""
     dev, n_slots, max_pages, n_pages, sl, pt, rc = _take_pages(seq_len, page_table, refcount)
     nl = _take(new_len, torch.int32, (n_slots,), "new_len", dev)
-    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev, stream)
     _launch(lib().irm_pages_resize, dev, stream, nl, sl, n_slots, pt, max_pages, rc, n_pages, ws, ws_bytes)
     return workspace
 
@@ -569,7 +580,7 @@ def irm_pages_fork(src, dst, kv, seq_len, page_table, refcount, workspace=None, 
         raise ValueError("src and dst must have the same length")
     dev, n_slots, max_pages, n_pages, sl, pt, rc = _take_pages(seq_len, page_table, refcount)
     cache, layers, _ = _take_cache(kv, dev, n_pages)
-    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev, stream)
     _launch(lib().irm_pages_fork, dev, stream, src.tobytes(), dst.tobytes(), len(src), cache, layers, sl, n_slots, pt, max_pages,
             rc, n_pages, ws, ws_bytes)
     return workspace
@@ -585,7 +596,7 @@ def irm_pages_compact(kv, page_table, base, path, n_accept, workspace=None, stre
     ba = _take(base, torch.int32, (n_slots,), "base", dev)
     pa = _take(path, torch.int32, (n_slots, max_path), "path", dev)
     na = _take(n_accept, torch.int32, (n_slots,), "n_accept", dev)
-    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
     _launch(lib().irm_pages_compact, dev, stream, cache, layers, n_pages, pt, max_pages, n_slots, ba, pa, max_path, na, ws,
             ws_bytes)
     return workspace

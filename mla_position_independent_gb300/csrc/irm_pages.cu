@@ -28,6 +28,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSlots = 8192;
 constexpr int kMaxForks = 1024;
+constexpr int64_t kMaxEntries = int64_t(1) << 30;  // of a page table: all requests' pages are counted in int32
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRowVec = kDRow * 2 / 16;        // 16-byte vectors of a row: 72
 constexpr int kPageVec = kRowVec * kPage;      // and of a page: 4608
@@ -413,6 +414,8 @@ irm_status check_workspace(const void* ws, size_t bytes, size_t need) {
 irm_status check_slots(int n_slots, int max_pages, int64_t n_pages) {
   if (n_slots < 1 || n_slots > kMaxSlots) return fail(IRM_ERR_UNSUPPORTED, "n_slots %d outside [1, %d]", n_slots, kMaxSlots);
   if (max_pages < 1 || max_pages > INT32_MAX / kPage) return fail(IRM_ERR_INVALID_ARG, "bad max_pages %d", max_pages);
+  if ((int64_t)n_slots * max_pages > kMaxEntries)
+    return fail(IRM_ERR_UNSUPPORTED, "a page table of %d x %d has more than 2^30 entries", n_slots, max_pages);
   if (n_pages < 1 || n_pages >= (int64_t(1) << 25)) return fail(IRM_ERR_UNSUPPORTED, "n_pages %lld outside [1, 2^25)", (long long)n_pages);
   return IRM_OK;
 }

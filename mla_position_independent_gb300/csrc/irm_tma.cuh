@@ -22,11 +22,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// The same box, into L2 only.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
-}
-
 // Shared-memory matrix descriptor, 64-byte swizzle (layout type 4): rows 64 B apart, 8-row
 // groups `sbo` bytes apart.
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
@@ -47,13 +42,10 @@ __device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, 
                : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
-}
-
-// Bounded waits as mbar_wait / mbar_wait_cluster, for roles whose waits are short and many: the
-// clock is first read after a thousand polls (reading it costs more than the usual wait), so the
-// common wait is the poll alone.  False once kWaitLimitNs has passed or *abort_flag != 0.
+// Bounded waits as mbar_wait / mbar_wait_cluster, but the clock and the flag are first looked at after
+// a thousand polls, so that the common wait is the poll alone (a tile's time is the same with
+// earlier looks, 1.2 us, but a role's code is shorter).  False once kWaitLimitNs has passed or
+// *abort_flag != 0.
 template <bool kCluster>
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
   uint64_t t0 = 0;

@@ -992,7 +992,7 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     return fail(IRM_ERR_INVALID_ARG, "a request of %lld rows needs more than max_pages=%d pages", (long long)rows, max_pages);
   if (mask_words < 1 || (int64_t)mask_words * 32 < nodes)
     return fail(IRM_ERR_INVALID_ARG, "mask_words=%d does not cover %d nodes", mask_words, nodes);
-  if (!std::isfinite(softmax_scale) || softmax_scale <= 0.f)
+  if (!std::isfinite(softmax_scale * 1.4426950408889634f) || softmax_scale <= 0.f)
     return fail(IRM_ERR_INVALID_ARG, "softmax_scale must be finite and positive");
   if ((int64_t)q_indptr_host[B] * H >= INT32_MAX) return fail(IRM_ERR_UNSUPPORTED, "too many query rows");
   if (!q_lat || !q_rope || !paged_kv || !page_table || !tree_mask || !out) return fail(IRM_ERR_INVALID_ARG, "null device pointer");

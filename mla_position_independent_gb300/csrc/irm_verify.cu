@@ -14,16 +14,20 @@
 //
 // Arithmetic.  Sums over the vocabulary decide which token comes out, so they must not depend
 // on the order of addition or on the split: every probability becomes a 44-bit fixed-point
-// integer (resolution 5.7e-14) and sums are 64-bit integers, exact in any order (2^20 entries
-// of 1.0 fit).  fp32 sums would shift the boundaries of a flat 100k-entry row by more than
-// some of its entries are wide; fp64 adds run at ~1/60 of the integer rate here.
+// integer (resolution 5.7e-14) and sums are 64-bit integers, exact in any order (below 2^20
+// entries of 1.0 fit).  fp32 sums would shift the boundaries of a flat 100k-entry row by more
+// than some of its entries are wide; fp64 sums depend on their order in the last bits.
 // The acceptance tests run in fp64 on the fp32 inputs, in the order written above.
 //
-// What bounds it: one row of V fp32 (two with draft probabilities) per request for the final
-// draw, read twice (sum, then locate: the second read is one warp's segment).  A cluster of C CTAs
-// shares a request's row in contiguous warp segments; the CTA totals travel through
-// distributed shared memory.  The children's probabilities are gathered in one round of loads,
-// all nodes at once, before the walk, which then runs in shared memory.
+// What bounds it: latency.  One row of V fp32 (two with draft probabilities) per request is read for
+// the final draw, 0.06 us of memory time at one request of 102400 entries and 3.9 us at 64, but
+// the chain of launch, gather, walk, sum, cluster exchange and locating the token takes 11.1 and
+// 18 us.  So a cluster of C CTAs shares a request's row in contiguous warp segments; the CTA
+// totals travel through distributed shared memory, and what is located is one group of one
+// warp's loads, from group sums kept during the sum.  The children's probabilities are gathered in
+// one round of loads, all nodes at once, before the walk, which then runs in shared memory.
+// With draft probabilities each rejection that another child follows is one more pass over two
+// rows (16 requests, 24 nodes, 102400 entries: 53 us).
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
@@ -377,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
 
 // CTAs a request's vocabulary is spread over: as many as keep the batch on the GPU at once (two CTAs
 // an SM).  Measured, vocabulary 102400: 1 request 20.8 / 17.7 / 11.3 us with 2 / 4 / 8; 64 requests
-// 36.3 / 24.6 / 27.0 us.  A large vocabulary needs enough of them for its groups (of 256 entries).
+// 36.3 / 24.6 / 27.0 us.  A large vocabulary needs enough of them for its groups
+// (of 256 entries at least).
 int cluster_size(int B, int vocab) {
   const int fit = 2 * 152 / B;
   int C = fit >= 8 ? 8 : fit >= 4 ? 4 : fit >= 2 ? 2 : 1;

@@ -290,6 +290,20 @@ def test_copy_more_pairs_than_a_launch_holds():
     assert torch.equal(kv[n:], kv[torch.from_numpy(order).cuda()])
 
 
+def test_a_call_on_another_stream_makes_its_workspace_there():
+    # zeroed behind the current stream's work, the workspace would lose what the call recorded in it
+    c = Cache(2, 4, 8)
+    new = torch.tensor([300, 0], dtype=torch.int32, device="cuda")  # 4 pages hold 256 rows
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    ws = irm.irm_pages_resize(new, c.seq, c.table, c.ref, stream=side)
+    torch.cuda.synchronize()
+    with pytest.raises(irm.IrmError) as e:
+        irm.device_status(ws)
+    assert e.value.status == CODES["bounds"]
+
+
 def test_replayed_graph():
     """A captured step (grow, compact, trim) advances the state at each replay."""
     c = Cache(2, 4, 9, layers=1)

@@ -36,7 +36,7 @@ def tree_args(ctx=(100, 7), indptr=(0, 3, 5), H=16, q_lat=FAKE, kv=FAKE, n_pages
     (dict(H=0), -4), (dict(H=129), -4), (dict(ctx=(-1, 7)), -1), (dict(indptr=(1, 3, 5)), -1),
     (dict(indptr=(0, 3, 2)), -1), (dict(indptr=(0, 1025, 1026), max_pages=100, words=40), -4),
     (dict(max_pages=1), -1), (dict(words=0), -1), (dict(indptr=(0, 33, 40), words=1), -1),
-    (dict(n_pages=0), -4), (dict(n_pages=1 << 25), -4), (dict(scale=float("nan")), -1), (dict(scale=0.0), -1),
+    (dict(n_pages=0), -4), (dict(n_pages=1 << 25), -4), (dict(scale=float("nan")), -1), (dict(scale=0.0), -1), (dict(scale=3e38), -1),
     (dict(q_lat=ctypes.c_void_p((1 << 20) + 8)), -1), (dict(kv=None), -1), (dict(table=ctypes.c_void_p((1 << 20) + 2)), -1),
     (dict(lse=ctypes.c_void_p((1 << 20) + 2)), -1), (dict(ws=None), -8), (dict(ws_bytes=255), -8),
     (dict(ws=ctypes.c_void_p((1 << 21) + 128)), -8), (dict(ctx=(2**31 - 10, 7), max_pages=2**25), -4),
@@ -88,6 +88,7 @@ def test_verify_refusals(irm, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(n_slots=0), -4), (dict(n_slots=8193), -4), (dict(max_pages=0), -1), (dict(n_pages=0), -4), (dict(seq=None), -1),
     (dict(seq=ctypes.c_void_p((1 << 20) + 1)), -1), (dict(ws=None), -8), (dict(ws_bytes=256), -8),
+    (dict(n_slots=8192, max_pages=(1 << 17) + 1), -4),
 ])
 def test_resize_refusals(irm, change, code):
     d = dict(n_slots=4, max_pages=4, n_pages=100, seq=FAKE, ws=WS, ws_bytes=1 << 20)
