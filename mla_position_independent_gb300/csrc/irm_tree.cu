@@ -92,7 +92,7 @@ enum : int {
   BAR_PR_FULL = BAR_X_FREE + 2,      // [2] the peer's rows of P and factors arrived (its live warps + tx)
   BAR_P_FREE = BAR_PR_FULL + 2,      // [2] P V of the buffer done in both CTAs (2)
   BAR_GO = BAR_P_FREE + 2,           // [2] the own rows' P written and O rescaled: live warps
-  BAR_RESC = BAR_GO + 2,             // [2] O rescaled for the peer's rows: live warps
+  BAR_RESC = BAR_GO + 2,             // [2] O rescaled for 32 of the peer's rows (only where a factor is not 1)
   BAR_PV = BAR_RESC + 2,               // P V of a tile done in this CTA
   BAR_MAX = BAR_PV + 1,              // [2] running maximum of 32 own rows published
   BAR_QIN = BAR_MAX + 2,             // Q's TMA bytes (1 + tx)
@@ -251,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(BAR_PR_FULL + s), max(1, live_peer));
       mbar_init(bar(BAR_P_FREE + s), 2);
       mbar_init(bar(BAR_GO + s), max(1, live_own));
-      mbar_init(bar(BAR_RESC + s), max(1, live_peer));
+      mbar_init(bar(BAR_RESC + s), 1);
       mbar_init(bar(BAR_MAX + s), 1);
       mbar_init(bar(BAR_DRAIN + s), 1);
       // the first two tiles' bytes (a barrier that nothing is sent to is not waited for either)
@@ -350,10 +350,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!warp_poll(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
         tc_fence_after();
         rescale_o(tO, corr);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_RESC + (quad & 1)));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_RESC + set));
       return true;
     };
 
@@ -496,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (j >= tail && !(ok = mbar_poll<false>(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
         if (j >= 2 && !(ok = mbar_poll<false>(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
-        fence_proxy_async_smem();  // the cleared rows' plain stores
+        if (j >= tail) fence_proxy_async_smem();  // the cleared rows' plain stores
         const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
         const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(st + 4 * kSlab, 512);
         const uint32_t d = tmem + kTmemS + 64u * (uint32_t)set;
@@ -517,15 +517,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kPvWarp) {
     // ================= P V (one thread) =================
     if (lane == 0) {
+      uint32_t resc = 0;  // parities of the next rescalings of the peer's rows
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
         if (live_own && !(ok = mbar_poll<false>(bar(BAR_GO + set), ph, abort_flag))) break;
         if (live_peer) {
           if (!(ok = mbar_poll<true>(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
-          const volatile int* flag = reinterpret_cast<const volatile int*>(smem + kOffFlag) + 2 * set;
-          const bool moved = flag[0] != 0 || (live_peer > 1 && flag[1] != 0);
-          if (j > 0 && moved && !(ok = mbar_poll<false>(bar(BAR_RESC + set), ph, abort_flag))) break;
+          uint32_t f0, f1;
+          asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(f0), "=r"(f1) : "r"(sb + kOffFlag + 8u * (uint32_t)set) : "memory");
+          // a rescaling waits for P V of the tile before, so these phases are passed one by one
+          const uint32_t moved = j > 0 ? f0 | (live_peer > 1 ? 2u * f1 : 0u) : 0u;
+          if (moved != 0) {
+            if (moved & 1u) ok = mbar_poll<false>(bar(BAR_RESC), resc & 1u, abort_flag);
+            if (ok && moved & 2u) ok = mbar_poll<false>(bar(BAR_RESC + 1), resc >> 1, abort_flag);
+            resc ^= moved;
+            if (!ok) break;
+          }
         }
         tc_fence_after();
         fence_proxy_async_smem();  // P, written by both CTAs' threads
