@@ -42,6 +42,14 @@ __device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, 
                : "memory");
 }
 
+// `bytes` (a multiple of 16) of this CTA's shared memory to a peer's, counted on the peer's mbarrier.
+__device__ __forceinline__ void bulk_to_peer(uint32_t cluster_addr, uint32_t src, uint32_t bytes, uint32_t cluster_bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   cluster_addr),
+               "r"(src), "r"(bytes), "r"(cluster_bar)
+               : "memory");
+}
+
 // Bounded waits as mbar_wait / mbar_wait_cluster, but the clock and the flag are first looked at after
 // a thousand polls, so that the common wait is the poll alone (a tile's time is the same with
 // earlier looks, 1.2 us, but a role's code is shorter).  False once kWaitLimitNs has passed or

@@ -11,10 +11,13 @@
 //     each row is read once by the pair, and 36 KiB a tile leave room for four tiles in flight.
 //     128 rows x 512 fp32 columns of O alone would fill one SM's TMEM.
 //   - The softmax is split by rows: CTA r owns query rows [64 r, 64 r + 64).  Each CTA sends the
-//     other its fp32 partial scores of the other's rows (16 KiB a tile, st.async), adds what it
-//     receives to its own partials, and after the exponentials writes its rows of P into both
-//     CTAs' shared memory (8 KiB a tile).  Nothing is computed twice, and no partial score is
-//     rounded on the way.
+//     other its fp32 partial scores of the other's rows (16 KiB a tile, st.async from registers),
+//     adds what it receives to its own partials, and after the exponentials writes its rows of P
+//     for its own P V and copies them to the other's (8 KiB a tile, one bulk copy a warp: with
+//     st.async of each 16 bytes 64 x 32768 rows took 1115 instead of 988 us.  The scores would
+//     go the same way, but have no 16 KiB to be staged in: with one buffer for both sets, or in the
+//     buffer of P, what is waited for costs more: 1066 and 1146 us).  Nothing is computed twice,
+//     and no partial score is rounded on the way.
 //   - O accumulates in TMEM (256 columns), P V reads P and the page's cKV from shared memory;
 //     Q K^T reads Q's cKV columns from TMEM (128 columns) into one of two score buffers (64 each).
 //   - Two sets of four warps take even and odd tiles, a thread a row: of each set the two warps
@@ -427,11 +430,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i) {
           const uint4 w = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
           const uint32_t off = sw128_offset((uint32_t)m, (uint32_t)i);
-          st_async_v4_b32(remP + off, w, remPfull);
           st_shared_v4(sb + kOffP + buf * kPBytes + off, w);
         }
-        const bool moved = __any_sync(kFull, corr != 1.f);
         st_async_b32(remCorr + (uint32_t)(j & 3) * (kHalf * 4u), __float_as_uint(corr), remPfull);
+        fence_proxy_async_smem();  // P is read by the copy and by the tensor core
+        __syncwarp();
+        if (lane == 0) bulk_to_peer(remP + (uint32_t)quad * 4096u, sb + kOffP + buf * kPBytes + (uint32_t)quad * 4096u, 4096u, remPfull);
+        const bool moved = __any_sync(kFull, corr != 1.f);
         if (lane == 0) st_async_b32(remFlag, moved ? 1u : 0u, remPfull);
         if (j > 0 && moved) {
           if (!(ok = warp_poll(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
@@ -536,7 +541,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_after();
-        fence_proxy_async_smem();  // P, written by both CTAs' threads
         const uint64_t ad = sdesc_sw128(sb + kOffP + (uint32_t)set * kPBytes, 16, 1024);
         const uint64_t bd = sdesc_sw128(sb + kOffKv + (uint32_t)s * kStage, kSlab, 1024);
 #pragma unroll
