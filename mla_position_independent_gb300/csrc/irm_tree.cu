@@ -102,7 +102,8 @@ enum : int {
   BAR_Q = BAR_QIN + 1,               // Q's cKV columns copied to TMEM (8 warps)
   BAR_INV = BAR_Q + 1,               // the peer rows' 1 / l arrived (1 + tx)
   BAR_DRAIN = BAR_INV + 1,           // [2] all UMMAs of an issuer done
-  NUM_BARS = BAR_DRAIN + 2,
+  BAR_X_HALF = BAR_DRAIN + 2,        // [2] the first 32 keys of the partial scores (1 + tx)
+  NUM_BARS = BAR_X_HALF + 2,
 };
 static_assert(NUM_BARS * 8 <= kOffTmem, "barrier area");
 
@@ -250,6 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(BAR_S_FULL + s), 1);
       mbar_init(bar(BAR_S_FREE + s), live_own + live_peer);
       mbar_init(bar(BAR_X_FULL + s), 1);
+      mbar_init(bar(BAR_X_HALF + s), 1);
       mbar_init(bar(BAR_X_FREE + s), max(1, live_peer));
       mbar_init(bar(BAR_PR_FULL + s), max(1, live_peer));
       mbar_init(bar(BAR_P_FREE + s), 2);
@@ -258,7 +260,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(BAR_MAX + s), 1);
       mbar_init(bar(BAR_DRAIN + s), 1);
       // the first two tiles' bytes (a barrier that nothing is sent to is not waited for either)
-      if (live_own) mbar_arrive_expect_tx(bar(BAR_X_FULL + s), (uint32_t)live_own * (kXBytes / 2));
+      if (live_own) {
+        mbar_arrive_expect_tx(bar(BAR_X_FULL + s), (uint32_t)live_own * (kXBytes / 4));
+        mbar_arrive_expect_tx(bar(BAR_X_HALF + s), (uint32_t)live_own * (kXBytes / 4));
+      }
       for (int k = 0; k < live_peer; ++k) mbar_arrive_expect_tx(bar(BAR_PR_FULL + s), kPrBytes);
     }
     mbar_init(bar(BAR_PV), 1);
@@ -330,6 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t buf = (uint32_t)set;  // a set's tiles all use the buffers of its number
     const uint32_t remX = mapa_shared(sb + kOffX + buf * kXBytes, peer);
     const uint32_t remXfull = mapa_shared(bar(BAR_X_FULL + set), peer);
+    const uint32_t remXhalf = mapa_shared(bar(BAR_X_HALF + set), peer);
     const uint32_t remXfree = mapa_shared(bar(BAR_X_FREE + set), peer);
     const uint32_t remP = mapa_shared(sb + kOffP + buf * kPBytes, peer);
     const uint32_t remPfull = mapa_shared(bar(BAR_PR_FULL + set), peer);
@@ -364,21 +370,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (; live && ok && j < ntiles; j += 2) {  // warps without valid rows have no part in it
       const uint32_t ph = (uint32_t)(j >> 1) & 1u;
       uint32_t s[64];
+      if (!own && j >= 2 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
       if (!(ok = warp_poll(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-      tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
       tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
       if (own) {
+        tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
         float corr = 1.f;
         // ================= softmax of a row =================
-        if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
         float v[64];
+        if (!(ok = warp_poll_cluster(bar(BAR_X_HALF + set), ph, abort_flag))) break;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = X[i * kHalf + mh];
+          v[4 * i] = __uint_as_float(s[4 * i]) + __uint_as_float(x.x);
+          v[4 * i + 1] = __uint_as_float(s[4 * i + 1]) + __uint_as_float(x.y);
+          v[4 * i + 2] = __uint_as_float(s[4 * i + 2]) + __uint_as_float(x.z);
+          v[4 * i + 3] = __uint_as_float(s[4 * i + 3]) + __uint_as_float(x.w);
+        }
+        if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
+#pragma unroll
+        for (int i = 8; i < 16; ++i) {
           const uint4 x = X[i * kHalf + mh];
           v[4 * i] = __uint_as_float(s[4 * i]) + __uint_as_float(x.x);
           v[4 * i + 1] = __uint_as_float(s[4 * i + 1]) + __uint_as_float(x.y);
@@ -387,7 +404,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          if (first_quad && j + 2 < ntiles) mbar_arrive_expect_tx(bar(BAR_X_FULL + set), (uint32_t)live_own * (kXBytes / 2));
+          if (first_quad && j + 2 < ntiles) {
+            mbar_arrive_expect_tx(bar(BAR_X_FULL + set), (uint32_t)live_own * (kXBytes / 4));
+            mbar_arrive_expect_tx(bar(BAR_X_HALF + set), (uint32_t)live_own * (kXBytes / 4));
+          }
           mbar_arrive_remote_relaxed(remXfree);  // the values are in registers
         }
         if (j >= tail) {
@@ -448,9 +468,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
-        if (j >= 2 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
+        tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i)
+          st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
+                          remXhalf);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
+#pragma unroll
+        for (int i = 8; i < 16; ++i)
           st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
                           remXfull);
         if (j >= 2 && !(ok = take_factors(j - 2))) break;
