@@ -86,7 +86,7 @@ static_assert(kSmem <= 232448, "shared memory");
 
 enum : int {
   BAR_LANDED = 0,                    // [stage] TMA bytes of the page (1 + tx)
-  BAR_CLEAR = BAR_LANDED + kStages,  // [stage] unseen rows cleared (pages with drafts only)
+  BAR_CLEAR = BAR_LANDED + kStages,  // [stage] unseen rows cleared for P V (pages with drafts only)
   BAR_FREE = BAR_CLEAR + kStages,    // [stage] P V of the page done, and the clearing warp past it (2)
   BAR_S_FULL = BAR_FREE + kStages,   // [2] Q K^T done
   BAR_S_FREE = BAR_S_FULL + 2,       // [2] the set's live warps read the score buffer
@@ -370,6 +370,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (; live && ok && j < ntiles; j += 2) {  // warps without valid rows have no part in it
       const uint32_t ph = (uint32_t)(j >> 1) & 1u;
       uint32_t s[64];
+      uint64_t see = 0;  // read before the waits
+      if (own && j >= tail && valid) see = seen_rows(mask, a.mask_words, (kb + j) * kPage, ctx, n);
       if (!own && j >= 2 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
       if (!(ok = warp_poll(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
@@ -411,7 +413,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive_remote_relaxed(remXfree);  // the values are in registers
         }
         if (j >= tail) {
-          const uint64_t see = valid ? seen_rows(mask, a.mask_words, (kb + j) * kPage, ctx, n) : 0ull;
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (!(see >> i & 1)) v[i] = -INFINITY;
@@ -526,10 +527,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
         if (!(ok = mbar_poll<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
-        if (j >= tail && !(ok = mbar_poll<false>(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
         if (j >= 2 && !(ok = mbar_poll<false>(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
-        if (j >= tail) fence_proxy_async_smem();  // the cleared rows' plain stores
         const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
         const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(st + 4 * kSlab, 512);
         const uint32_t d = tmem + kTmemS + 64u * (uint32_t)set;
@@ -554,6 +553,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+        if (j >= tail) {
+          if (!(ok = mbar_poll<false>(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
+          fence_proxy_async_smem();  // the cleared rows' plain stores
+        }
         if (live_own && !(ok = mbar_poll<false>(bar(BAR_GO + set), ph, abort_flag))) break;
         if (live_peer) {
           if (!(ok = mbar_poll<true>(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
@@ -613,10 +616,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (j >= tail) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        for (uint64_t gone = ~((uint64_t)hi << 32 | lo); gone != 0; gone &= gone - 1) {
-          const uint32_t r = (uint32_t)__ffsll((long long)gone) - 1u;
-          st_shared_v4(st + (uint32_t)(lane >> 3) * kSlab + sw128_offset(r, (uint32_t)lane & 7u), zero);
-          if (lane < 4) st_shared_v4(st + 4 * kSlab + sw64_offset(r, (uint32_t)lane), zero);
+        const uint64_t gone = ~((uint64_t)hi << 32 | lo);
+#pragma unroll 8
+        for (uint32_t r = 0; r < 64; ++r) {
+          if (gone >> r & 1) st_shared_v4(st + (uint32_t)(lane >> 3) * kSlab + sw128_offset(r, (uint32_t)lane & 7u), zero);
         }
         fence_proxy_async_smem();
         __syncwarp();
