@@ -8,16 +8,13 @@
 // of CTAs (a cluster of 2, one CTA per SM); a page (64 rows) is one tile.
 //   - The contraction of Q K^T and the columns of O are split over the pair: CTA r loads, with
 //     TMA, cKV columns [256 r, 256 r + 256) and k_r columns [32 r, 32 r + 32) of each page, so
-//     each row is read once by the pair, and 36 KiB a tile leave room for four tiles in flight.
+//     each row is read once by the pair, and 32 KiB a tile leave room for five tiles in flight.
 //     128 rows x 512 fp32 columns of O alone would fill one SM's TMEM.
 //   - The softmax is split by rows: CTA r owns query rows [64 r, 64 r + 64).  Each CTA sends the
 //     other its fp32 partial scores of the other's rows (16 KiB a tile, st.async from registers),
 //     adds what it receives to its own partials, and after the exponentials writes its rows of P
-//     for its own P V and copies them to the other's (8 KiB a tile, one bulk copy a warp: with
-//     st.async of each 16 bytes 64 x 32768 rows took 1115 instead of 988 us.  The scores would
-//     go the same way, but have no 16 KiB to be staged in: with one buffer for both sets, or in the
-//     buffer of P, what is waited for costs more: 1066 and 1146 us).  Nothing is computed twice,
-//     and no partial score is rounded on the way.
+//     for its own P V and copies them to the other's (8 KiB a tile, one bulk copy a warp).
+//     Nothing is computed twice, and no partial score is rounded on the way.
 //   - O accumulates in TMEM (256 columns), P V reads P and the page's cKV from shared memory;
 //     Q K^T reads Q's cKV columns from TMEM (128 columns) into one of two score buffers (64 each).
 //   - Two sets of four warps take even and odd tiles, a thread a row: of each set the two warps
@@ -28,12 +25,32 @@
 //     the same maximum, so the result is exact); then the owner's factor per row, which travels
 //     with P, rescales O in both CTAs.  l is summed in fp32 before P is rounded to bf16 for
 //     the tensor cores (the rounding of P, half a step of bf16 a key, is of the output's own size).
-//   - Rows that no node of the unit sees (masked drafts, rows behind the last one) may hold NaN:
-//     a warp clears them in shared memory before the page is used.
-// Warps: 0-7 scores, 8 TMA, 9 Q K^T issue and TMEM, 10 P V issue, 11 the clearing.
+//   - Rows that no node of the unit sees (masked drafts, rows behind the last one) may hold NaN.
+//     Their scores are replaced whatever they are; a warp clears their cKV columns in shared memory,
+//     beside Q K^T, before P V reads them.
+// Warps: 0-7 scores, 8 TMA, 9 Q K^T issue and TMEM, 10 P V issue, 11 Q and the clearing.
 // Long contexts are cut into pieces of equal length (the rest last, so that the short ones fill the
 // gaps); their normalised fp32 partials are merged by a second kernel.
 // Every wait is bounded (2 s) and reports a timeout in the status word.
+//
+// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 855 us, 1.34 PFLOP/s, 0.70 of the
+// measured bf16 rate (1.40 of the floor, 608 us); in the units' own time a tile takes 0.92 us,
+// 1700 cycles.  Two limits are near it:
+//   - Issue of MMAs: at N = 64 one takes 44.5 cycles, not 32, so that Q K^T (18) and P V (4 of 128
+//     cycles) keep the tensor core for 1313 cycles a tile.  N = 128 runs at the full rate, but two
+//     pages at once start both sets at once: 1066 us.
+//   - The tiles in flight: a page is held from its TMA until its P V, ~8000 cycles, a fifth of which
+//     is the exchange of scores (with an eighth of the bytes, and wrong results, a tile takes an eighth less
+//     time).  With four pages in flight 975 us, although the received scores then have a
+//     buffer for each set.  So everything else makes room for the fifth: one buffer for received
+//     scores (their senders keep them in registers until it is free), k_r in a ring of two.
+// Measured and not taken (64 x 32768, when the kernel stood at the first figure): P by st.async of
+// 16 bytes 1115 (988 with bulk copies); scores by bulk copies 1049 (991); by plain remote stores and a
+// release 1193 (988); tiles of 32 rows, four sets 1381 (988); pages of 64 rows with four sets of 32
+// keys 1010 (988); softmax split by keys 1.09 times the time; a second warp for each row 1.18 times.
+// Few rows (16 heads, one node; 76 x 8000) stream pages at 0.88 us a tile and pair, 6.3 TB/s, 0.93 of
+// the measured copy rate.  One short request (512 rows, 16 heads) takes 12.1 us, three dependent
+// launch-to-end latencies: set-up ~2, unit ~6, merge ~3.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -60,28 +77,31 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Shared memory: barriers and small arrays, then 1024-byte aligned tiles.
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr uint32_t kSlab = 64 * 128;                  // 64 rows x 64 columns
-constexpr uint32_t kStage = 4 * kSlab + 64 * 64;      // + 64 rows x 32 k_r columns
+constexpr uint32_t kStage = 4 * kSlab;                // the cKV columns of a page
+constexpr uint32_t kRing = kStages * kSlab;           // pages in turn, for each 64 columns
+constexpr uint32_t kKr = 64 * 64;                     // and its 32 k_r columns, which only Q K^T needs
 constexpr uint32_t kXBytes = kHalf * kPage * 4;       // received scores of one tile
 constexpr uint32_t kPBytes = kBM * 128;               // P of one tile
 constexpr uint32_t kOffBars = 0;
 constexpr uint32_t kOffTmem = 384;
 constexpr uint32_t kOffAbort = 388;
+constexpr uint32_t kOffFlag = 400;                    // int [2 sets][2 warps]: some factor is not 1
 constexpr uint32_t kOffMax = 512;                     // float [64]: running maximum of the own rows
 constexpr uint32_t kOffCorr = kOffMax + 64 * 4;       // float [4 tiles][64]: the peer rows' factors
-constexpr uint32_t kOffFlag = 400;                    // int [2 sets][2 warps]: some factor is not 1
-constexpr uint32_t kOffSum = kOffCorr + 4 * 64 * 4;   // float2 [2][64]: (maximum, sum) of each set
-constexpr uint32_t kOffInv = kOffSum + 2 * 64 * 8;    // float [128]: 1 / l of every row
 constexpr uint32_t kPrBytes = kPBytes / 4 + 128 + 4;  // what a warp sends of P: 32 rows, factors, flag
-constexpr uint32_t kOffQr = 4096;                     // 128 rows x 64 B (swizzled)
-constexpr uint32_t kOffX = kOffQr + 128 * 64;         // [2] 16-byte words [16][64 rows]
-constexpr uint32_t kOffP = kOffX + 2 * kXBytes;
+constexpr uint32_t kOffQr = 2048;                     // 128 rows x 64 B (swizzled)
+constexpr uint32_t kOffSum = kOffQr;                  // at the end: float2 [2][64], (maximum, sum) of each set
+constexpr uint32_t kOffInv = kOffSum + 2 * 64 * 8;    // and float [128], 1 / l of every row
+constexpr uint32_t kOffX = kOffQr + 128 * 64;         // 16-byte words [16][64 rows]
+constexpr uint32_t kOffKr = kOffX + kXBytes;          // [2]
+constexpr uint32_t kOffP = kOffKr + 2 * kKr;
 constexpr uint32_t kOffKv = kOffP + 2 * kPBytes;
-constexpr uint32_t kOffQl = kOffKv + 2 * kStage;      // 4 slabs of Q's cKV columns at the start, in stages 2 and 3
+constexpr uint32_t kOffQl = kOffKv + 2 * kSlab;       // 4 slabs of Q's cKV columns at the start, in stages 2 and 3
 constexpr uint32_t kSmem = kOffKv + kStages * kStage + 1024;  // room to align the base
-static_assert(4 * kBM * 128 <= 2 * kStage && kStages == 4, "Q's place");
-static_assert(kOffInv + 128 * 4 <= kOffQr && kOffQr % 1024 == 0 && kOffX % 1024 == 0 && kOffKv % 1024 == 0, "layout");
+static_assert(kBM * 128 <= 2 * kSlab && kStages >= 4, "Q's place");
+static_assert(kOffCorr + 4 * 64 * 4 <= kOffQr && kOffQr % 1024 == 0 && kOffKr % 1024 == 0 && kOffP % 1024 == 0, "layout");
 static_assert(kSmem <= 232448, "shared memory");
 
 enum : int {
@@ -90,9 +110,9 @@ enum : int {
   BAR_FREE = BAR_CLEAR + kStages,    // [stage] P V of the page done, and the clearing warp past it (2)
   BAR_S_FULL = BAR_FREE + kStages,   // [2] Q K^T done
   BAR_S_FREE = BAR_S_FULL + 2,       // [2] the set's live warps read the score buffer
-  BAR_X_FULL = BAR_S_FREE + 2,       // [2] the peer's partial scores arrived (1 + tx)
-  BAR_X_FREE = BAR_X_FULL + 2,       // [2] the peer's warps have read what was sent
-  BAR_PR_FULL = BAR_X_FREE + 2,      // [2] the peer's rows of P and factors arrived (its live warps + tx)
+  BAR_X_FULL = BAR_S_FREE + 2,       // [2][32 rows] the peer's partial scores arrived, keys 32 to 63 (1 + tx)
+  BAR_X_FREE = BAR_X_FULL + 4,       // [2][32 rows] the peer's warp has read what was sent
+  BAR_PR_FULL = BAR_X_FREE + 4,      // [2] the peer's rows of P and factors arrived (its live warps + tx)
   BAR_P_FREE = BAR_PR_FULL + 2,      // [2] P V of the buffer done in both CTAs (2)
   BAR_GO = BAR_P_FREE + 2,           // [2] the own rows' P written and O rescaled: live warps
   BAR_RESC = BAR_GO + 2,             // [2] O rescaled for 32 of the peer's rows (only where a factor is not 1)
@@ -102,8 +122,8 @@ enum : int {
   BAR_Q = BAR_QIN + 1,               // Q's cKV columns copied to TMEM (8 warps)
   BAR_INV = BAR_Q + 1,               // the peer rows' 1 / l arrived (1 + tx)
   BAR_DRAIN = BAR_INV + 1,           // [2] all UMMAs of an issuer done
-  BAR_X_HALF = BAR_DRAIN + 2,        // [2] the first 32 keys of the partial scores (1 + tx)
-  NUM_BARS = BAR_X_HALF + 2,
+  BAR_X_HALF = BAR_DRAIN + 2,        // [2][32 rows] the peer's partial scores, keys 0 to 31 (1 + tx)
+  NUM_BARS = BAR_X_HALF + 4,
 };
 static_assert(NUM_BARS * 8 <= kOffTmem, "barrier area");
 
@@ -250,9 +270,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(BAR_S_FULL + s), 1);
       mbar_init(bar(BAR_S_FREE + s), live_own + live_peer);
-      mbar_init(bar(BAR_X_FULL + s), 1);
-      mbar_init(bar(BAR_X_HALF + s), 1);
-      mbar_init(bar(BAR_X_FREE + s), max(1, live_peer));
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(BAR_X_FULL + 2 * s + h), 1);
+        mbar_init(bar(BAR_X_HALF + 2 * s + h), 1);
+        mbar_init(bar(BAR_X_FREE + 2 * s + h), 1);
+      }
       mbar_init(bar(BAR_PR_FULL + s), max(1, live_peer));
       mbar_init(bar(BAR_P_FREE + s), 2);
       mbar_init(bar(BAR_GO + s), max(1, live_own));
@@ -260,9 +282,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(BAR_MAX + s), 1);
       mbar_init(bar(BAR_DRAIN + s), 1);
       // the first two tiles' bytes (a barrier that nothing is sent to is not waited for either)
-      if (live_own) {
-        mbar_arrive_expect_tx(bar(BAR_X_FULL + s), (uint32_t)live_own * (kXBytes / 4));
-        mbar_arrive_expect_tx(bar(BAR_X_HALF + s), (uint32_t)live_own * (kXBytes / 4));
+      for (int h = 0; h < live_own; ++h) {
+        mbar_arrive_expect_tx(bar(BAR_X_FULL + 2 * s + h), kXBytes / 4);
+        mbar_arrive_expect_tx(bar(BAR_X_HALF + 2 * s + h), kXBytes / 4);
       }
       for (int k = 0; k < live_peer; ++k) mbar_arrive_expect_tx(bar(BAR_PR_FULL + s), kPrBytes);
     }
@@ -297,6 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_arrive();  // every warp waits for it before its first remote access, or at its end
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
   bool ok = true;
+  float2 state = make_float2(-INFINITY, 0.f);  // of the own rows' warps: maximum and sum of their tiles
 
   if (warp < kScoreWarps) {
     const int set = warp >> 2, quad = warp & 3;
@@ -317,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffQl + slab * (kBM * 128) + sw128_offset((uint32_t)m, (uint32_t)i));
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffQl + slab * kRing + sw128_offset((uint32_t)m, (uint32_t)i));
           r[4 * i] = v.x;
           r[4 * i + 1] = v.y;
           r[4 * i + 2] = v.z;
@@ -333,19 +356,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_wait();
     const uint32_t buf = (uint32_t)set;  // a set's tiles all use the buffers of its number
-    const uint32_t remX = mapa_shared(sb + kOffX + buf * kXBytes, peer);
-    const uint32_t remXfull = mapa_shared(bar(BAR_X_FULL + set), peer);
-    const uint32_t remXhalf = mapa_shared(bar(BAR_X_HALF + set), peer);
-    const uint32_t remXfree = mapa_shared(bar(BAR_X_FREE + set), peer);
+    const uint32_t remX = mapa_shared(sb + kOffX, peer);
+    const int xq = 2 * set + (quad & 1);
+    const uint32_t remXfull = mapa_shared(bar(BAR_X_FULL + xq), peer);
+    const uint32_t remXhalf = mapa_shared(bar(BAR_X_HALF + xq), peer);
+    const uint32_t remXfree = mapa_shared(bar(BAR_X_FREE + xq), peer);
     const uint32_t remP = mapa_shared(sb + kOffP + buf * kPBytes, peer);
     const uint32_t remPfull = mapa_shared(bar(BAR_PR_FULL + set), peer);
     const uint32_t remCorr = mapa_shared(sb + kOffCorr + 4u * (uint32_t)mh, peer);
     const uint32_t remFlag = mapa_shared(sb + kOffFlag + 8u * buf + 4u * (uint32_t)(quad & 1), peer);
-    const uint4* X = reinterpret_cast<const uint4*>(smem + kOffX + buf * kXBytes);
+    const uint4* X = reinterpret_cast<const uint4*>(smem + kOffX);
     float* max_sh = reinterpret_cast<float*>(smem + kOffMax);
     const float* corr_sh = reinterpret_cast<const float*>(smem + kOffCorr);
     const uint32_t* mask = a.mask + (int64_t)(first_node + (row0 + (valid ? m : 0)) / a.H) * a.mask_words;
-    const bool first_quad = (quad & 1) == 0;  // arms the byte counts
     float m_l = -INFINITY, l = 0.f;           // this set's sum, relative to m_l
 
     // The factors of the peer's rows at tile t, after its P has arrived.  A sender looks at them one
@@ -372,7 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t s[64];
       uint64_t see = 0;  // read before the waits
       if (own && j >= tail && valid) see = seen_rows(mask, a.mask_words, (kb + j) * kPage, ctx, n);
-      if (!own && j >= 2 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + set), ph ^ 1u, abort_flag))) break;
       if (!(ok = warp_poll(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
@@ -386,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float corr = 1.f;
         // ================= softmax of a row =================
         float v[64];
-        if (!(ok = warp_poll_cluster(bar(BAR_X_HALF + set), ph, abort_flag))) break;
+        if (!(ok = warp_poll_cluster(bar(BAR_X_HALF + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint4 x = X[i * kHalf + mh];
@@ -395,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           v[4 * i + 2] = __uint_as_float(s[4 * i + 2]) + __uint_as_float(x.z);
           v[4 * i + 3] = __uint_as_float(s[4 * i + 3]) + __uint_as_float(x.w);
         }
-        if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + set), ph, abort_flag))) break;
+        if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 8; i < 16; ++i) {
           const uint4 x = X[i * kHalf + mh];
@@ -406,9 +428,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          if (first_quad && j + 2 < ntiles) {
-            mbar_arrive_expect_tx(bar(BAR_X_FULL + set), (uint32_t)live_own * (kXBytes / 4));
-            mbar_arrive_expect_tx(bar(BAR_X_HALF + set), (uint32_t)live_own * (kXBytes / 4));
+          if (j + 2 < ntiles) {
+            mbar_arrive_expect_tx(bar(BAR_X_FULL + xq), kXBytes / 4);
+            mbar_arrive_expect_tx(bar(BAR_X_HALF + xq), kXBytes / 4);
           }
           mbar_arrive_remote_relaxed(remXfree);  // the values are in registers
         }
@@ -470,23 +492,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         // ================= partial scores of the peer's rows =================
         tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
-                          remXhalf);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
+        if (j >= 1 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + (xq ^ 2)), (uint32_t)((j - 1) >> 1) & 1u, abort_flag))) break;
 #pragma unroll
-        for (int i = 8; i < 16; ++i)
+        for (int i = 0; i < 16; ++i)
           st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
-                          remXfull);
+                          i < 8 ? remXhalf : remXfull);
         if (j >= 2 && !(ok = take_factors(j - 2))) break;
       }
     }
     if (ok && live && !own && j > set) ok = take_factors(j - 2);
-    if (own) reinterpret_cast<float2*>(smem + kOffSum)[set * kHalf + mh] = make_float2(m_l, l);
+    if (own) state = make_float2(m_l, l);
   } else if (warp == kTmaWarp) {
     // ================= pages in =================
     int page = 0, sent = 0;
@@ -504,13 +523,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (j == 2 && !(ok = warp_poll(bar(BAR_Q), 0, abort_flag))) break;
       if (j >= kStages && !(ok = warp_poll(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) {
-        const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
-        mbar_arrive_expect_tx(bar(BAR_LANDED + s), kStage);
+        const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
+        mbar_arrive_expect_tx(bar(BAR_LANDED + s), kStage + kKr);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tma_load_2d(st + c * kSlab, &a.map_lat, 256 * rank + 64 * c, y, bar(BAR_LANDED + s));
-        tma_load_2d(st + 4 * kSlab, &a.map_rope, kDLat + 32 * rank, y, bar(BAR_LANDED + s));
+        for (int c = 0; c < 4; ++c) tma_load_2d(st + c * kRing, &a.map_lat, 256 * rank + 64 * c, y, bar(BAR_LANDED + s));
       }
       sent = j + 1;
+      // the k_r buffer's last page has been through Q K^T
+      if (j >= 2 && !(ok = warp_poll(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+      if (lane == 0) tma_load_2d(sb + kOffKr + (uint32_t)(j & 1) * kKr, &a.map_rope, kDLat + 32 * rank, y, bar(BAR_LANDED + s));
     }
     // the copies in flight land before the CTA ends, whatever became of the others
     ok = warp_poll(bar(BAR_QIN), 0, nullptr) && ok;
@@ -529,14 +550,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_poll<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
         if (j >= 2 && !(ok = mbar_poll<false>(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
-        const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
-        const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(st + 4 * kSlab, 512);
+        const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
+        const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(sb + kOffKr + (uint32_t)set * kKr, 512);
         const uint32_t d = tmem + kTmemS + 64u * (uint32_t)set;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, sdesc_add(bd, c * kSlab + kk * 32), kIdescS, (c | kk) ? 1u : 0u);
+            umma_bf16_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, sdesc_add(bd, c * kRing + kk * 32), kIdescS, (c | kk) ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) umma_bf16(d, sdesc_add(aq, kk * 32), sdesc_add(bk, kk * 32), kIdescS, 1u);
         umma_commit(bar(BAR_S_FULL + set));
@@ -573,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint64_t ad = sdesc_sw128(sb + kOffP + (uint32_t)set * kPBytes, 16, 1024);
-        const uint64_t bd = sdesc_sw128(sb + kOffKv + (uint32_t)s * kStage, kSlab, 1024);
+        const uint64_t bd = sdesc_sw128(sb + kOffKv + (uint32_t)s * kSlab, kRing, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16(tmem + kTmemO, sdesc_add(ad, kk * 32), sdesc_add(bd, kk * 2048), kIdescPV, (j | kk) ? 1u : 0u);
@@ -595,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int y = (int)grow0 + 32 * q;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          tma_load_2d(sb + kOffQl + c * (kBM * 128) + q * 4096, &a.map_ql, 256 * rank + 64 * c, y, bar(BAR_QIN));
+          tma_load_2d(sb + kOffQl + c * kRing + q * 4096, &a.map_ql, 256 * rank + 64 * c, y, bar(BAR_QIN));
         tma_load_2d(sb + kOffQr + q * 2048, &a.map_qr, 32 * rank, y, bar(BAR_QIN));
       }
     }
@@ -614,12 +635,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!(ok = warp_poll(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
       if (j >= tail) {
-        const uint32_t st = sb + kOffKv + (uint32_t)s * kStage;
+        const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         const uint64_t gone = ~((uint64_t)hi << 32 | lo);
 #pragma unroll 8
         for (uint32_t r = 0; r < 64; ++r) {
-          if (gone >> r & 1) st_shared_v4(st + (uint32_t)(lane >> 3) * kSlab + sw128_offset(r, (uint32_t)lane & 7u), zero);
+          if (gone >> r & 1) st_shared_v4(st + (uint32_t)(lane >> 3) * kRing + sw128_offset(r, (uint32_t)lane & 7u), zero);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -639,6 +660,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (warp < kScoreWarps && (warp >> 1 & 1) == rank)
+    reinterpret_cast<float2*>(smem + kOffSum)[(warp >> 2) * kHalf + (warp & 1) * 32 + lane] = state;
+  __syncthreads();
   const bool split = pieces > 1;
   if (split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for the rest of it
   const int64_t part = split ? (int64_t)req.part_base + (int64_t)mtile * pieces + piece : 0;
@@ -871,10 +895,11 @@ double makespan(int64_t n_long, double piece, int64_t n_rest, double rest, doubl
   return from + std::ceil((double)left / pairs) * tr;
 }
 
-// The cut with the least estimated time.  In tile times, measured: a unit's start and end take ~8 (12
-// where units have at most 64 rows and a tile takes ~0.9 instead of ~1.2 us), a cut batch's merge 5
-// and a tenth for each partial.  With 8 for few rows a batch of 8 x 8192, 16 heads, one node, got
-// 80 units for the 76 pairs: 32.2 against 25.4 us.
+// The cut with the least estimated time.  In tile times, measured: a unit's start and end take ~10 (12
+// where units have at most 64 rows), a cut batch's merge 5 and a tenth for each partial.  With 8 for
+// many rows 23 x 5000 ragged rows, 13 nodes of 24 heads, take 33.4 instead of 31.8 us; with a
+// twentieth for a partial 16 x 2000, 5 nodes of 32 heads, 22.7 instead of 19.1 us; with 6 and 0.15 for
+// the merge 4 x 1000, 4 nodes of 128 heads, is not cut: 24.6 instead of 19.3 us.
 constexpr double kMergeCost = 5.0, kPartCost = 0.1;
 Plan plan_batch(const int32_t* ctx, const int32_t* indptr, int B, int H, int pairs) {
   struct Like {
@@ -893,7 +918,7 @@ Plan plan_batch(const int32_t* ctx, const int32_t* indptr, int B, int H, int pai
   double best_cost = 1e300;
   // pieces from the longest context down, by steps of a few percent (fewer steps where every
   // request is of another length)
-  const double unit = rows <= kHalf ? 12.0 : 8.0;
+  const double unit = rows <= kHalf ? 12.0 : 10.0;
   const double step = kinds <= 8 ? 0.97 : 0.88;
   int last = 0;
   for (double f = 1.0;; f *= step) {
