@@ -33,9 +33,9 @@
 // gaps); their normalised fp32 partials are merged by a second kernel.
 // Every wait is bounded (2 s) and reports a timeout in the status word.
 //
-// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 855 us, 1.34 PFLOP/s, 0.70 of the
-// measured bf16 rate (1.40 of the floor, 608 us); in the units' own time a tile takes 0.92 us,
-// 1700 cycles.  Two limits are near it:
+// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 855 us, 1.37 PFLOP/s, 0.71 of the
+// measured bf16 rate; in the units' own time a tile takes 0.92 us, ~1750 cycles.  Two limits are
+// near it:
 //   - Issue of MMAs: at N = 64 one takes 44.5 cycles, not 32, so that Q K^T (18) and P V (4 of 128
 //     cycles) keep the tensor core for 1313 cycles a tile.  N = 128 runs at the full rate, but two
 //     pages at once start both sets at once: 1066 us.
@@ -48,9 +48,9 @@
 // 16 bytes 1115 (988 with bulk copies); scores by bulk copies 1049 (991); by plain remote stores and a
 // release 1193 (988); tiles of 32 rows, four sets 1381 (988); pages of 64 rows with four sets of 32
 // keys 1010 (988); softmax split by keys 1.09 times the time; a second warp for each row 1.18 times.
-// Few rows (16 heads, one node; 76 x 8000) stream pages at 0.88 us a tile and pair, 6.3 TB/s, 0.93 of
-// the measured copy rate.  One short request (512 rows, 16 heads) takes 12.1 us, three dependent
-// launch-to-end latencies: set-up ~2, unit ~6, merge ~3.
+// Few rows (16 heads, one node, 76 requests) stream 0.89 us a further page, 6.3 TB/s, 0.93 of the
+// measured copy rate.  One short request (512 rows, 16 heads) takes 12.1 us, of which one tile alone
+// (63 rows) is 9.4: it is set-up, the chain of one tile and the way out.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -976,11 +976,11 @@ irm_status check_lengths(const int32_t* ctx, const int32_t* indptr, int B, int H
   return IRM_OK;
 }
 
-// Scratch of the largest launch (the launches follow one another on the stream).
-size_t scratch_bytes(const int32_t* ctx, const int32_t* indptr, int B, int H) {
-  const int pairs = sm_pairs();
-  int64_t parts = 0;
-  for (int b0 = 0; b0 < B; b0 += kBatch)
+// Scratch of the largest launch (the launches follow one another on the stream), and the first one's plan.
+size_t scratch_bytes(const int32_t* ctx, const int32_t* indptr, int B, int H, int pairs, Plan* first) {
+  *first = plan_batch(ctx, indptr, std::min(kBatch, B), H, pairs);
+  int64_t parts = first->parts;
+  for (int b0 = kBatch; b0 < B; b0 += kBatch)
     parts = std::max(parts, plan_batch(ctx + b0, indptr + b0, std::min(kBatch, B - b0), H, pairs).parts);
   return opart_bytes(parts) + lsepart_bytes(parts);
 }
@@ -1040,7 +1040,8 @@ irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32
   int64_t rows = 0;
   const irm_status st = check_lengths(ctx_host, q_indptr_host, B, H, &nodes, &rows);
   if (st != IRM_OK) return st;
-  *bytes = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H);
+  Plan first;
+  *bytes = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H, sm_pairs(), &first);
   return IRM_OK;
 }
 
@@ -1069,7 +1070,8 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
   if (!aligned(page_table, 4) || !aligned(tree_mask, 4) || !aligned(lse, 4))
     return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
   const int pairs = sm_pairs();
-  const size_t need = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H);
+  Plan first;
+  const size_t need = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H, pairs, &first);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
     return fail(IRM_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %zu bytes (got %zu)", need, workspace_bytes);
   if (q_indptr_host[B] == 0) return IRM_OK;
@@ -1095,7 +1097,7 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     a.b0 = b0;
     a.B = std::min(kBatch, B - b0);
     const int32_t *ctx = ctx_host + b0, *indptr = q_indptr_host + b0;
-    const Plan p = plan_batch(ctx, indptr, a.B, H, pairs);
+    const Plan p = b0 == 0 ? first : plan_batch(ctx, indptr, a.B, H, pairs);
     const int units = (int)(p.n_long + p.n_rest);
     if (units == 0) continue;
     a.piece = p.piece;
