@@ -398,10 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!(ok = warp_poll(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+      tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
       tmem_ld_wait();
       if (own) {
-        tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
@@ -494,8 +493,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
-        tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
