@@ -400,10 +400,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
       tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
       tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
       if (own) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
         float corr = 1.f;
         // ================= softmax of a row =================
         float v[64];
@@ -493,9 +493,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_S_FREE + set));
         if (j >= 1 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + (xq ^ 2)), (uint32_t)((j - 1) >> 1) & 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
