@@ -374,8 +374,10 @@ __global__ void __launch_bounds__(kCompactLayers * kRowVec) pages_compact_kernel
   bool bad = n < 0 || n > a.max_path || base < 0;
   if (!bad)
     for (int k = threadIdx.x; k < n; k += blockDim.x) {
+      // path[k] >= k holds on every good path (it starts at 0 or above and increases); asked for by itself,
+      // since base + k must lie in the table here even where another thread's step is the bad one
       const int64_t from = (int64_t)base + path[k];
-      if (path[k] < 0 || (k > 0 && path[k] <= path[k - 1]) || from >= (int64_t)a.max_pages * kPage) {
+      if (path[k] < k || (k > 0 && path[k] <= path[k - 1]) || from >= (int64_t)a.max_pages * kPage) {
         bad = true;
         break;
       }

@@ -266,6 +266,22 @@ def test_compact_refuses_bad_paths(bad):
     assert torch.equal(kv.cpu().view(torch.int16), want.view(torch.int16))
 
 
+def test_compact_looks_up_no_row_behind_the_table():
+    """A path that is long and steps back, of the last request and near its table's end: step 39 is fine
+    by itself (0 -> 1, row 190 of 192), while base + 39 would lie behind the table."""
+    kv = torch.randn((2, 10, 64, 576), device="cuda").to(torch.bfloat16)
+    table, base, n = np.arange(6).reshape(2, 3), [0, 189], [2, 40]
+    path = np.full((2, 40), -1)
+    path[0, :2] = [0, 5]
+    path[1] = [2, 1] * 19 + [0, 1]
+    want = moved(kv.cpu(), table, base, path, [2, 0])
+    ws = compact(kv, table, base, path, n)
+    with pytest.raises(irm.IrmError) as e:
+        irm.device_status(ws)
+    assert e.value.status == -7
+    assert torch.equal(kv.cpu().view(torch.int16), want.view(torch.int16))
+
+
 # ---------------------------------------------------------------------------------- copies
 
 @pytest.mark.parametrize("n,layers", [(1, 1), (3, 5), (100, 2)])
