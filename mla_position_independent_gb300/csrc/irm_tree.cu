@@ -145,6 +145,7 @@ struct TreeArgs {
   int64_t n_pages;
   int B, b0, H, max_pages, mask_words;
   int piece;   // pages of a piece
+  uint32_t zero;  // 0, which the compiler does not know
   int n_long;  // units of full pieces; the requests' rests follow
   float scale_log2;
   __nv_bfloat16* out;
@@ -406,6 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (own) {
         float corr = 1.f;
         // ================= softmax of a row =================
+        // the maximum is taken over each half of the scores as it comes
         float v[64];
         if (!(ok = warp_poll_cluster(bar(BAR_X_HALF + xq), ph, abort_flag))) break;
 #pragma unroll
@@ -416,6 +418,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           v[4 * i + 2] = __uint_as_float(s[4 * i + 2]) + __uint_as_float(x.z);
           v[4 * i + 3] = __uint_as_float(s[4 * i + 3]) + __uint_as_float(x.w);
         }
+        if (j >= tail) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(see >> i & 1)) v[i] = -INFINITY;
+        }
+        float u[11];
+#pragma unroll
+        for (int i = 0; i < 10; ++i) u[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+        u[10] = fmaxf(v[30], v[31]);
+        const float low = fmax3(fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmax3(u[6], u[7], u[8])), u[9], u[10]);
         if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 8; i < 16; ++i) {
@@ -425,28 +437,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           v[4 * i + 2] = __uint_as_float(s[4 * i + 2]) + __uint_as_float(x.z);
           v[4 * i + 3] = __uint_as_float(s[4 * i + 3]) + __uint_as_float(x.w);
         }
-        __syncwarp();
+        if (j >= tail) {
+#pragma unroll
+          for (int i = 32; i < 64; ++i)
+            if (!(see >> i & 1)) v[i] = -INFINITY;
+        }
+        float t[11];
+#pragma unroll
+        for (int i = 0; i < 10; ++i) t[i] = fmax3(v[32 + 3 * i], v[33 + 3 * i], v[34 + 3 * i]);
+        t[10] = fmaxf(v[62], v[63]);
+        const float raw = fmax3(fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8])), fmax3(t[9], t[10], low), low);
+        const float top = raw * a.scale_log2;
+        // The peer may overwrite the received scores once they have been read, so the arrival that says so
+        // takes its address through a vote of the warp on the maximum of all that it read: it cannot be
+        // made before every lane's loads have returned.  (Without the vote the loads could still be under
+        // way: 64 x 32768 rows 855 instead of 873 us.)  A release at cluster scope costs far more, 1260 us
+        // from here, where it also waits for the st.async under way, and 1500 from a warp that has none.
+        const uint32_t vote = __ballot_sync(kFull, raw > 0.f);
         if (lane == 0) {
           if (j + 2 < ntiles) {
             mbar_arrive_expect_tx(bar(BAR_X_FULL + xq), kXBytes / 4);
             mbar_arrive_expect_tx(bar(BAR_X_HALF + xq), kXBytes / 4);
           }
-          // The warp's reads of shared memory are served in order, before this arrival leaves the SM, and
-          // what it lets in comes a round trip later.  A release would also wait for the st.async
-          // under way: 64 x 32768 rows 1260 instead of 855 us.
-          mbar_arrive_remote_relaxed(remXfree);
+          mbar_arrive_remote_relaxed(remXfree + (vote & a.zero));
         }
-        if (j >= tail) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!(see >> i & 1)) v[i] = -INFINITY;
-        }
-        float t[21];
-#pragma unroll
-        for (int i = 0; i < 21; ++i) t[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-#pragma unroll
-        for (int i = 0; i < 7; ++i) t[i] = fmax3(t[3 * i], t[3 * i + 1], t[3 * i + 2]);
-        const float top = fmaxf(fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), t[6]), v[63]) * a.scale_log2;
         if (j > 0 && !(ok = warp_poll(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
         const float before = j > 0 ? max_sh[mh] : -INFINITY;
         const bool up = top > before + 8.f;

@@ -317,3 +317,21 @@ def test_two_streams_and_a_replayed_graph():
     a["ctx"][:] = [3000, 50]
     irm.device_status(ws)
     check(a, out, lse)
+
+
+@pytest.mark.parametrize("ctx,nodes,H,q_std", [([4000, 4100, 900], [2, 1, 9], 128, 0.07), ([30000], [3], 16, 0.6), ([700] * 20, [13] * 20, 24, 0.3)])
+def test_repeats_beside_other_work(ctx, nodes, H, q_std):
+    """Hand-overs between the two halves of a pair, with their timing disturbed: the same bits each time."""
+    c = make(ctx, nodes, H, seed=27, q_std=q_std)
+    ws = irm.new_workspace(irm.tree_workspace_size(c["ctx"], c["indptr"], H))
+    out, lse, _ = call(c, workspace=ws)
+    check(c, out, lse, heads=[0, H - 1])
+    side, junk = torch.cuda.Stream(), torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+    for k in range(60):
+        if k % 2:
+            with torch.cuda.stream(side):
+                junk.add_(1)
+        again, lse2, _ = call(c, workspace=ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2), k
+    irm.device_status(ws)
+    torch.cuda.synchronize()
