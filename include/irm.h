@@ -334,8 +334,10 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  *   softmax_scale  positive, finite also when multiplied by log2(e)
  *   out     device bf16 [T, H, 512];  lse device fp32 [T, H] or NULL
  * Rows of the last page behind ctx_b + n_b - 1, and rows of drafts that no node of the request
- * sees, may hold anything (NaN included).  A NaN or infinity in any other row may spread to
- * every node of its request.
+ * sees, may hold anything (NaN included).  A score that is NaN or +infinity (from a query or a row that a
+ * node sees) makes O and lse of its (node, head) NaN, and one beyond 2^30 in magnitude may; a score of
+ * -infinity weighs nothing, and a row of nothing else counts as seeing none.  A NaN or infinity in a row
+ * that some node sees may also reach O of the request's other nodes (as 0 times it).
  * Workspace: irm_mla_attn_tree_workspace_size bytes for the same lengths and H.
  */
 irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32_t* q_indptr_host, int B, int H,

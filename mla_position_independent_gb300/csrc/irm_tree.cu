@@ -683,11 +683,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // both sets' sums are relative to the last maximum they saw; O to the last one of all, the larger
     const float2 x = reinterpret_cast<const float2*>(smem + kOffSum)[tid];
     const float2 y = reinterpret_cast<const float2*>(smem + kOffSum)[kHalf + tid];
-    const float mx = fmaxf(x.x, y.x);
-    float l = 0.f;
-    if (mx != -INFINITY) l = x.y * fast_exp2(x.x - mx) + y.y * fast_exp2(y.x - mx);
-    const bool some = m < rows_valid && *abort_flag == 0 && l > 0.f;
-    const float inv = some ? 1.f / l : 0.f, lse2 = some ? mx + __log2f(l) : -INFINITY;
+    const float mx = fmaxf(x.x, y.x), use = mx == -INFINITY ? 0.f : mx;
+    float l = x.y * fast_exp2(x.x - use) + y.y * fast_exp2(y.x - use);
+    // No key seen: maximum -inf and sum 0, and then alone O = 0 and lse = -inf.  Any other sum that is not a
+    // positive number comes from scores that are NaN, infinite or beyond 2^30, and stays visible.
+    const bool none = m >= rows_valid || *abort_flag != 0 || (mx == -INFINITY && l == 0.f);
+    if (!(l > 0.f && l < INFINITY)) l = NAN;
+    const float inv = none ? 0.f : 1.f / l, lse2 = none ? -INFINITY : mx + __log2f(l);
     inv_sh[m] = inv;
     if (tid < 32 * live_own)
       st_async_b32(mapa_shared(sb + kOffInv + 4u * (uint32_t)m, peer), __float_as_uint(inv), mapa_shared(bar(BAR_INV), peer));
@@ -713,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_ld32(tO + 32u, reinterpret_cast<uint32_t(&)[32]>(r[32]));
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) r[i] = inv > 0.f ? __float_as_uint(__uint_as_float(r[i]) * inv) : 0u;
+        for (int i = 0; i < 64; ++i) r[i] = inv != 0.f ? __float_as_uint(__uint_as_float(r[i]) * inv) : 0u;
         const int col = 256 * rank + c;
         __syncwarp();
         if (split) {  // rows of 256 bytes, 16-byte pieces XOR-ed with the row
@@ -760,7 +762,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Rows whose context was cut into pieces: O = sum 2^(lse_p - max) O_p / sum 2^(lse_p - max).  Rows
-// of uncut requests have nothing to do.
+// of uncut requests have nothing to do.  A piece of which a row sees nothing (lse -inf) weighs 0; a NaN
+// among the lse, which the maximum passes over, makes the row's sum NaN.
 //
 // Few pieces (and so, as a rule, many rows): a warp a row, 16 columns a lane, no barrier.
 constexpr int kMergeFew = 8;
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_few_kernel(const _
 #pragma unroll
   for (int k = 4; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, k));  // kMergeFew lanes
   mx = __shfl_sync(kFull, mx, 0);
-  const float w = mx == -INFINITY ? 0.f : fast_exp2(mine - mx);
+  const float w = mine == -INFINITY ? 0.f : fast_exp2(mine - mx);
   float4 acc[4] = {};
   float sum = 0.f;
 #pragma unroll 2
@@ -799,13 +802,13 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_few_kernel(const _
       acc[c].w += wp * v.w;
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const int64_t grow = (int64_t)req.first * a.H + row;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     *reinterpret_cast<uint2*>(a.out + grow * kDLat + 128 * c + 4 * lane) =
         make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+  if (a.lse != nullptr && lane == 0) a.lse[grow] = sum != 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Many pieces (few rows): a block a row; groups of 128 threads (4 columns a thread) share the row's
@@ -837,9 +840,12 @@ __global__ void __launch_bounds__(kMergeGroup * kMergeGroups) tree_merge_kernel(
   for (int w = 0; w < (int)blockDim.x / 32; ++w) mx = fmaxf(mx, top[w]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  for (int p0 = 0; p0 < pieces && mx != -INFINITY; p0 += kMergeWeights) {
+  for (int p0 = 0; p0 < pieces; p0 += kMergeWeights) {
     const int n = min(kMergeWeights, pieces - p0);
-    if (tid < n) weight[tid] = fast_exp2(lse[(int64_t)(p0 + tid) * kBM] - mx);
+    if (tid < n) {
+      const float x = lse[(int64_t)(p0 + tid) * kBM];
+      weight[tid] = x == -INFINITY ? 0.f : fast_exp2(x - mx);
+    }
     __syncthreads();
     for (int k = 0; k < n; ++k) sum += weight[k];
     constexpr int kUnroll = 8;
@@ -870,11 +876,11 @@ __global__ void __launch_bounds__(kMergeGroup * kMergeGroups) tree_merge_kernel(
     acc.z += v.z;
     acc.w += v.w;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const int64_t grow = (int64_t)req.first * a.H + row;
   *reinterpret_cast<uint2*>(a.out + grow * kDLat + 4 * tid) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse != nullptr && tid == 0) a.lse[grow] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+  if (a.lse != nullptr && tid == 0) a.lse[grow] = sum != 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------------- host

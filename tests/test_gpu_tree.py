@@ -335,3 +335,125 @@ def test_repeats_beside_other_work(ctx, nodes, H, q_std):
         assert torch.equal(out, again) and torch.equal(lse, lse2), k
     irm.device_status(ws)
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------- values that are not finite
+
+def lengths(cut):
+    """A request that is cut into pieces or not, and a short one beside it."""
+    return ([9000, 70], [3, 4]) if cut else ([150, 70], [3, 4])
+
+
+def set_row(c, b, t, col, value):
+    """Entry `col` of row t of request b's cache."""
+    c["kv"][int(c["table"][b, t // 64]), t % 64, col] = value
+
+
+def both(c):
+    out, lse, ws = call(c)
+    irm.device_status(ws)
+    return out.clone(), lse.clone()
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("col", [3, 300, 530, 575])
+@pytest.mark.parametrize("t", [0, 100, 149])
+def test_a_nan_key_reaches_every_row_that_sees_it(cut, col, t):
+    """One NaN entry of a committed row: its score is NaN, and so are the sums that it enters."""
+    ctx, nodes = lengths(cut)
+    c = make(ctx, nodes, 16, seed=30)
+    assert (irm.tree_workspace_size(c["ctx"], c["indptr"], 16) > 256) == cut
+    clean, clean_lse = both(c)
+    set_row(c, 0, t, col, float("nan"))
+    out, lse = both(c)
+    assert torch.isnan(out[:3]).all() and torch.isnan(lse[:3]).all()
+    assert torch.equal(out[3:], clean[3:]) and torch.equal(lse[3:], clean_lse[3:])
+
+
+@pytest.mark.parametrize("ctx", [0, 64, 9000])
+def test_a_nan_draft_reaches_the_nodes_that_see_it(ctx):
+    """Others may get NaN in O (0 times NaN), and have the sum of what they see in lse."""
+    c = make([ctx], [12], 16, seed=31)
+    sees = c["seen"][0][:, 5]
+    assert sees.any() and not sees.all()
+    set_row(c, 0, ctx + 5, 17, float("nan"))
+    out, lse = both(c)
+    q, kv = request(c, 0)
+    kv[ctx + 5] = 0.0
+    _, L, _, S = ref.tree_attention(q, kv, c["seen"][0], ctx, SCALE)
+    lse, out = lse.double().cpu().numpy(), out.float().cpu().numpy()
+    assert np.isnan(lse[sees]).all() and np.isnan(out[sees]).all()
+    d = np.abs(lse[~sees] - L[~sees])
+    assert (d <= 576 * 2.0 ** -22 * S[~sees] + 2.0 ** -20 * (1 + np.abs(L[~sees]))).all()
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("part", ["q_lat", "q_rope"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_is_its_own_rows_alone(cut, part, value):
+    """Among many keys some score is infinite or NaN: no weights are defined, and NaN comes out."""
+    ctx, nodes = lengths(cut)
+    c = make(ctx, nodes, 16, seed=32)
+    clean, clean_lse = both(c)
+    c[part][1, 6, 40] = value
+    c[part][4, 0, 2] = value
+    out, lse = both(c)
+    hit = torch.zeros((7, 16), dtype=torch.bool, device="cuda")
+    hit[1, 6], hit[4, 0] = True, True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("ctx", [40, 9000])
+def test_an_infinite_key(ctx):
+    """k_r alone infinite: a score of -inf weighs nothing, one of +inf (or 0 times infinity) gives NaN."""
+    c = make([ctx], [3], 16, seed=33)
+    set_row(c, 0, 20, 540, float("inf"))
+    q = c["q_rope"][:, :, 540 - 512].double().cpu().numpy()
+    out, lse = both(c)
+    low = q < 0
+    assert low.any() and not low.all()
+    g = lse.double().cpu().numpy()
+    assert np.isnan(g[~low]).all() and np.isnan(out.float().cpu().numpy()[~low]).all()
+    qq, kv = request(c, 0)
+    kv[20, 540] = 0.0
+    seen = np.delete(kv, 20, 0)  # the definition without that row
+    O, L, A, S = ref.tree_attention(qq, seen, c["seen"][0], ctx - 1, SCALE)
+    e = 576 * 2.0 ** -22 * S
+    o = out.double().cpu().numpy()
+    tol = STEP * np.abs(O) + (STEP + 2 * e[..., None] + 2.0 ** -20) * A + 1e-30
+    assert (np.abs(o - O) <= tol)[low].all()
+    assert (np.abs(g - L) <= e + 2.0 ** -20 * (1 + np.abs(L)))[low].all()
+
+
+def test_a_row_whose_every_score_is_minus_infinity():
+    """counts as one that sees nothing."""
+    c = make([1, 5], [1, 2], 2, seed=34, mask="none")
+    c["q_rope"][0, :, 0] = torch.tensor([-1.0, 1.0], device="cuda").to(torch.bfloat16)
+    set_row(c, 0, 0, 512, float("inf"))
+    out, lse = both(c)
+    assert (out[0, 0] == 0).all() and lse[0, 0] == -float("inf")
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    check(c, out, lse, requests=[1])
+
+
+@pytest.mark.parametrize("power", [20, 28, 40, 60])
+@pytest.mark.parametrize("cut", [False, True])
+def test_scores_of_great_size(power, cut):
+    """Up to 2^30 the sums keep their meaning (lse to the error of a score); beyond, NaN may come out, and
+    never the answer of a row that sees nothing."""
+    ctx, nodes = lengths(cut)
+    c = make(ctx, nodes, 16, seed=35, q_std=2.0 ** (power / 2), kv_std=2.0 ** (power / 2 - 4))
+    out, lse = both(c)
+    assert not torch.isinf(lse).any()
+    for b in range(2):
+        lo, hi = c["indptr"][b], c["indptr"][b + 1]
+        q, kv = request(c, b)
+        _, L, _, S = ref.tree_attention(q, kv, c["seen"][b], int(c["ctx"][b]), SCALE)
+        g = lse[lo:hi].double().cpu().numpy()
+        fine = np.abs(g - L) <= 576 * 2.0 ** -22 * S + 2.0 ** -20 * (1 + np.abs(L))
+        if np.abs(S).max() * 1.4427 < 2.0 ** 30:
+            assert fine.all() and torch.isfinite(out[lo:hi]).all()
+        assert (fine | np.isnan(g)).all()
+        some = (out[lo:hi].float().abs().amax(2) > 0) | torch.isnan(out[lo:hi]).any(2)
+        assert some.all()
