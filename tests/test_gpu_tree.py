@@ -12,6 +12,7 @@ import torch
 
 import mla_position_independent_gb300 as irm
 import spec_reference as ref
+import tree_bounds
 from helpers import SCALE
 
 pytestmark = pytest.mark.gpu
@@ -457,3 +458,57 @@ def test_scores_of_great_size(power, cut):
         assert (fine | np.isnan(g)).all()
         some = (out[lo:hi].float().abs().amax(2) > 0) | torch.isnan(out[lo:hi]).any(2)
         assert some.all()
+
+
+# ------------------------------------------------------------- every key of a long context
+
+def pages_apart(c):
+    """The values of each page of a request in a column of their own (page index mod 512): O holds the pages'
+    weights, each to the rounding of its own size."""
+    for b in range(len(c["ctx"])):
+        rows = int(c["ctx"][b]) + int(c["indptr"][b + 1] - c["indptr"][b])
+        for i, t in enumerate(range(0, rows, 64)):
+            page = c["kv"][int(c["table"][b, i]), :rows - t]
+            page[:, :512] = 0.0
+            page[:, i % 512] = 1.0
+    return c
+
+
+LONG = [([200], [3], 16), ([50000], [1], 2), ([50000], [5], 2), ([20000], [9], 128), ([9000, 20, 4100], [3, 5, 17], 16), ([4095] * 3, [1] * 3, 16)]
+
+
+@pytest.mark.parametrize("ctx,nodes,H", LONG)
+def test_each_page_has_its_weight(ctx, nodes, H):
+    run_and_check(pages_apart(make(ctx, nodes, H, seed=40)), heads=sorted({0, H // 2, H - 1}))
+
+
+@pytest.mark.parametrize("ctx,nodes,H", LONG)
+@pytest.mark.parametrize("q_std", [1.0 / np.sqrt(192.0), 1.0])
+def test_rows_as_a_whole(ctx, nodes, H, q_std):
+    """Each row's error against a bound that shrinks with the row, so that no page can be missed."""
+    c = make(ctx, nodes, H, seed=41, q_std=q_std)
+    out, lse, ws = call(c)
+    irm.device_status(ws)
+    hs = sorted({0, H // 2, H - 1})
+    check(c, out, lse, heads=hs)
+    for b in range(len(ctx)):
+        q, kv = request(c, b)
+        o = out[c["indptr"][b]:c["indptr"][b + 1]].double().cpu().numpy()
+        assert tree_bounds.row_errors(o[:, hs], q[:, hs], kv, c["seen"][b], ctx[b], SCALE).max() <= 1.0
+
+
+def test_cut_contexts_in_later_launches():
+    """A launch takes 256 requests: long contexts at the edges and in the middle of the second and third, where
+    the partials' buffer is used anew and the first node is not 0."""
+    rng = np.random.default_rng(42)
+    ctx, n = rng.integers(0, 90, 600), rng.integers(0, 4, 600)
+    for b, rows in ((10, 6000), (255, 500), (256, 7000), (300, 9000), (511, 700), (512, 12000), (599, 5000)):
+        ctx[b], n[b] = rows, 2
+    n[[0, 254, 257, 510, 513, 598]] = 1, 3, 1, 2, 3, 1
+    c = pages_apart(make(ctx.tolist(), n.tolist(), 16, seed=42))
+    for lo in (0, 256, 512):  # each launch has a cut context
+        hi = min(lo + 256, 600)
+        assert irm.tree_workspace_size(c["ctx"][lo:hi], c["indptr"][lo:hi + 1] - c["indptr"][lo], 16) > 256
+    out, lse, ws = call(c)
+    irm.device_status(ws)
+    check(c, out, lse, requests=sorted({0, 10, 254, 255, 256, 257, 300, 510, 511, 512, 513, 598, 599} | set(range(3, 600, 41))))
