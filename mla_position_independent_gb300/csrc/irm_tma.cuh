@@ -50,30 +50,6 @@ __device__ __forceinline__ void bulk_to_peer(uint32_t cluster_addr, uint32_t src
                : "memory");
 }
 
-// Bounded waits as mbar_wait / mbar_wait_cluster, but the clock and the flag are first looked at after
-// a thousand polls, so that the common wait is the poll alone (a tile's time is the same with
-// earlier looks, 1.2 us, but a role's code is shorter).  False once kWaitLimitNs has passed or
-// *abort_flag != 0.
-template <bool kCluster>
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023u) == 0) {
-      if (abort_flag != nullptr && *abort_flag) return false;
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) return false;
-    }
-  }
-}
-__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, mbar_poll<false>(bar, parity, abort_flag));
-}
-__device__ __forceinline__ bool warp_poll_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, mbar_poll<true>(bar, parity, abort_flag));
-}
-
 // Arrive (once) on the mbarrier at this offset in every CTA of `mask` when all UMMAs issued so
 // far are complete.
 __device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mask) {

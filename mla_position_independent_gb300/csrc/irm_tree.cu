@@ -334,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool valid = m < rows_valid;
     // ---- Q, this CTA's cKV columns: from shared memory (where TMA put it) to TMEM; set h takes
     //      slabs 2h, 2h + 1
-    ok = warp_poll(bar(BAR_QIN), 0, abort_flag);
+    ok = warp_wait(bar(BAR_QIN), 0, abort_flag);
     if (live && ok) {
 #pragma unroll
       for (int slab = 2 * set; slab < 2 * set + 2; ++slab) {
@@ -376,11 +376,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // turn late, after it has shipped the scores of tile t + 2, so that the peer never waits for it;
     // P V waits for this only where a factor is not 1.
     auto take_factors = [&](int t) -> bool {
-      if (!warp_poll_cluster(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
+      if (!warp_wait_cluster(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
       if (lane == 0 && t + 2 < ntiles) mbar_arrive_expect_tx(bar(BAR_PR_FULL + set), kPrBytes);
       const float corr = corr_sh[(t & 3) * kHalf + mh];
       if (t > 0 && __any_sync(kFull, corr != 1.f)) {
-        if (!warp_poll(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
+        if (!warp_wait(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
         tc_fence_after();
         rescale_o(tO, corr);
         tc_fence_before();
@@ -396,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t s[64];
       uint64_t see = 0;  // read before the waits
       if (own && j >= tail && valid) see = seen_rows(mask, a.mask_words, (kb + j) * kPage, ctx, n);
-      if (!(ok = warp_poll(bar(BAR_S_FULL + set), ph, abort_flag))) break;
+      if (!(ok = warp_wait(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
       tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
@@ -409,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ================= softmax of a row =================
         // the maximum is taken over each half of the scores as it comes
         float v[64];
-        if (!(ok = warp_poll_cluster(bar(BAR_X_HALF + xq), ph, abort_flag))) break;
+        if (!(ok = warp_wait_cluster(bar(BAR_X_HALF + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint4 x = X[i * kHalf + mh];
@@ -428,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 10; ++i) u[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
         u[10] = fmaxf(v[30], v[31]);
         const float low = fmax3(fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmax3(u[6], u[7], u[8])), u[9], u[10]);
-        if (!(ok = warp_poll_cluster(bar(BAR_X_FULL + xq), ph, abort_flag))) break;
+        if (!(ok = warp_wait_cluster(bar(BAR_X_FULL + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 8; i < 16; ++i) {
           const uint4 x = X[i * kHalf + mh];
@@ -461,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_remote_relaxed(remXfree + (vote & a.zero));
         }
-        if (j > 0 && !(ok = warp_poll(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+        if (j > 0 && !(ok = warp_wait(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
         const float before = j > 0 ? max_sh[mh] : -INFINITY;
         const bool up = top > before + 8.f;
         const float now = up ? top : before;
@@ -484,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const float2 part = f2_unpack(f2_add(sum[0], sum[1]));
         l += part.x + part.y;
-        if (j >= 2 && !(ok = warp_poll_cluster(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint4 w = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
@@ -498,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool moved = __any_sync(kFull, corr != 1.f);
         if (lane == 0) st_async_b32(remFlag, moved ? 1u : 0u, remPfull);
         if (j > 0 && moved) {
-          if (!(ok = warp_poll(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+          if (!(ok = warp_wait(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
           tc_fence_after();
           rescale_o(tO, corr);
         }
@@ -507,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
-        if (j >= 1 && !(ok = warp_poll_cluster(bar(BAR_X_FREE + (xq ^ 2)), (uint32_t)((j - 1) >> 1) & 1u, abort_flag))) break;
+        if (j >= 1 && !(ok = warp_wait_cluster(bar(BAR_X_FREE + (xq ^ 2)), (uint32_t)((j - 1) >> 1) & 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
@@ -531,8 +531,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int y = __shfl_sync(kFull, page, j & 31) * kPage;
       const int s = j % kStages;
       // stages 2 and 3 hold Q until it is in TMEM
-      if (j == 2 && !(ok = warp_poll(bar(BAR_Q), 0, abort_flag))) break;
-      if (j >= kStages && !(ok = warp_poll(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
+      if (j == 2 && !(ok = warp_wait(bar(BAR_Q), 0, abort_flag))) break;
+      if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         mbar_arrive_expect_tx(bar(BAR_LANDED + s), kStage + kKr);
@@ -541,25 +541,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       sent = j + 1;
       // the k_r buffer's last page has been through Q K^T
-      if (j >= 2 && !(ok = warp_poll(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+      if (j >= 2 && !(ok = warp_wait(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) tma_load_2d(sb + kOffKr + (uint32_t)(j & 1) * kKr, &a.map_rope, kDLat + 32 * rank, y, bar(BAR_LANDED + s));
     }
     // the copies in flight land before the CTA ends, whatever became of the others
-    ok = warp_poll(bar(BAR_QIN), 0, nullptr) && ok;
+    ok = warp_wait(bar(BAR_QIN), 0, nullptr) && ok;
     for (int j = max(0, sent - kStages); j < sent; ++j)
-      ok = warp_poll(bar(BAR_LANDED + j % kStages), (uint32_t)(j / kStages) & 1u, nullptr) && ok;
+      ok = warp_wait(bar(BAR_LANDED + j % kStages), (uint32_t)(j / kStages) & 1u, nullptr) && ok;
     __syncwarp();
     cluster_wait();
   } else if (warp == kSWarp) {
     // ================= Q K^T (one thread) =================
     if (lane == 0) {
-      ok = mbar_poll<false>(bar(BAR_QIN), 0, abort_flag) && mbar_poll<false>(bar(BAR_Q), 0, abort_flag);
+      ok = mbar_wait(bar(BAR_QIN), 0, abort_flag) && mbar_wait(bar(BAR_Q), 0, abort_flag);
       tc_fence_after();
       const uint64_t aq = sdesc_sw64(sb + kOffQr, 512);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
-        if (!(ok = mbar_poll<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
-        if (j >= 2 && !(ok = mbar_poll<false>(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+        if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = mbar_wait(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(sb + kOffKr + (uint32_t)set * kKr, 512);
@@ -574,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         umma_commit(bar(BAR_S_FULL + set));
       }
       umma_commit(bar(BAR_DRAIN));
-      ok = mbar_poll<false>(bar(BAR_DRAIN), 0, nullptr) && ok;
+      ok = mbar_wait(bar(BAR_DRAIN), 0, nullptr) && ok;
     }
     __syncwarp();
     cluster_wait();
@@ -586,19 +586,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int s = j % kStages, set = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
         if (j >= tail) {
-          if (!(ok = mbar_poll<false>(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
+          if (!(ok = mbar_wait(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
           fence_proxy_async_smem();  // the cleared rows' plain stores
         }
-        if (live_own && !(ok = mbar_poll<false>(bar(BAR_GO + set), ph, abort_flag))) break;
+        if (live_own && !(ok = mbar_wait(bar(BAR_GO + set), ph, abort_flag))) break;
         if (live_peer) {
-          if (!(ok = mbar_poll<true>(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
+          if (!(ok = mbar_wait_cluster(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
           uint32_t f0, f1;
           asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(f0), "=r"(f1) : "r"(sb + kOffFlag + 8u * (uint32_t)set) : "memory");
           // a rescaling waits for P V of the tile before, so these phases are passed one by one
           const uint32_t moved = j > 0 ? f0 | (live_peer > 1 ? 2u * f1 : 0u) : 0u;
           if (moved != 0) {
-            if (moved & 1u) ok = mbar_poll<false>(bar(BAR_RESC), resc & 1u, abort_flag);
-            if (ok && moved & 2u) ok = mbar_poll<false>(bar(BAR_RESC + 1), resc >> 1, abort_flag);
+            if (moved & 1u) ok = mbar_wait(bar(BAR_RESC), resc & 1u, abort_flag);
+            if (ok && moved & 2u) ok = mbar_wait(bar(BAR_RESC + 1), resc >> 1, abort_flag);
             resc ^= moved;
             if (!ok) break;
           }
@@ -614,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         umma_commit_multicast(bar(BAR_P_FREE + set), (uint16_t)3);
       }
       umma_commit(bar(BAR_DRAIN + 1));
-      ok = mbar_poll<false>(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
+      ok = mbar_wait(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
     }
     __syncwarp();
     cluster_wait();
@@ -644,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         lo = __reduce_or_sync(kFull, (uint32_t)see);
         hi = __reduce_or_sync(kFull, (uint32_t)(see >> 32));
       }
-      if (!(ok = warp_poll(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+      if (!(ok = warp_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
       if (j >= tail) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -705,7 +705,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kScoreWarps) {
     const int quad = warp & 3, m = quad * 32 + lane;
     if (quad * 32 < rows_valid) {
-      if ((quad >> 1) != rank && !warp_poll_cluster(bar(BAR_INV), 0, abort_flag)) set_status(a.status, kDevErrTimeout);
+      if ((quad >> 1) != rank && !warp_wait_cluster(bar(BAR_INV), 0, abort_flag)) set_status(a.status, kDevErrTimeout);
       const float inv = inv_sh[m];
       uint8_t* stage = smem + kOffKv + warp * 8192;
       for (int c = 128 * (warp >> 2); c < 128 * (warp >> 2) + 128; c += 64) {

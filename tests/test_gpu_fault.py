@@ -35,3 +35,20 @@ def test_bounded_wait_reports_timeout_and_context_survives(oracle_mod):
     O, _ = oracle_mod.mla_attention(synth.bits(case.q_lat), synth.bits(case.q_rope), case.chunks,
                                     case.indptr, synth.bits(case.kv_rows), SCALE)
     assert_close(widen_bf16(out[:, None]), O, "decode after the timeout")
+
+
+def test_both_forms_of_the_wait_give_up_at_their_limit():
+    """The status is set only where the wait for a barrier of this CTA and the one for a peer's both gave up;
+    they run side by side, and look at the clock every few tries."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ws = irm.new_workspace(256)
+    torch.cuda.synchronize()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    irm.selftest_wait_timeout(ws)
+    end.record()
+    with pytest.raises(irm.IrmError) as e:
+        irm.device_status(ws)
+    assert e.value.status == -6
+    assert 2000.0 <= start.elapsed_time(end) < 3000.0
