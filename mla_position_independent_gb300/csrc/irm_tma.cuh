@@ -29,12 +29,6 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
          (4ull << 61);
 }
 
-// Byte offset of 16-byte chunk `chunk` (0..3) of row `row` in a 64-byte-swizzled slab whose base
-// is 512-byte aligned: rows are 64 B apart, chunks XOR-ed with bits 1-2 of the row.
-__host__ __device__ constexpr uint32_t sw64_offset(uint32_t row, uint32_t chunk) {
-  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
-}
-
 // 4-byte store into a peer CTA's shared memory, counted in bytes on the peer's mbarrier.
 __device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, uint32_t cluster_bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
