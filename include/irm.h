@@ -310,6 +310,8 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  * b owns nodes [q_indptr_host[b], q_indptr_host[b + 1]), at most IRM_MAX_TREE, possibly none.
  * Host arrays of these calls travel in the launch parameters: the caller may reuse them as
  * soon as the call returns, and a captured graph replays the lengths as they were given.
+ * irm_mla_attn_tree takes its context lengths so, and the next step's are base + n_accept: the
+ * caller reads irm_tree_verify's n_accept back once between two steps.
  * These calls leave scratch of their own in a workspace and expect none: they may share one, one
  * after another.  A workspace that they have used is zeroed again before a decode or prefill call
  * gets it, since those keep counters there.
@@ -379,7 +381,7 @@ irm_status irm_tree_verify(const float* target_probs, const float* draft_probs, 
                            int32_t* next_token, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
- * Pages of a cache, kept on the device so that a step needs no host round trip.  The cache is
+ * Pages of a cache, kept on the device so that within a step no call waits for the host.  The cache is
  * bf16 [n_layers, n_pages, 64, 576]; all layers share one page table.
  *   seq_len    device int32 [n_slots]: rows of each request; request s holds the pages
  *              page_table[s, 0 .. ceil(seq_len[s] / 64) - 1], n_slots <= 8192
