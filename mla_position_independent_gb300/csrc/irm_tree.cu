@@ -33,24 +33,24 @@
 // gaps); their normalised fp32 partials are merged by a second kernel.
 // Every wait is bounded (2 s) and reports a timeout in the status word.
 //
-// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 855 us, 1.37 PFLOP/s, 0.71 of the
-// measured bf16 rate; in the units' own time a tile takes 0.92 us, ~1750 cycles.  Two limits are
-// near it:
+// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 940 us under the power cap (1.77 GHz),
+// 1.24 PFLOP/s, 0.65 of the measured bf16 rate; 872 us and 0.70 in a run too short to reach the cap, where a
+// tile takes 0.94 us in the units' own time, ~1800 cycles.  Two limits are near it:
 //   - Issue of MMAs: at N = 64 one takes 44.5 cycles, not 32, so that Q K^T (18) and P V (4 of 128
 //     cycles) keep the tensor core for 1313 cycles a tile.  N = 128 runs at the full rate, but two
 //     pages at once start both sets at once: 1066 us.
-//   - The tiles in flight: a page is held from its TMA until its P V, ~8000 cycles, a fifth of which
-//     is the exchange of scores (with an eighth of the bytes, and wrong results, a tile takes an eighth less
-//     time).  With four pages in flight 975 us, although the received scores then have a
-//     buffer for each set.  So everything else makes room for the fifth: one buffer for received
-//     scores (their senders keep them in registers until it is free), k_r in a ring of two.
-// Measured and not taken (64 x 32768, when the kernel stood at the first figure): P by st.async of
+//   - The tiles in flight: a page is held from its TMA until its P V, ~8000 cycles, in which a softmax
+//     warp waits ~1070 cycles for the other CTA's scores.  With four pages in flight 975 us (855 with
+//     five), although the received scores then have a buffer for each set.  So everything else makes
+//     room for the fifth: one buffer for received scores (their senders keep them in registers until it
+//     is free), k_r in a ring of two.
+// Measured and not taken (64 x 32768, when the kernel stood at the figure in brackets): P by st.async of
 // 16 bytes 1115 (988 with bulk copies); scores by bulk copies 1049 (991); by plain remote stores and a
 // release 1193 (988); tiles of 32 rows, four sets 1381 (988); pages of 64 rows with four sets of 32
 // keys 1010 (988); softmax split by keys 1.09 times the time; a second warp for each row 1.18 times.
-// Few rows (16 heads, one node, 76 requests) stream 0.89 us a further page, 6.3 TB/s, 0.93 of the
+// Few rows (16 heads, one node, 76 requests) stream 0.88 us a further page, 6.3 TB/s, 0.93 of the
 // measured copy rate.  One short request (512 rows, 16 heads) takes 12.1 us, of which one tile alone
-// (63 rows) is 9.4: it is set-up, the chain of one tile and the way out.
+// (63 rows) is 8.4: it is set-up, the chain of one tile and the way out.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>

@@ -26,8 +26,8 @@
 //
 // What bounds it: latency.  One row of V fp32 (two with draft probabilities) per request is read for
 // the final draw, 0.06 us of memory time at one request of 102400 entries and 3.9 us at 64, but
-// the chain of launch, gather, walk, sum, cluster exchange and locating the token takes 11.1 and
-// 18 us.  So a cluster of C CTAs shares a request's row in contiguous warp segments; the CTA
+// the chain of launch, gather, walk, sum, cluster exchange and locating the token takes 11.2 and
+// 18.1 us.  So a cluster of C CTAs shares a request's row in contiguous warp segments; the CTA
 // totals travel through distributed shared memory, and what is located is one group of one
 // warp's loads, from group sums kept during the sum.  The children's probabilities are gathered in
 // one round of loads, all nodes at once, before the walk, which then runs in shared memory.
