@@ -81,6 +81,9 @@ typedef struct CUstream_st* cudaStream_t; /* identical to the CUDA runtime's typ
 #define IRM_MAX_HEADS 128
 #define IRM_WORKSPACE_HEADER 256
 #define IRM_MAX_TREE 1024    /* drafted tokens of one request */
+#define IRM_ROW_BYTES8 656   /* KV row of an 8-bit cache: 512 codes, 4 scales, 64 bf16 of k_r */
+#define IRM_ROW8_SCALES 512  /* where its scales start, bytes */
+#define IRM_ROW8_ROPE 528    /* and its k_r */
 
 typedef enum irm_status {
   IRM_OK = 0,
@@ -297,11 +300,11 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
                                      size_t workspace_bytes, cudaStream_t stream);
 
 /*
- * Speculative decoding over the paged cache.  The calls below work on 64-row pages, the layout
- * irm_assemble_kv writes, and make up one step: irm_pages_resize makes room for the drafts,
- * the model writes their rows, irm_mla_attn_tree attends (once a layer), irm_tree_verify
- * accepts a path and draws the next token, irm_pages_compact moves the path's rows up, and
- * irm_pages_resize gives the rest back.
+ * Decoding over the paged cache, token by token or speculatively.  The calls below work on 64-row
+ * pages, the layout irm_assemble_kv writes, and make up one step: irm_pages_resize makes room for
+ * the new tokens or drafts, irm_rope_apply encodes their queries and irm_pages_append their
+ * rows, irm_mla_attn_tree attends (these once a layer); for drafts, irm_tree_verify accepts a path and draws the
+ * next token, irm_pages_compact moves the path's rows up, and irm_pages_resize gives the rest back.
  *
  * A request's tree has n nodes, numbered so that a parent comes before its children; node 0
  * is the last committed token (its row is not in the cache yet).  Node i's KV row sits at slot
@@ -318,7 +321,65 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  */
 
 /*
- * Attention of a tree of drafted tokens over the paged cache (absorbed MLA, as the decode).
+ * Rotation of queries (or any bf16 vectors of 64 entries) by their positions:
+ *   out[t, h] = factor * R(position[t]) x[t, h]
+ * in fp32 from an exactly reduced angle, rounded to bf16 once.  A negative position turns
+ * backwards, which undoes a rotation (with factor 1 / factor) and is its gradient (with the same
+ * factor).
+ *   x        device bf16, 64 entries of head h of token t at t * x_token + h * x_head (elements,
+ *            multiples of 8; 16-byte aligned): part of a wider head as well as a tensor of its own
+ *   position device int32 [n_tokens]
+ *   rope     the model's frequencies and pairing (NULL: the default)
+ *   factor   finite; the magnitude that some scaled tables bring along, else 1
+ *   out      as x, of its own strides; x itself, or memory that does not overlap it
+ * n_tokens < 2^31, n_heads <= 65535.
+ */
+irm_status irm_rope_apply(const void* x, int64_t x_token, int64_t x_head, int64_t n_tokens, int n_heads,
+                          const int32_t* position, const irm_rope* rope, float factor, void* out, int64_t out_token,
+                          int64_t out_head, cudaStream_t stream);
+
+/*
+ * New rows into one layer of the paged cache, k_r rotated on the way: for every token t with row[t] >= 0
+ *   s = request ? request[t] : t,  i = row[t],  p = position ? position[t] : i
+ *   kv[page_table[s, i / 64], i % 64] = [c_kv[t] | factor * R(p) k_rope[t]]
+ *
+ *   c_kv     device bf16, row t at t * c_stride (elements, a multiple of 8), 16-byte aligned;
+ *   k_rope   the same, t * k_stride (both may be columns of one projection's output [T, 576])
+ *   kv       irm_pages_append: device bf16 [n_pages, 64, 576]
+ *            irm_pages_append8: device bytes [n_pages, 64, 656], the 8-bit cache (below)
+ *   page_table device int32 [n_slots, max_pages]
+ *   row, request, position   device int32 [n_tokens] (request NULL: one token a slot, n_tokens <=
+ *            n_slots; position NULL: the row).  A negative row means that the token is not written
+ *            (padding).  (request, row) pairs must be distinct: of a row named twice nothing is
+ *            promised but that only its bytes are written.
+ *   rope, factor as for irm_rope_apply
+ *   encoded  1: k_rope is copied as it is (rows that are already encoded, such as an assembled
+ *            request's); position, rope and factor are not looked at.  Else 0.
+ * A request outside [0, n_slots), a row beyond the table or a page outside [0, n_pages) is recorded as
+ * IRM_ERR_DEVICE_BOUNDS and the token is not written.  Workspace: IRM_WORKSPACE_HEADER bytes.
+ *
+ * A row of the 8-bit cache is 656 bytes:
+ *   bytes   0 .. 511  e4m3 codes of cKV
+ *   bytes 512 .. 527  four fp32 scales, one for 128 columns: cKV[j] = code[j] * scale[j / 128]
+ *   bytes 528 .. 655  k_r, 64 bf16
+ * A scale is the smallest power of two in [2^-126, 2^7] for which the 128 columns fit e4m3 (448 at most;
+ * 1 where all are zero), so code * scale is exact in bf16; codes are rounded to the nearest even, and
+ * magnitudes beyond 448 * 2^7 become that.  A group with a NaN or an infinity gets a NaN scale and reads as
+ * NaN.  Rows from elsewhere may bring any codes but 0x7f and 0xff (which read as +-480) and any scales
+ * below 2^8: of a scale that is no power of two the upper 16 bits count, and the product is rounded to bf16.
+ */
+irm_status irm_pages_append(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t k_stride, int64_t n_tokens,
+                            void* kv, int64_t n_pages, const int32_t* page_table, int n_slots, int max_pages,
+                            const int32_t* row, const int32_t* request, const int32_t* position, const irm_rope* rope,
+                            float factor, int encoded, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+irm_status irm_pages_append8(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t k_stride, int64_t n_tokens,
+                             void* kv, int64_t n_pages, const int32_t* page_table, int n_slots, int max_pages,
+                             const int32_t* row, const int32_t* request, const int32_t* position, const irm_rope* rope,
+                             float factor, int encoded, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache (absorbed MLA, as the decode); a single
+ * token is a tree of one node.
  *   node i of request b sees the request's rows t < ctx_b, and the rows ctx_b + k of the
  *   drafts k whose bit k is set in its mask; bits of k >= n_b are ignored
  *   O = softmax(s) . cKV, s_t = scale * (q_lat . cKV_t + q_rope . k_r,t); a node that sees no
@@ -341,6 +402,10 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  * -infinity weighs nothing, and a row of nothing else counts as seeing none.  A NaN or infinity in a row
  * that some node sees may also reach O of the request's other nodes (as 0 times it).
  * Workspace: irm_mla_attn_tree_workspace_size bytes for the same lengths and H.
+ *
+ * irm_mla_attn_tree8 attends over an 8-bit cache (device bytes [n_pages, 64, 656], see irm_pages_append8):
+ * cKV_t is code * scale as read in bf16, everything else is as above, the workspace's size too.  A NaN
+ * scale makes the row's 128 columns NaN.
  */
 irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32_t* q_indptr_host, int B, int H,
                                             size_t* bytes);
@@ -349,6 +414,11 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
                              const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
                              float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                              cudaStream_t stream);
+irm_status irm_mla_attn_tree8(const void* q_lat, const void* q_rope, int B, int H, const int32_t* ctx_host,
+                              const int32_t* q_indptr_host, const void* paged_kv, int64_t n_pages,
+                              const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
+                              float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
 
 /*
  * Verification of a batch's trees against the target's probabilities, from given uniform
@@ -382,7 +452,8 @@ irm_status irm_tree_verify(const float* target_probs, const float* draft_probs, 
 
 /*
  * Pages of a cache, kept on the device so that within a step no call waits for the host.  The cache is
- * bf16 [n_layers, n_pages, 64, 576]; all layers share one page table.
+ * bf16 [n_layers, n_pages, 64, 576]; all layers share one page table.  irm_pages_fork8, irm_pages_compact8
+ * and irm_pages_copy8 are the same calls for an 8-bit cache, bytes [n_layers, n_pages, 64, 656].
  *   seq_len    device int32 [n_slots]: rows of each request; request s holds the pages
  *              page_table[s, 0 .. ceil(seq_len[s] / 64) - 1], n_slots <= 8192
  *   page_table device int32 [n_slots, max_pages], at most 2^30 entries; those given back become -1
@@ -413,6 +484,9 @@ irm_status irm_pages_resize(const int32_t* new_len, int32_t* seq_len, int n_slot
 irm_status irm_pages_fork(const int32_t* src_host, const int32_t* dst_host, int n_forks, void* kv, int n_layers,
                           int32_t* seq_len, int n_slots, int32_t* page_table, int max_pages, int32_t* refcount,
                           int64_t n_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+irm_status irm_pages_fork8(const int32_t* src_host, const int32_t* dst_host, int n_forks, void* kv, int n_layers,
+                           int32_t* seq_len, int n_slots, int32_t* page_table, int max_pages, int32_t* refcount,
+                           int64_t n_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 /* Moves the rows of an accepted path up: row base[s] + path[s, k] to row base[s] + k, for k <
  * n_accept[s], in every layer (base, n_accept device int32 [n_slots], path device int32 [n_slots,
  * max_path], as irm_tree_verify writes them; paths increase strictly).  Lengths and pages
@@ -420,10 +494,15 @@ irm_status irm_pages_fork(const int32_t* src_host, const int32_t* dst_host, int 
 irm_status irm_pages_compact(void* kv, int n_layers, int64_t n_pages, const int32_t* page_table, int max_pages,
                              int n_slots, const int32_t* base, const int32_t* path, int max_path,
                              const int32_t* n_accept, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+irm_status irm_pages_compact8(void* kv, int n_layers, int64_t n_pages, const int32_t* page_table, int max_pages,
+                              int n_slots, const int32_t* base, const int32_t* path, int max_path,
+                              const int32_t* n_accept, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 /* Copies pages src_host[i] -> dst_host[i] (host int32 [n]) in every layer; destinations distinct
  * and not sources.  Tables and counts are the caller's to change. */
 irm_status irm_pages_copy(void* kv, int n_layers, int64_t n_pages, const int32_t* src_host, const int32_t* dst_host,
                           int n, cudaStream_t stream);
+irm_status irm_pages_copy8(void* kv, int n_layers, int64_t n_pages, const int32_t* src_host, const int32_t* dst_host,
+                           int n, cudaStream_t stream);
 
 /*
  * Content-defined chunking of token streams, the step that cuts a request's unmatched tail

@@ -19,6 +19,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libirm.so"
 _lib = None
 
 WORKSPACE_HEADER = 256
+ROW_BYTES8 = 656  # a row of an 8-bit cache: 512 e4m3 codes, 4 fp32 scales, 64 bf16 of k_r
 DEFAULT_SCALE = 1.0 / math.sqrt(192.0)
 
 EXPORTS = ["irm_status_string", "irm_last_error", "irm_version", "irm_validate_chunks",
@@ -29,7 +30,8 @@ EXPORTS = ["irm_status_string", "irm_last_error", "irm_version", "irm_validate_c
            "irm_cdc_sizes", "irm_cdc_chunk", "irm_registry_create", "irm_registry_stats",
            "irm_registry_assemble", "irm_selftest_wait_timeout", "irm_mla_attn_tree_workspace_size",
            "irm_mla_attn_tree", "irm_tree_verify", "irm_pages_workspace_size", "irm_pages_resize",
-           "irm_pages_fork", "irm_pages_compact", "irm_pages_copy"]
+           "irm_pages_fork", "irm_pages_compact", "irm_pages_copy", "irm_mla_attn_tree8", "irm_pages_fork8",
+           "irm_pages_compact8", "irm_pages_copy8", "irm_rope_apply", "irm_pages_append", "irm_pages_append8"]
 
 ROPE_NEOX, ROPE_INTERLEAVED = 0, 1
 
@@ -114,6 +116,11 @@ def lib():
         L.irm_pages_fork.argtypes = [P, P, I, P, I, P, I, P, I, P, I64, P, SZ, P]
         L.irm_pages_compact.argtypes = [P, I, I64, P, I, I, P, P, I, P, P, SZ, P]
         L.irm_pages_copy.argtypes = [P, I, I64, P, P, I, P]
+        for name in ("irm_mla_attn_tree", "irm_pages_fork", "irm_pages_compact", "irm_pages_copy"):  # over an 8-bit cache
+            getattr(L, name + "8").argtypes = getattr(L, name).argtypes
+        L.irm_rope_apply.argtypes = [P, I64, I64, I64, I, P, P, ctypes.c_float, P, I64, I64, P]
+        L.irm_pages_append.argtypes = [P, I64, P, I64, I64, P, I64, P, I, I, P, P, P, P, ctypes.c_float, I, P, SZ, P]
+        L.irm_pages_append8.argtypes = L.irm_pages_append.argtypes
         for name in EXPORTS:
             if name not in ("irm_status_string", "irm_last_error", "irm_version"):
                 getattr(L, name).restype = I
@@ -454,9 +461,9 @@ def tree_workspace_size(ctx: np.ndarray, q_indptr: np.ndarray, H: int) -> int:
 
 def irm_mla_attn_tree(q_lat, q_rope, ctx, q_indptr, paged_kv, page_table, tree_mask, softmax_scale=DEFAULT_SCALE,
                       out=None, lse=None, workspace=None, stream=None):
-    """Attention of drafted trees over the paged cache: q_lat [T, H, 512] / q_rope [T, H, 64] bf16 of
-    all nodes end to end, ctx [B] and q_indptr [B + 1] integers in host memory, paged_kv [n_pages, 64,
-    576] bf16, page_table [B, max_pages] int32, tree_mask [T, words] int32 (bit k of a row: the node
+    """Attention of drafted trees (or single tokens: trees of one node) over the paged cache: q_lat [T, H, 512]
+    / q_rope [T, H, 64] bf16 of all nodes end to end, ctx [B] and q_indptr [B + 1] integers in host memory,
+    paged_kv [n_pages, 64, 576] bf16 or, an 8-bit cache, [n_pages, 64, 656] uint8, page_table [B, max_pages] int32, tree_mask [T, words] int32 (bit k of a row: the node
     sees draft k).  Returns (out [T, H, 512] bf16, lse or None, workspace)."""
     ctx, q_indptr = _host_i32(ctx, "ctx"), _host_i32(q_indptr, "q_indptr")
     B = len(ctx)
@@ -468,7 +475,9 @@ def irm_mla_attn_tree(q_lat, q_rope, ctx, q_indptr, paged_kv, page_table, tree_m
     ql = _take(q_lat, torch.bfloat16, (T, H, 512), "q_lat", dev)
     n_pages, max_pages, words = _size(paged_kv, 0, "paged_kv"), _size(page_table, 1, "page_table"), _size(tree_mask, 1, "tree_mask")
     qr = _take(q_rope, torch.bfloat16, (T, H, 64), "q_rope", dev)
-    kv = _take(paged_kv, torch.bfloat16, (n_pages, 64, 576), "paged_kv", dev)
+    codes = paged_kv.dtype is torch.uint8
+    kv = (_take(paged_kv, torch.uint8, (n_pages, 64, ROW_BYTES8), "paged_kv", dev) if codes
+          else _take(paged_kv, torch.bfloat16, (n_pages, 64, 576), "paged_kv", dev))
     pt = _take(page_table, torch.int32, (B, max_pages), "page_table", dev)
     tm = _take(tree_mask, torch.int32, (T, words), "tree_mask", dev)
     if out is None:
@@ -477,7 +486,7 @@ def irm_mla_attn_tree(q_lat, q_rope, ctx, q_indptr, paged_kv, page_table, tree_m
     ls = None if lse is None else _take(lse, torch.float32, (T, H), "lse", dev)
     workspace, ws, ws_bytes = _take_workspace(workspace, lambda: tree_workspace_size(ctx, q_indptr, H), dev, stream)
     if T > 0:
-        _launch(lib().irm_mla_attn_tree, dev, stream, ql, qr, B, H, ctx.tobytes(), q_indptr.tobytes(), kv, n_pages, pt, max_pages,
+        _launch(lib().irm_mla_attn_tree8 if codes else lib().irm_mla_attn_tree, dev, stream, ql, qr, B, H, ctx.tobytes(), q_indptr.tobytes(), kv, n_pages, pt, max_pages,
                 tm, words, softmax_scale, o, ls, ws, ws_bytes)
     return out, lse, workspace
 
@@ -552,14 +561,16 @@ def _take_pages(seq_len, page_table, refcount):
 
 
 def _take_cache(kv, device, n_pages=None):
-    """[n_layers, n_pages, 64, 576] bf16, or one layer's [n_pages, 64, 576]: (address, layers, pages)."""
+    """[n_layers, n_pages, 64, 576] bf16 or, an 8-bit cache, [n_layers, n_pages, 64, 656] uint8, or one
+    layer's: (address, layers, pages, "" or the suffix of the 8-bit calls)."""
     if not isinstance(kv, torch.Tensor) or kv.dim() not in (3, 4):
-        raise ValueError("kv must be [n_layers, n_pages, 64, 576] or [n_pages, 64, 576]")
-    shape = kv.shape
+        raise ValueError("kv must be [n_layers, n_pages, 64, 576] or [n_pages, 64, 576] (an 8-bit cache: rows of 656 bytes)")
+    shape, codes = kv.shape, kv.dtype is torch.uint8
     pages = shape[-3] if n_pages is None else n_pages
     layers = shape[0] if len(shape) == 4 else 1
-    want = (layers, pages, 64, 576) if len(shape) == 4 else (pages, 64, 576)
-    return _take(kv, torch.bfloat16, want, "kv", device), layers, pages
+    row = ROW_BYTES8 if codes else 576
+    want = (layers, pages, 64, row) if len(shape) == 4 else (pages, 64, row)
+    return _take(kv, torch.uint8 if codes else torch.bfloat16, want, "kv", device), layers, pages, "8" if codes else ""
 
 
 def irm_pages_resize(new_len, seq_len, page_table, refcount, workspace=None, stream=None):
@@ -574,14 +585,15 @@ def irm_pages_resize(new_len, seq_len, page_table, refcount, workspace=None, str
 
 def irm_pages_fork(src, dst, kv, seq_len, page_table, refcount, workspace=None, stream=None):
     """Forks requests src into the empty slots dst (integers in host memory): full pages are shared, the
-    partly filled last page is copied in every layer of kv ([n_layers, n_pages, 64, 576] bf16)."""
+    partly filled last page is copied in every layer of kv ([n_layers, n_pages, 64, 576] bf16, or an 8-bit
+    cache's [n_layers, n_pages, 64, 656] uint8)."""
     src, dst = _host_i32(src, "src"), _host_i32(dst, "dst")
     if len(src) != len(dst):
         raise ValueError("src and dst must have the same length")
     dev, n_slots, max_pages, n_pages, sl, pt, rc = _take_pages(seq_len, page_table, refcount)
-    cache, layers, _ = _take_cache(kv, dev, n_pages)
+    cache, layers, _, eight = _take_cache(kv, dev, n_pages)
     workspace, ws, ws_bytes = _take_workspace(workspace, lambda: pages_workspace_size(n_slots), dev, stream)
-    _launch(lib().irm_pages_fork, dev, stream, src.tobytes(), dst.tobytes(), len(src), cache, layers, sl, n_slots, pt, max_pages,
+    _launch(getattr(lib(), "irm_pages_fork" + eight), dev, stream, src.tobytes(), dst.tobytes(), len(src), cache, layers, sl, n_slots, pt, max_pages,
             rc, n_pages, ws, ws_bytes)
     return workspace
 
@@ -591,13 +603,13 @@ def irm_pages_compact(kv, page_table, base, path, n_accept, workspace=None, stre
     n_accept [n_slots] and path [n_slots, max_path] int32 on the device (irm_tree_verify's outputs)."""
     max_pages, max_path = _size(page_table, 1, "page_table"), _size(path, 1, "path")
     dev, n_slots = page_table.device, page_table.shape[0]
-    cache, layers, n_pages = _take_cache(kv, dev)
+    cache, layers, n_pages, eight = _take_cache(kv, dev)
     pt = _take(page_table, torch.int32, (n_slots, max_pages), "page_table", dev)
     ba = _take(base, torch.int32, (n_slots,), "base", dev)
     pa = _take(path, torch.int32, (n_slots, max_path), "path", dev)
     na = _take(n_accept, torch.int32, (n_slots,), "n_accept", dev)
     workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
-    _launch(lib().irm_pages_compact, dev, stream, cache, layers, n_pages, pt, max_pages, n_slots, ba, pa, max_path, na, ws,
+    _launch(getattr(lib(), "irm_pages_compact" + eight), dev, stream, cache, layers, n_pages, pt, max_pages, n_slots, ba, pa, max_path, na, ws,
             ws_bytes)
     return workspace
 
@@ -609,8 +621,66 @@ def irm_pages_copy(kv, src, dst, stream=None):
         raise ValueError("src and dst must have the same length")
     if not isinstance(kv, torch.Tensor):
         raise ValueError("kv must be [n_layers, n_pages, 64, 576] or [n_pages, 64, 576]")
-    cache, layers, n_pages = _take_cache(kv, kv.device)
-    _launch(lib().irm_pages_copy, kv.device, stream, cache, layers, n_pages, src.tobytes(), dst.tobytes(), len(src))
+    cache, layers, n_pages, eight = _take_cache(kv, kv.device)
+    _launch(getattr(lib(), "irm_pages_copy" + eight), kv.device, stream, cache, layers, n_pages, src.tobytes(), dst.tobytes(), len(src))
+
+
+def _take_rows(t, width, name, device):
+    """(address, row stride, rows) of bf16 rows [T, width] that may lie in wider ones (each row contiguous, on 16 bytes)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-d torch.bfloat16 tensor on the GPU")
+    if t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows of {width}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width, t.shape[0]
+
+
+def irm_pages_append(c_kv, k_rope, kv, page_table, row, request=None, position=None, rope: Rope | None = None, factor=1.0,
+                     encoded=False, workspace=None, stream=None):
+    """New rows into one layer's pages, k_rope rotated on the way: c_kv [T, 512] and k_rope [T, 64] bf16 (rows may be
+    strided: columns of one projection's output), kv [n_pages, 64, 576] bf16 or, an 8-bit cache, [n_pages, 64,
+    656] uint8, page_table [n_slots, max_pages]; token t becomes row[t] of request[t] (t unless given) at
+    position[t] (row[t] unless given), int32 [T] on the device; a negative row is left out.  rope selects the
+    model's variant, factor its magnitude; encoded: k_rope is copied as it is.  Returns the workspace."""
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
+        raise ValueError("kv must be one layer's [n_pages, 64, 576] (an 8-bit cache: [n_pages, 64, 656] uint8)")
+    dev = kv.device
+    cache, _, n_pages, eight = _take_cache(kv, dev)
+    c, c_ld, T = _take_rows(c_kv, 512, "c_kv", dev)
+    k, k_ld, T_k = _take_rows(k_rope, 64, "k_rope", dev)
+    if T_k != T:
+        raise ValueError(f"c_kv has {T} rows, k_rope {T_k}")
+    n_slots, max_pages = _size(page_table, 0, "page_table"), _size(page_table, 1, "page_table")
+    pt = _take(page_table, torch.int32, (n_slots, max_pages), "page_table", dev)
+    ro = _take(row, torch.int32, (T,), "row", dev)
+    rq = None if request is None else _take(request, torch.int32, (T,), "request", dev)
+    po = None if position is None else _take(position, torch.int32, (T,), "position", dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
+    if T > 0:
+        _launch(getattr(lib(), "irm_pages_append" + eight), dev, stream, c, c_ld, k, k_ld, T, cache, n_pages, pt, n_slots, max_pages, ro,
+                rq, po, _rope_ptr(rope), factor, int(bool(encoded)), ws, ws_bytes)
+    return workspace
+
+
+def irm_rope_apply(x, position, rope: Rope | None = None, factor=1.0, out=None, stream=None):
+    """x [T, H, 64] bf16 turned by its positions (int32 [T] on the device) and multiplied by factor; x may be part of
+    wider heads (any strides of tokens and heads in multiples of 8, each row contiguous).  out: a tensor of that
+    shape, x itself for in place; a new contiguous one unless given.  Returns out."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.dim() != 3 or x.shape[2] != 64 or not x.is_cuda:
+        raise ValueError("x must be a [T, H, 64] torch.bfloat16 tensor on the GPU")
+    dev, (T, H) = x.device, x.shape[:2]
+    po = _take(position, torch.int32, (T,), "position", dev)
+    if out is None:
+        out = _make(lambda: torch.empty((T, H, 64), dtype=torch.bfloat16, device=dev), dev, stream)
+    elif not isinstance(out, torch.Tensor) or out.dtype is not torch.bfloat16 or out.shape != x.shape or out.device != dev:
+        raise ValueError(f"out must be a {tuple(x.shape)} torch.bfloat16 tensor on {dev}")
+    if x.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("x and out must have contiguous rows of 64")
+    if T > 0 and H > 0:
+        _launch(lib().irm_rope_apply, dev, stream, x.data_ptr(), x.stride(0), x.stride(1), T, H, po, _rope_ptr(rope), factor, out.data_ptr(),
+                out.stride(0), out.stride(1))
+    return out
 
 
 ASSEMBLE_S1 = 1

@@ -620,6 +620,7 @@ irm_status cdc_check(const int64_t* offsets_host, int n_streams, const irm_cdc_p
 namespace irm {
 // Sets the calling thread's last-error text (used by the registry's translation unit).
 void set_last_error(const char* msg) { g_last_error = msg; }
+irm_status select_rope(const irm_rope* rope, uint64_t* F, int* interleaved) { return rope_select(rope, F, interleaved); }
 }  // namespace irm
 
 extern "C" {

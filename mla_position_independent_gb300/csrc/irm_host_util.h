@@ -1,5 +1,5 @@
-// Host-side helpers of the entry points over the paged cache (tree attention, draft
-// verification, page operations): error text, CUDA errors, alignment.
+// Host-side helpers of the entry points over the paged cache (appending rows, tree attention,
+// sampling, draft verification, page operations): error text, CUDA errors, alignment.
 #pragma once
 #include <cstdarg>
 #include <cstdint>
@@ -11,6 +11,8 @@
 namespace irm {
 
 void set_last_error(const char* msg);  // irm_host.cu: the calling thread's irm_last_error()
+// irm_host.cu: phase steps [32] and pairing of a RoPE variant (NULL: the default), checked.
+irm_status select_rope(const irm_rope* rope, uint64_t* F, int* interleaved);
 
 inline irm_status fail(irm_status st, const char* fmt, ...) {
   char buf[512];

@@ -30,8 +30,10 @@ constexpr int kMaxSlots = 8192;
 constexpr int kMaxForks = 1024;
 constexpr int64_t kMaxEntries = int64_t(1) << 30;  // of a page table: all requests' pages are counted in int32
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kRowVec = kDRow * 2 / 16;        // 16-byte vectors of a row: 72
-constexpr int kPageVec = kRowVec * kPage;      // and of a page: 4608
+// 16-byte vectors of a row: 72 of a bf16 cache, 41 of an 8-bit one.  What moves rows is compiled for both,
+// since its loops and shares are in vectors.
+constexpr int kRowVec16 = kDRow * 2 / 16, kRowVec8 = IRM_ROW_BYTES8 / 16;
+static_assert(kRowVec16 * 16 == kDRow * 2 && kRowVec8 * 16 == IRM_ROW_BYTES8, "whole vectors");
 constexpr int kScanPages = 16;                 // counts one thread looks at per round of the scan
 
 __device__ __forceinline__ int pages_of(int rows) { return (rows + kPage - 1) / kPage; }
@@ -327,8 +329,10 @@ __device__ __forceinline__ void copy_vec(const uint4* src, uint4* dst, int n) {
 constexpr int kCopyThreads = 256;
 
 // grid (jobs, layers, parts): a part takes an equal share of the job's vectors
+template <int kRowVec>
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_jobs_kernel(uint4* kv, int64_t layer_vec,
                                                                        const CopyJob* __restrict__ jobs) {
+  constexpr int kPageVec = kRowVec * kPage;
   const CopyJob j = jobs[blockIdx.x];
   const int n = j.rows * kRowVec;
   const int lo = (int)((int64_t)n * blockIdx.z / gridDim.z), hi = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
@@ -344,7 +348,9 @@ struct CopyArgs {
 };
 static_assert(sizeof(CopyArgs) <= 32764, "kernel parameter block");
 
+template <int kRowVec>
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyArgs a) {
+  constexpr int kPageVec = kRowVec * kPage;
   const int lo = kPageVec / (int)gridDim.z * (int)blockIdx.z;  // 1, 2, 4, 8 or 16 parts: whole shares
   uint4* layer = a.kv + (int64_t)blockIdx.y * a.layer_vec;
   copy_vec(layer + (int64_t)a.src[blockIdx.x] * kPageVec + lo, layer + (int64_t)a.dst[blockIdx.x] * kPageVec + lo,
@@ -366,7 +372,9 @@ constexpr int kCompactLayers = 4;  // layers of one block
 // A thread owns one 16-byte column of a layer's rows, for all rows of the path: since path[k] >= k
 // and the path increases, moving k in order never overwrites a row that is still to be read,
 // and neither does a batch that is loaded before it is stored.
+template <int kRowVec>
 __global__ void __launch_bounds__(kCompactLayers * kRowVec) pages_compact_kernel(const CompactArgs a) {
+  constexpr int kPageVec = kRowVec * kPage;
   const int s = blockIdx.x;
   const int n = a.n_accept[s], base = a.base[s];
   const int32_t* path = a.path + (int64_t)s * a.max_path;
@@ -486,6 +494,88 @@ int copy_parts(int64_t blocks) {
   return parts;
 }
 
+template <int kRowVec>
+irm_status fork_rows(const int32_t* src_host, const int32_t* dst_host, int n_forks, void* kv, int n_layers,
+                     int32_t* seq_len, int n_slots, int32_t* page_table, int max_pages, int32_t* refcount,
+                     int64_t n_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  irm_status st = check_slots(n_slots, max_pages, n_pages);
+  if (st != IRM_OK) return st;
+  if (n_forks < 0 || n_forks > kMaxForks) return fail(IRM_ERR_UNSUPPORTED, "n_forks %d outside [0, %d]", n_forks, kMaxForks);
+  if ((n_forks > 0 && (!src_host || !dst_host)) || !seq_len || !page_table || !refcount)
+    return fail(IRM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(seq_len, 4) || !aligned(page_table, 4) || !aligned(refcount, 4))
+    return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
+  if ((st = check_cache(kv, n_layers)) != IRM_OK) return st;
+  if ((st = check_pairs(src_host, dst_host, n_forks, n_slots, "slot")) != IRM_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, workspace_need())) != IRM_OK) return st;
+  if (n_forks == 0) return IRM_OK;
+  ForkArgs a;
+  a.seq_len = seq_len;
+  a.n_slots = n_slots;
+  a.max_pages = max_pages;
+  a.n_forks = n_forks;
+  a.table = page_table;
+  a.refcount = refcount;
+  a.n_pages = n_pages;
+  a.jobs = reinterpret_cast<CopyJob*>(static_cast<uint8_t*>(workspace) + IRM_WORKSPACE_HEADER);
+  a.status = static_cast<int*>(workspace);
+  std::memcpy(a.src, src_host, (size_t)n_forks * sizeof(int32_t));
+  std::memcpy(a.dst, dst_host, (size_t)n_forks * sizeof(int32_t));
+  std::memset(a.src + n_forks, 0, (size_t)(kMaxForks - n_forks) * sizeof(int32_t));
+  std::memset(a.dst + n_forks, 0, (size_t)(kMaxForks - n_forks) * sizeof(int32_t));
+  pages_fork_kernel<<<1, kThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "page fork launch");
+  const dim3 grid((unsigned)n_forks, (unsigned)n_layers, (unsigned)copy_parts((int64_t)n_forks * n_layers));
+  pages_copy_jobs_kernel<kRowVec><<<grid, kCopyThreads, 0, stream>>>(static_cast<uint4*>(kv), n_pages * kRowVec * kPage, a.jobs);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? IRM_OK : cuda_fail(e, "page copy launch");
+}
+
+template <int kRowVec>
+irm_status compact_rows(void* kv, int n_layers, int64_t n_pages, const int32_t* page_table, int max_pages,
+                        int n_slots, const int32_t* base, const int32_t* path, int max_path,
+                        const int32_t* n_accept, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  irm_status st = check_slots(n_slots, max_pages, n_pages);
+  if (st != IRM_OK) return st;
+  if (max_path < 1) return fail(IRM_ERR_INVALID_ARG, "max_path must be positive");
+  if (!page_table || !base || !path || !n_accept) return fail(IRM_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned(page_table, 4) || !aligned(base, 4) || !aligned(path, 4) || !aligned(n_accept, 4))
+    return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
+  if ((st = check_cache(kv, n_layers)) != IRM_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, IRM_WORKSPACE_HEADER)) != IRM_OK) return st;
+  const CompactArgs a{static_cast<uint4*>(kv), n_layers, max_pages, max_path, n_pages, page_table, base, path, n_accept,
+                      static_cast<int*>(workspace)};
+  const dim3 grid((unsigned)n_slots, (unsigned)((n_layers + kCompactLayers - 1) / kCompactLayers));
+  pages_compact_kernel<kRowVec><<<grid, kCompactLayers * kRowVec, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? IRM_OK : cuda_fail(e, "page compaction launch");
+}
+
+template <int kRowVec>
+irm_status copy_rows(void* kv, int n_layers, int64_t n_pages, const int32_t* src_host, const int32_t* dst_host,
+                     int n, cudaStream_t stream) {
+  irm_status st = check_slots(1, 1, n_pages);
+  if (st != IRM_OK) return st;
+  if (n < 0) return fail(IRM_ERR_INVALID_ARG, "n must not be negative");
+  if (n > 0 && (!src_host || !dst_host)) return fail(IRM_ERR_INVALID_ARG, "null pointer");
+  if ((st = check_cache(kv, n_layers)) != IRM_OK) return st;
+  if ((st = check_pairs(src_host, dst_host, n, n_pages, "page")) != IRM_OK) return st;
+  thread_local CopyArgs a;  // 32 KB: kept off the stack
+  a.kv = static_cast<uint4*>(kv);
+  a.layer_vec = n_pages * kRowVec * kPage;
+  for (int i0 = 0; i0 < n; i0 += kCopyPairs) {
+    const int m = n - i0 < kCopyPairs ? n - i0 : kCopyPairs;
+    std::memcpy(a.src, src_host + i0, (size_t)m * sizeof(int32_t));
+    std::memcpy(a.dst, dst_host + i0, (size_t)m * sizeof(int32_t));
+    const dim3 grid((unsigned)m, (unsigned)n_layers, (unsigned)copy_parts((int64_t)m * n_layers));
+    pages_copy_kernel<kRowVec><<<grid, kCopyThreads, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
+  }
+  return IRM_OK;
+}
+
 }  // namespace
 }  // namespace irm
 
@@ -521,83 +611,36 @@ irm_status irm_pages_resize(const int32_t* new_len, int32_t* seq_len, int n_slot
 irm_status irm_pages_fork(const int32_t* src_host, const int32_t* dst_host, int n_forks, void* kv, int n_layers,
                           int32_t* seq_len, int n_slots, int32_t* page_table, int max_pages, int32_t* refcount,
                           int64_t n_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  using namespace irm;
-  irm_status st = check_slots(n_slots, max_pages, n_pages);
-  if (st != IRM_OK) return st;
-  if (n_forks < 0 || n_forks > kMaxForks) return fail(IRM_ERR_UNSUPPORTED, "n_forks %d outside [0, %d]", n_forks, kMaxForks);
-  if ((n_forks > 0 && (!src_host || !dst_host)) || !seq_len || !page_table || !refcount)
-    return fail(IRM_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(seq_len, 4) || !aligned(page_table, 4) || !aligned(refcount, 4))
-    return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
-  if ((st = check_cache(kv, n_layers)) != IRM_OK) return st;
-  if ((st = check_pairs(src_host, dst_host, n_forks, n_slots, "slot")) != IRM_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, workspace_need())) != IRM_OK) return st;
-  if (n_forks == 0) return IRM_OK;
-  ForkArgs a;
-  a.seq_len = seq_len;
-  a.n_slots = n_slots;
-  a.max_pages = max_pages;
-  a.n_forks = n_forks;
-  a.table = page_table;
-  a.refcount = refcount;
-  a.n_pages = n_pages;
-  a.jobs = reinterpret_cast<CopyJob*>(static_cast<uint8_t*>(workspace) + IRM_WORKSPACE_HEADER);
-  a.status = static_cast<int*>(workspace);
-  std::memcpy(a.src, src_host, (size_t)n_forks * sizeof(int32_t));
-  std::memcpy(a.dst, dst_host, (size_t)n_forks * sizeof(int32_t));
-  std::memset(a.src + n_forks, 0, (size_t)(kMaxForks - n_forks) * sizeof(int32_t));
-  std::memset(a.dst + n_forks, 0, (size_t)(kMaxForks - n_forks) * sizeof(int32_t));
-  pages_fork_kernel<<<1, kThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "page fork launch");
-  const dim3 grid((unsigned)n_forks, (unsigned)n_layers, (unsigned)copy_parts((int64_t)n_forks * n_layers));
-  pages_copy_jobs_kernel<<<grid, kCopyThreads, 0, stream>>>(static_cast<uint4*>(kv), n_pages * kPageVec, a.jobs);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? IRM_OK : cuda_fail(e, "page copy launch");
+  return irm::fork_rows<irm::kRowVec16>(src_host, dst_host, n_forks, kv, n_layers, seq_len, n_slots, page_table,
+                                        max_pages, refcount, n_pages, workspace, workspace_bytes, stream);
+}
+irm_status irm_pages_fork8(const int32_t* src_host, const int32_t* dst_host, int n_forks, void* kv, int n_layers,
+                           int32_t* seq_len, int n_slots, int32_t* page_table, int max_pages, int32_t* refcount,
+                           int64_t n_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return irm::fork_rows<irm::kRowVec8>(src_host, dst_host, n_forks, kv, n_layers, seq_len, n_slots, page_table,
+                                       max_pages, refcount, n_pages, workspace, workspace_bytes, stream);
 }
 
 irm_status irm_pages_compact(void* kv, int n_layers, int64_t n_pages, const int32_t* page_table, int max_pages,
                              int n_slots, const int32_t* base, const int32_t* path, int max_path,
                              const int32_t* n_accept, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  using namespace irm;
-  irm_status st = check_slots(n_slots, max_pages, n_pages);
-  if (st != IRM_OK) return st;
-  if (max_path < 1) return fail(IRM_ERR_INVALID_ARG, "max_path must be positive");
-  if (!page_table || !base || !path || !n_accept) return fail(IRM_ERR_INVALID_ARG, "null device pointer");
-  if (!aligned(page_table, 4) || !aligned(base, 4) || !aligned(path, 4) || !aligned(n_accept, 4))
-    return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
-  if ((st = check_cache(kv, n_layers)) != IRM_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, IRM_WORKSPACE_HEADER)) != IRM_OK) return st;
-  const CompactArgs a{static_cast<uint4*>(kv), n_layers, max_pages, max_path, n_pages, page_table, base, path, n_accept,
-                      static_cast<int*>(workspace)};
-  const dim3 grid((unsigned)n_slots, (unsigned)((n_layers + kCompactLayers - 1) / kCompactLayers));
-  pages_compact_kernel<<<grid, kCompactLayers * kRowVec, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? IRM_OK : cuda_fail(e, "page compaction launch");
+  return irm::compact_rows<irm::kRowVec16>(kv, n_layers, n_pages, page_table, max_pages, n_slots, base, path,
+                                           max_path, n_accept, workspace, workspace_bytes, stream);
+}
+irm_status irm_pages_compact8(void* kv, int n_layers, int64_t n_pages, const int32_t* page_table, int max_pages,
+                              int n_slots, const int32_t* base, const int32_t* path, int max_path,
+                              const int32_t* n_accept, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return irm::compact_rows<irm::kRowVec8>(kv, n_layers, n_pages, page_table, max_pages, n_slots, base, path,
+                                          max_path, n_accept, workspace, workspace_bytes, stream);
 }
 
 irm_status irm_pages_copy(void* kv, int n_layers, int64_t n_pages, const int32_t* src_host, const int32_t* dst_host,
                           int n, cudaStream_t stream) {
-  using namespace irm;
-  irm_status st = check_slots(1, 1, n_pages);
-  if (st != IRM_OK) return st;
-  if (n < 0) return fail(IRM_ERR_INVALID_ARG, "n must not be negative");
-  if (n > 0 && (!src_host || !dst_host)) return fail(IRM_ERR_INVALID_ARG, "null pointer");
-  if ((st = check_cache(kv, n_layers)) != IRM_OK) return st;
-  if ((st = check_pairs(src_host, dst_host, n, n_pages, "page")) != IRM_OK) return st;
-  thread_local CopyArgs a;  // 32 KB: kept off the stack
-  a.kv = static_cast<uint4*>(kv);
-  a.layer_vec = n_pages * kPageVec;
-  for (int i0 = 0; i0 < n; i0 += kCopyPairs) {
-    const int m = n - i0 < kCopyPairs ? n - i0 : kCopyPairs;
-    std::memcpy(a.src, src_host + i0, (size_t)m * sizeof(int32_t));
-    std::memcpy(a.dst, dst_host + i0, (size_t)m * sizeof(int32_t));
-    const dim3 grid((unsigned)m, (unsigned)n_layers, (unsigned)copy_parts((int64_t)m * n_layers));
-    pages_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
-  }
-  return IRM_OK;
+  return irm::copy_rows<irm::kRowVec16>(kv, n_layers, n_pages, src_host, dst_host, n, stream);
+}
+irm_status irm_pages_copy8(void* kv, int n_layers, int64_t n_pages, const int32_t* src_host, const int32_t* dst_host,
+                           int n, cudaStream_t stream) {
+  return irm::copy_rows<irm::kRowVec8>(kv, n_layers, n_pages, src_host, dst_host, n, stream);
 }
 
 }  // extern "C"

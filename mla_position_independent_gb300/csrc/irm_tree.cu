@@ -72,15 +72,14 @@ constexpr int kBM = 128;     // query rows of a unit
 constexpr int kHalf = 64;    // of which a CTA owns
 constexpr int kScoreWarps = 8;
 constexpr int kTmaWarp = 8, kSWarp = 9, kPvWarp = 10, kClearWarp = 11;
-constexpr int kThreads = 12 * 32;
+constexpr int kConvWarp = 12, kConvWarps = 4;  // of an 8-bit cache
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Shared memory: barriers and small arrays, then 1024-byte aligned tiles.
-constexpr int kStages = 5;
 constexpr uint32_t kSlab = 64 * 128;                  // 64 rows x 64 columns
 constexpr uint32_t kStage = 4 * kSlab;                // the cKV columns of a page
-constexpr uint32_t kRing = kStages * kSlab;           // pages in turn, for each 64 columns
+constexpr uint32_t kCodes = 64 * 256;                 // and their codes, two boxes of 128 columns
 constexpr uint32_t kKr = 64 * 64;                     // and its 32 k_r columns, which only Q K^T needs
 constexpr uint32_t kXBytes = kHalf * kPage * 4;       // received scores of one tile
 constexpr uint32_t kPBytes = kBM * 128;               // P of one tile
@@ -98,17 +97,10 @@ constexpr uint32_t kOffX = kOffQr + 128 * 64;         // 16-byte words [16][64 r
 constexpr uint32_t kOffKr = kOffX + kXBytes;          // [2]
 constexpr uint32_t kOffP = kOffKr + 2 * kKr;
 constexpr uint32_t kOffKv = kOffP + 2 * kPBytes;
-constexpr uint32_t kOffQl = kOffKv + 2 * kSlab;       // 4 slabs of Q's cKV columns at the start, in stages 2 and 3
-constexpr uint32_t kSmem = kOffKv + kStages * kStage + 1024;  // room to align the base
-static_assert(kBM * 128 <= 2 * kSlab && kStages >= 4, "Q's place");
 static_assert(kOffCorr + 4 * 64 * 4 <= kOffQr && kOffQr % 1024 == 0 && kOffKr % 1024 == 0 && kOffP % 1024 == 0, "layout");
-static_assert(kSmem <= 232448, "shared memory");
 
 enum : int {
-  BAR_LANDED = 0,                    // [stage] TMA bytes of the page (1 + tx)
-  BAR_CLEAR = BAR_LANDED + kStages,  // [stage] unseen rows cleared for P V (pages with drafts only)
-  BAR_FREE = BAR_CLEAR + kStages,    // [stage] P V of the page done, and the clearing warp past it (2)
-  BAR_S_FULL = BAR_FREE + kStages,   // [2] Q K^T done
+  BAR_S_FULL = 0,                    // [2] Q K^T done
   BAR_S_FREE = BAR_S_FULL + 2,       // [2] the set's live warps read the score buffer
   BAR_X_FULL = BAR_S_FREE + 2,       // [2][32 rows] the peer's partial scores arrived, keys 32 to 63 (1 + tx)
   BAR_X_FREE = BAR_X_FULL + 4,       // [2][32 rows] the peer's warp has read what was sent
@@ -123,9 +115,30 @@ enum : int {
   BAR_INV = BAR_Q + 1,               // the peer rows' 1 / l arrived (1 + tx)
   BAR_DRAIN = BAR_INV + 1,           // [2] all UMMAs of an issuer done
   BAR_X_HALF = BAR_DRAIN + 2,        // [2][32 rows] the peer's partial scores, keys 0 to 31 (1 + tx)
-  NUM_BARS = BAR_X_HALF + 4,
+  BAR_LANDED = BAR_X_HALF + 4,       // [stage] TMA bytes of the page (1 + tx); 8-bit: its cKV is there as bf16 (4 warps)
 };
-static_assert(NUM_BARS * 8 <= kOffTmem, "barrier area");
+
+// What depends on the cache's type: pages in shared memory, and the barriers of their ring.
+template <bool kCodes8>
+struct Layout {
+  static constexpr int kThreads = (kCodes8 ? 16 : 12) * 32;
+  static constexpr int kStages = kCodes8 ? 3 : 5;  // pages of bf16
+  static constexpr int kRaw = kCodes8 ? 4 : 0;     // pages of codes
+  static constexpr uint32_t kRing = kStages * kSlab;  // pages in turn, for each 64 columns
+  static constexpr int kQStage = kCodes8 ? 1 : 2;     // 4 slabs of Q's cKV columns at the start, in this stage and the next
+  static constexpr uint32_t kOffQl = kOffKv + kQStage * kSlab;
+  static constexpr uint32_t kOffRaw = kOffKv + kStages * kStage;
+  static constexpr uint32_t kSmem = kOffRaw + kRaw * kCodes + 1024;  // room to align the base
+  static constexpr int BAR_FREE = BAR_LANDED + kStages;    // [stage] P V of the page done; bf16: and the clearing warp past it (2)
+  static constexpr int BAR_CLEAR = BAR_FREE + kStages;     // bf16: [stage] unseen rows cleared for P V (pages with drafts only)
+  static constexpr int BAR_RAW_FULL = BAR_FREE + kStages;  // 8-bit: [raw] TMA bytes of the codes (1 + tx)
+  static constexpr int BAR_RAW_FREE = BAR_RAW_FULL + kRaw; // [raw] codes read (4 warps)
+  static constexpr int BAR_KR = BAR_RAW_FREE + kRaw;       // [2] TMA bytes of k_r (1 + tx)
+  static constexpr int kBars = kCodes8 ? BAR_KR + 2 : BAR_CLEAR + kStages;
+  static_assert(kBM * 128 <= 2 * kSlab && kStages >= kQStage + 2, "Q's place");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kBars * 8 <= kOffTmem, "barrier area");
+};
 
 constexpr uint32_t kTmemO = 0, kTmemQ = 256, kTmemS = 384, kTmemCols = 512;
 constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kPage, 0, 0);
@@ -138,10 +151,13 @@ struct Request {
 };
 
 struct TreeArgs {
-  CUtensorMap map_lat, map_rope;  // pages [rows, 576]: boxes of 64 x 64, and of 64 rows x 32 columns
+  // pages [rows, 576]: boxes of 64 x 64, and of 64 rows x 32 columns; 8-bit [rows, 656 bytes]: of 64 rows x 128
+  // bytes, and of 64 rows x 32 columns of k_r
+  CUtensorMap map_lat, map_rope;
   CUtensorMap map_ql, map_qr;     // queries [T H, 512] and [T H, 64]: boxes of 32 rows x 64, and x 32 columns
   const int32_t* page_table;
   const uint32_t* mask;
+  const uint8_t* kv8;  // 8-bit: the pages, for their scales
   int64_t n_pages;
   int B, b0, H, max_pages, mask_words;
   int piece;   // pages of a piece
@@ -229,8 +245,27 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float corr) {
   tmem_st_wait();
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// Four e4m3 codes as bf16 times the scale (a pair of bf16, 2^120 times the scale of the codes): a code's
+// sign and 7 bits, put where bf16 has sign, low exponent bits and first mantissa bits, are its value
+// times 2^-120, denormals included.
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, __nv_bfloat162 scale) {
+  uint32_t r[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t t = __byte_perm(w, 0u, h ? 0x3424 : 0x1404);
+    const uint32_t u = (t >> 4 & 0x07f007f0u) | (t & 0x80008000u);
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), scale);
+    r[h] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+template <bool kCodes8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TreeArgs a) {
+  using L = Layout<kCodes8>;
+  constexpr int kStages = L::kStages, kRaw = kCodes8 ? L::kRaw : 1, BAR_FREE = L::BAR_FREE;
+  constexpr uint32_t kRing = L::kRing, kOffQl = L::kOffQl;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // alike in both CTAs
   const uint32_t sb = smem_u32(smem);
@@ -264,9 +299,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(BAR_LANDED + s), 1);
-      mbar_init(bar(BAR_CLEAR + s), 1);
-      mbar_init(bar(BAR_FREE + s), 2);
+      mbar_init(bar(BAR_LANDED + s), kCodes8 ? kConvWarps : 1);
+      mbar_init(bar(BAR_FREE + s), kCodes8 ? 1 : 2);
+      if (!kCodes8) mbar_init(bar(L::BAR_CLEAR + s), 1);
+    }
+    if (kCodes8) {
+      for (int s = 0; s < kRaw; ++s) {
+        mbar_init(bar(L::BAR_RAW_FULL + s), 1);
+        mbar_init(bar(L::BAR_RAW_FREE + s), kConvWarps);
+      }
+      for (int s = 0; s < 2; ++s) mbar_init(bar(L::BAR_KR + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(BAR_S_FULL + s), 1);
@@ -300,8 +342,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // what the first copies need, on its way during the set-up
   const int32_t* ptab = a.page_table + (int64_t)(a.b0 + b) * a.max_pages + kb;
   int page0 = 0;
-  if (warp == kTmaWarp) {
+  if (warp == kTmaWarp || (kCodes8 && warp == kClearWarp)) {
     if (lane < ntiles) page0 = ptab[lane];
+  }
+  if (warp == kTmaWarp) {
     if (lane == 0) {
       tma_prefetch_map(&a.map_lat);
       tma_prefetch_map(&a.map_rope);
@@ -529,6 +573,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       const int y = __shfl_sync(kFull, page, j & 31) * kPage;
+      if constexpr (kCodes8) {
+        const int r = j % kRaw;
+        if (j >= kRaw && !(ok = warp_wait(bar(L::BAR_RAW_FREE + r), ((uint32_t)(j / kRaw) & 1u) ^ 1u, abort_flag))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::BAR_RAW_FULL + r), kCodes);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            tma_load_2d(sb + L::kOffRaw + (uint32_t)r * kCodes + c * kSlab, &a.map_lat, 256 * rank + 128 * c, y, bar(L::BAR_RAW_FULL + r));
+        }
+        sent = j + 1;
+        continue;
+      }
       const int s = j % kStages;
       // stages 2 and 3 hold Q until it is in TMEM
       if (j == 2 && !(ok = warp_wait(bar(BAR_Q), 0, abort_flag))) break;
@@ -546,8 +602,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     // the copies in flight land before the CTA ends, whatever became of the others
     ok = warp_wait(bar(BAR_QIN), 0, nullptr) && ok;
-    for (int j = max(0, sent - kStages); j < sent; ++j)
-      ok = warp_wait(bar(BAR_LANDED + j % kStages), (uint32_t)(j / kStages) & 1u, nullptr) && ok;
+    constexpr int kFlight = kCodes8 ? kRaw : kStages, kBar = kCodes8 ? L::BAR_RAW_FULL : BAR_LANDED;
+    for (int j = max(0, sent - kFlight); j < sent; ++j)
+      ok = warp_wait(bar(kBar + j % kFlight), (uint32_t)(j / kFlight) & 1u, nullptr) && ok;
     __syncwarp();
     cluster_wait();
   } else if (warp == kSWarp) {
@@ -559,6 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
         if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+        if (kCodes8 && !(ok = mbar_wait(bar(L::BAR_KR + set), (uint32_t)(j >> 1) & 1u, abort_flag))) break;
         if (j >= 2 && !(ok = mbar_wait(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
@@ -585,8 +643,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
-        if (j >= tail) {
-          if (!(ok = mbar_wait(bar(BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
+        if (!kCodes8 && j >= tail) {
+          if (!(ok = mbar_wait(bar(L::BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
           fence_proxy_async_smem();  // the cleared rows' plain stores
         }
         if (live_own && !(ok = mbar_wait(bar(BAR_GO + set), ph, abort_flag))) break;
@@ -618,6 +676,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_wait();
+  } else if (kCodes8 && warp >= kConvWarp) {
+    // ================= codes to bf16: a thread a row of 128 columns =================
+    const int r = (warp & 1) * 32 + lane, box = (warp - kConvWarp) >> 1;
+    const int node0 = row0 / a.H, node1 = (row0 + rows_valid - 1) / a.H;
+    const uint8_t* scales = a.kv8 + (int64_t)r * IRM_ROW_BYTES8 + IRM_ROW8_SCALES + 4 * (2 * rank + box);
+    // a page's scale is read one page ahead, its index two (a page outside the cache reads as zeros)
+    auto page_at = [&](int j) -> int { return j < ntiles ? ptab[j] : -1; };
+    auto scale_of = [&](int page) -> uint32_t {
+      return page >= 0 && page < a.n_pages ? __ldg(reinterpret_cast<const uint32_t*>(scales + (int64_t)page * (kPage * IRM_ROW_BYTES8))) : 0u;
+    };
+    uint32_t next = scale_of(page_at(0));
+    int page = page_at(1);
+    for (int j = 0; j < ntiles; ++j) {
+      const int raw = j % kRaw, s = j % kStages;
+      const uint32_t scale = next;
+      next = scale_of(page);
+      page = page_at(j + 2);
+      bool seen = true;
+      if (j >= tail) {  // rows that no node of the unit sees become zeros
+        uint64_t see = 0;
+        for (int i = node0 + lane; i <= node1; i += 32)
+          see |= seen_rows(a.mask + (int64_t)(first_node + i) * a.mask_words, a.mask_words, (kb + j) * kPage, ctx, n);
+        const uint32_t lo = __reduce_or_sync(kFull, (uint32_t)see), hi = __reduce_or_sync(kFull, (uint32_t)(see >> 32));
+        seen = ((warp & 1 ? hi : lo) >> lane & 1u) != 0;
+      }
+      if (!(ok = warp_wait(bar(L::BAR_RAW_FULL + raw), (uint32_t)(j / kRaw) & 1u, abort_flag))) break;
+      uint4 v[8];
+      const uint8_t* from = smem + L::kOffRaw + (uint32_t)raw * kCodes + (uint32_t)box * kSlab;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(from + sw128_offset((uint32_t)r, (uint32_t)i));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::BAR_RAW_FREE + raw));
+      // the second and third page's places hold Q until it is in TMEM
+      if (j == L::kQStage && !(ok = warp_wait(bar(BAR_Q), 0, abort_flag))) break;
+      if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
+      const __nv_bfloat162 m = __float2bfloat162_rn(__uint_as_float(scale & 0xffff0000u) * 0x1p120f);
+      const uint32_t to = sb + kOffKv + (uint32_t)(2 * box) * kRing + (uint32_t)s * kSlab;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint2 a0 = codes_to_bf16(v[i].x, m), a1 = codes_to_bf16(v[i].y, m), a2 = codes_to_bf16(v[i].z, m), a3 = codes_to_bf16(v[i].w, m);
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t at = to + (uint32_t)(i >> 2) * kRing;
+        st_shared_v4(at + sw128_offset((uint32_t)r, (uint32_t)(2 * i & 7)), seen ? make_uint4(a0.x, a0.y, a1.x, a1.y) : zero);
+        st_shared_v4(at + sw128_offset((uint32_t)r, (uint32_t)(2 * i & 7) + 1u), seen ? make_uint4(a2.x, a2.y, a3.x, a3.y) : zero);
+      }
+      fence_proxy_async_smem();  // read by the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_LANDED + s));
+    }
+    __syncwarp();
+    cluster_wait();
   } else if (warp == kClearWarp) {
     // ================= Q in =================
     if (lane == 0) {
@@ -632,6 +741,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    if constexpr (kCodes8) {
+      // ================= k_r in =================
+      int page = 0, sent = 0;
+      for (int j = 0; j < ntiles; ++j) {
+        if ((j & 31) == 0) {
+          page = j == 0 ? page0 : j + lane < ntiles ? ptab[j + lane] : 0;
+          if (page < 0 || page >= a.n_pages) page = (int)a.n_pages;  // recorded by the other copying warp
+        }
+        const int y = __shfl_sync(kFull, page, j & 31) * kPage;
+        // the buffer's last page has been through Q K^T
+        if (j >= 2 && !(ok = warp_wait(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::BAR_KR + (j & 1)), kKr);
+          tma_load_2d(sb + kOffKr + (uint32_t)(j & 1) * kKr, &a.map_rope, IRM_ROW8_ROPE / 2 + 32 * rank, y, bar(L::BAR_KR + (j & 1)));
+        }
+        sent = j + 1;
+      }
+      for (int j = max(0, sent - 2); j < sent; ++j) ok = warp_wait(bar(L::BAR_KR + (j & 1)), (uint32_t)(j >> 1) & 1u, nullptr) && ok;
+    } else {
     // ================= rows that no node of the unit sees become zeros =================
     const int node0 = row0 / a.H, node1 = (row0 + rows_valid - 1) / a.H;
     for (int j = 0; j < ntiles; ++j) {
@@ -655,10 +783,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_CLEAR + s));
+        if (lane == 0) mbar_arrive(bar(L::BAR_CLEAR + s));
       }
       // every page is waited for, and given back, so that no phase is missed
       if (lane == 0) mbar_arrive(bar(BAR_FREE + s));
+    }
     }
     __syncwarp();
     cluster_wait();
@@ -1018,19 +1147,22 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map of `rows` rows of `width` bf16: boxes of box_rows x box_cols, as wide as the swizzle.
+// Map of `rows` rows of `width` elements: boxes of box_rows x box_cols, as wide as the swizzle.
+template <class T>
 irm_status encode_map(CUtensorMap* m, const void* base, int64_t rows, int width, uint32_t box_rows, uint32_t box_cols) {
+  constexpr bool kBytes = sizeof(T) == 1;
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return fail(IRM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * sizeof(T)};
   const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+  const CUresult r = fn(m, kBytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols * sizeof(T) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? IRM_OK : fail(IRM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
 // The kernel's dynamic shared memory limit belongs to the device: raised once on each.
+template <bool kCodes8>
 cudaError_t raise_smem_limit() {
   static std::mutex mu;
   static bool done[128];
@@ -1039,35 +1171,17 @@ cudaError_t raise_smem_limit() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
   if (dev >= 0 && dev < 128 && done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  e = cudaFuncSetAttribute(tree_attn_kernel<kCodes8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<kCodes8>::kSmem);
   if (e == cudaSuccess && dev >= 0 && dev < 128) done[dev] = true;
   return e;
 }
 
-}  // namespace
-}  // namespace irm
-
-extern "C" {
-
-irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32_t* q_indptr_host, int B, int H,
-                                            size_t* bytes) {
-  using namespace irm;
-  if (bytes == nullptr) return fail(IRM_ERR_INVALID_ARG, "bytes is null");
-  int nodes = 0;
-  int64_t rows = 0;
-  const irm_status st = check_lengths(ctx_host, q_indptr_host, B, H, &nodes, &rows);
-  if (st != IRM_OK) return st;
-  Plan first;
-  *bytes = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H, sm_pairs(), &first);
-  return IRM_OK;
-}
-
-irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H, const int32_t* ctx_host,
-                             const int32_t* q_indptr_host, const void* paged_kv, int64_t n_pages,
-                             const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
-                             float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                             cudaStream_t stream) {
-  using namespace irm;
+template <bool kCodes8>
+irm_status attend(const void* q_lat, const void* q_rope, int B, int H, const int32_t* ctx_host,
+                  const int32_t* q_indptr_host, const void* paged_kv, int64_t n_pages,
+                  const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
+                  float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream) {
   int nodes = 0;
   int64_t rows = 0;
   irm_status st = check_lengths(ctx_host, q_indptr_host, B, H, &nodes, &rows);
@@ -1094,11 +1208,19 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
   if (q_indptr_host[B] == 0) return IRM_OK;
   TreeArgs a{};
   const int64_t q_rows = (int64_t)q_indptr_host[B] * H;
-  if ((st = encode_map(&a.map_lat, paged_kv, n_pages * kPage, kDRow, kPage, 64)) != IRM_OK) return st;
-  if ((st = encode_map(&a.map_rope, paged_kv, n_pages * kPage, kDRow, kPage, 32)) != IRM_OK) return st;
-  if ((st = encode_map(&a.map_ql, q_lat, q_rows, kDLat, 32, 64)) != IRM_OK) return st;
-  if ((st = encode_map(&a.map_qr, q_rope, q_rows, kDRope, 32, 32)) != IRM_OK) return st;
-  cudaError_t e = raise_smem_limit();
+  const int64_t kv_rows = n_pages * kPage;
+  if (kCodes8) {
+    st = encode_map<uint8_t>(&a.map_lat, paged_kv, kv_rows, IRM_ROW_BYTES8, kPage, 128);
+    if (st == IRM_OK) st = encode_map<uint16_t>(&a.map_rope, paged_kv, kv_rows, IRM_ROW_BYTES8 / 2, kPage, 32);
+    a.kv8 = static_cast<const uint8_t*>(paged_kv);
+  } else {
+    st = encode_map<uint16_t>(&a.map_lat, paged_kv, kv_rows, kDRow, kPage, 64);
+    if (st == IRM_OK) st = encode_map<uint16_t>(&a.map_rope, paged_kv, kv_rows, kDRow, kPage, 32);
+  }
+  if (st != IRM_OK) return st;
+  if ((st = encode_map<uint16_t>(&a.map_ql, q_lat, q_rows, kDLat, 32, 64)) != IRM_OK) return st;
+  if ((st = encode_map<uint16_t>(&a.map_qr, q_rope, q_rows, kDRope, 32, 32)) != IRM_OK) return st;
+  cudaError_t e = raise_smem_limit<kCodes8>();
   if (e != cudaSuccess) return cuda_fail(e, "tree attention set-up");
   a.page_table = page_table;
   a.mask = tree_mask;
@@ -1133,7 +1255,7 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     uint8_t* ws = static_cast<uint8_t*>(workspace) + IRM_WORKSPACE_HEADER;
     a.opart = reinterpret_cast<float*>(ws);
     a.lsepart = reinterpret_cast<float*>(ws + opart_bytes(p.parts));
-    tree_attn_kernel<<<2 * units, kThreads, kSmem, stream>>>(a);
+    tree_attn_kernel<kCodes8><<<2 * units, Layout<kCodes8>::kThreads, Layout<kCodes8>::kSmem, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tree attention launch");
     if (p.parts) {
       cudaLaunchConfig_t cfg = {};
@@ -1152,6 +1274,42 @@ irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H
     }
   }
   return IRM_OK;
+}
+
+}  // namespace
+}  // namespace irm
+
+extern "C" {
+
+irm_status irm_mla_attn_tree_workspace_size(const int32_t* ctx_host, const int32_t* q_indptr_host, int B, int H,
+                                            size_t* bytes) {
+  using namespace irm;
+  if (bytes == nullptr) return fail(IRM_ERR_INVALID_ARG, "bytes is null");
+  int nodes = 0;
+  int64_t rows = 0;
+  const irm_status st = check_lengths(ctx_host, q_indptr_host, B, H, &nodes, &rows);
+  if (st != IRM_OK) return st;
+  Plan first;
+  *bytes = IRM_WORKSPACE_HEADER + scratch_bytes(ctx_host, q_indptr_host, B, H, sm_pairs(), &first);
+  return IRM_OK;
+}
+
+irm_status irm_mla_attn_tree(const void* q_lat, const void* q_rope, int B, int H, const int32_t* ctx_host,
+                             const int32_t* q_indptr_host, const void* paged_kv, int64_t n_pages,
+                             const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
+                             float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  return irm::attend<false>(q_lat, q_rope, B, H, ctx_host, q_indptr_host, paged_kv, n_pages, page_table, max_pages, tree_mask, mask_words,
+                             softmax_scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+irm_status irm_mla_attn_tree8(const void* q_lat, const void* q_rope, int B, int H, const int32_t* ctx_host,
+                              const int32_t* q_indptr_host, const void* paged_kv, int64_t n_pages,
+                              const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
+                              float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+  return irm::attend<true>(q_lat, q_rope, B, H, ctx_host, q_indptr_host, paged_kv, n_pages, page_table, max_pages, tree_mask, mask_words,
+                            softmax_scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
