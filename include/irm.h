@@ -303,7 +303,8 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  * Decoding over the paged cache, token by token or speculatively.  The calls below work on 64-row
  * pages, the layout irm_assemble_kv writes, and make up one step: irm_pages_resize makes room for
  * the new tokens or drafts, irm_rope_apply encodes their queries and irm_pages_append their
- * rows, irm_mla_attn_tree attends (these once a layer); for drafts, irm_tree_verify accepts a path and draws the
+ * rows, irm_mla_attn_tree attends (these once a layer), irm_sample draws the next token; or, for
+ * drafts, irm_sample turns logits into probabilities, irm_tree_verify accepts a path and draws the
  * next token, irm_pages_compact moves the path's rows up, and irm_pages_resize gives the rest back.
  *
  * A request's tree has n nodes, numbered so that a parent comes before its children; node 0
@@ -419,6 +420,36 @@ irm_status irm_mla_attn_tree8(const void* q_lat, const void* q_rope, int B, int 
                               const int32_t* page_table, int max_pages, const uint32_t* tree_mask, int mask_words,
                               float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                               cudaStream_t stream);
+
+/*
+ * Sampling from logits, from given uniform numbers; its probabilities are what irm_tree_verify takes.
+ * For every row: candidates in the order of their logits, the highest first, ties by the lowest index;
+ *   w_v = exp((l_v - max l) / temperature)
+ *   top-k:  the first top_k candidates stay
+ *   top-p:  of those, the shortest run from the first on whose w reach top_p of their sum
+ *   min-p:  of those, the ones with w >= min_p (the first has w = 1)
+ *   probs   = w / sum w over those left, 0 elsewhere
+ *   token   = the lowest v with cumsum(w)(v) > uniform * sum(w), in index order over those left
+ *
+ *   logits   device fp32 or bf16 (logits_type IRM_FP32 / IRM_BF16), row t at t * row_stride
+ *            elements; 4-byte (bf16: 2-byte) aligned.  NaN counts as -infinity; -infinity has w = 0;
+ *            where +infinity occurs those entries have w = 1 and all others 0.
+ *   temperature, top_p, min_p  device fp32 [n_rows], top_k device int32 [n_rows]; each may be NULL.
+ *            temperature NULL: 1; 0, negative or NaN: the first candidate alone.  top_k <= 0, top_p
+ *            >= 1 or NaN, min_p <= 0 or NaN: no cut.  The first candidate always stays.
+ *   uniforms device fp32 [n_rows] in [0, 1); needed for token
+ *   token    device int32 [n_rows] or NULL; -1 for a row without a finite or +infinite logit
+ *   probs    device fp32, row t at t * probs_stride, or NULL (one of the two is needed); such a row's
+ *            are zeros
+ * Weights are held in units of 2^-43 of the largest and summed as integers, so that nothing depends on
+ * the order of addition.  logits and probs must not overlap.  vocab at most 2^20, n_rows below 2^28.  Workspace: IRM_WORKSPACE_HEADER bytes (status word).
+ */
+#define IRM_FP32 0
+#define IRM_BF16 1
+irm_status irm_sample(const void* logits, int logits_type, int64_t row_stride, int64_t n_rows, int32_t vocab,
+                      const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                      const float* uniforms, int32_t* token, float* probs, int64_t probs_stride, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Verification of a batch's trees against the target's probabilities, from given uniform

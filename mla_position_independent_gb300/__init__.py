@@ -11,7 +11,7 @@ from .binding import (CDC_LOW_BITS, CDC_THRESHOLD, ROPE_INTERLEAVED, ROPE_NEOX, 
                       device_status, irm_assemble_kv, irm_mla_attn_decode,
                       irm_mla_attn_decode_noalloc, irm_mla_attn_prefill, irm_mla_attn_tree,
                       irm_pages_append, irm_pages_compact, irm_pages_copy, irm_pages_fork, irm_pages_resize,
-                      irm_rope_apply, irm_tree_verify,
+                      irm_rope_apply, irm_sample, irm_tree_verify,
                       lib, new_workspace, pages_workspace_size, prefill_workspace_size,
                       ROW_BYTES8, selftest_wait_timeout, tree_workspace_size, validate_chunks, WORKSPACE_HEADER)
 
@@ -20,6 +20,6 @@ __all__ = ["Registry", "CDC_LOW_BITS", "CDC_THRESHOLD", "CdcParams", "cdc_sizes"
            "assemble_kv_workspace_size", "decode_noalloc_status", "decode_workspace_size",
            "device_status", "irm_assemble_kv", "irm_mla_attn_decode", "irm_mla_attn_decode_noalloc",
            "irm_mla_attn_prefill", "irm_mla_attn_tree", "irm_pages_compact", "irm_pages_copy",
-           "irm_pages_append", "irm_pages_fork", "irm_pages_resize", "irm_rope_apply", "irm_tree_verify", "pages_workspace_size",
+           "irm_pages_append", "irm_pages_fork", "irm_pages_resize", "irm_rope_apply", "irm_sample", "irm_tree_verify", "pages_workspace_size",
            "tree_workspace_size", "ROW_BYTES8", "WORKSPACE_HEADER",
            "lib", "new_workspace", "prefill_workspace_size", "selftest_wait_timeout", "validate_chunks"]

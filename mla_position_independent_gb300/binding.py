@@ -31,7 +31,7 @@ EXPORTS = ["irm_status_string", "irm_last_error", "irm_version", "irm_validate_c
            "irm_registry_assemble", "irm_selftest_wait_timeout", "irm_mla_attn_tree_workspace_size",
            "irm_mla_attn_tree", "irm_tree_verify", "irm_pages_workspace_size", "irm_pages_resize",
            "irm_pages_fork", "irm_pages_compact", "irm_pages_copy", "irm_mla_attn_tree8", "irm_pages_fork8",
-           "irm_pages_compact8", "irm_pages_copy8", "irm_rope_apply", "irm_pages_append", "irm_pages_append8"]
+           "irm_pages_compact8", "irm_pages_copy8", "irm_rope_apply", "irm_pages_append", "irm_pages_append8", "irm_sample"]
 
 ROPE_NEOX, ROPE_INTERLEAVED = 0, 1
 
@@ -121,6 +121,7 @@ def lib():
         L.irm_rope_apply.argtypes = [P, I64, I64, I64, I, P, P, ctypes.c_float, P, I64, I64, P]
         L.irm_pages_append.argtypes = [P, I64, P, I64, I64, P, I64, P, I, I, P, P, P, P, ctypes.c_float, I, P, SZ, P]
         L.irm_pages_append8.argtypes = L.irm_pages_append.argtypes
+        L.irm_sample.argtypes = [P, I, I64, I64, ctypes.c_int32, P, P, P, P, P, P, P, I64, P, SZ, P]
         for name in EXPORTS:
             if name not in ("irm_status_string", "irm_last_error", "irm_version"):
                 getattr(L, name).restype = I
@@ -678,9 +679,45 @@ def irm_rope_apply(x, position, rope: Rope | None = None, factor=1.0, out=None, 
     if x.stride(2) != 1 or out.stride(2) != 1:
         raise ValueError("x and out must have contiguous rows of 64")
     if T > 0 and H > 0:
-        _launch(lib().irm_rope_apply, dev, stream, x.data_ptr(), x.stride(0), x.stride(1), T, H, po, _rope_ptr(rope), factor, out.data_ptr(),
-                out.stride(0), out.stride(1))
+        (xt, xh), (ot, oh) = ((t.stride(0) if T > 1 else 64, t.stride(1) if H > 1 else 64) for t in (x, out))
+        _launch(lib().irm_rope_apply, dev, stream, x.data_ptr(), xt, xh, T, H, po, _rope_ptr(rope), factor, out.data_ptr(), ot, oh)
     return out
+
+
+def irm_sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, token=None, workspace=None,
+               stream=None):
+    """Sampling from logits [T, vocab] (fp32 or bf16, rows may be strided) with uniforms [T] fp32: temperature, top_p, min_p
+    fp32 [T] and top_k int32 [T] on the device, each optional.  probs: an fp32 [T, vocab] tensor that receives
+    the probabilities left (what irm_tree_verify takes).  uniforms None: probabilities alone.  Returns (token [T]
+    int32 or None, probs or None, workspace)."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-d torch.float32 or torch.bfloat16 tensor on the GPU")
+    dev, (T, V) = logits.device, logits.shape
+    ld = logits.stride(0) if T > 1 else V
+    if ld < V or (V > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must have contiguous rows that do not overlap")
+    te, tp, mp = (None if t is None else _take(t, torch.float32, (T,), n, dev)
+                  for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")))
+    tk = None if top_k is None else _take(top_k, torch.int32, (T,), "top_k", dev)
+    un = to = pr = None
+    pr_ld = 0
+    if probs is not None:
+        pr, pr_ld = _take_probs(probs, (T, V), "probs", dev)
+    if uniforms is not None:
+        un = _take(uniforms, torch.float32, (T,), "uniforms", dev)
+        if token is None:
+            token = _make(lambda: torch.empty(T, dtype=torch.int32, device=dev), dev, stream)
+    elif token is not None:
+        raise ValueError("a token needs uniforms")
+    elif probs is None:
+        raise ValueError("neither uniforms nor probs: nothing to compute")
+    if token is not None:
+        to = _take(token, torch.int32, (T,), "token", dev)
+    workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
+    if T > 0:
+        _launch(lib().irm_sample, dev, stream, logits.data_ptr(), int(logits.dtype is torch.bfloat16), ld, T, V, te, tk, tp, mp, un, to, pr,
+                pr_ld, ws, ws_bytes)
+    return token, probs, workspace
 
 
 ASSEMBLE_S1 = 1
