@@ -84,9 +84,9 @@ constexpr uint32_t kKr = 64 * 64;                     // and its 32 k_r columns,
 constexpr uint32_t kXBytes = kHalf * kPage * 4;       // received scores of one tile
 constexpr uint32_t kPBytes = kBM * 128;               // P of one tile
 constexpr uint32_t kOffBars = 0;
-constexpr uint32_t kOffTmem = 384;
-constexpr uint32_t kOffAbort = 388;
-constexpr uint32_t kOffFlag = 400;                    // int [2 sets][2 warps]: some factor is not 1
+constexpr uint32_t kOffTmem = 416;
+constexpr uint32_t kOffAbort = 420;
+constexpr uint32_t kOffFlag = 432;                    // int [2 sets][2 warps]: some factor is not 1
 constexpr uint32_t kOffMax = 512;                     // float [64]: running maximum of the own rows
 constexpr uint32_t kOffCorr = kOffMax + 64 * 4;       // float [4 tiles][64]: the peer rows' factors
 constexpr uint32_t kPrBytes = kPBytes / 4 + 128 + 4;  // what a warp sends of P: 32 rows, factors, flag
@@ -115,15 +115,15 @@ enum : int {
   BAR_INV = BAR_Q + 1,               // the peer rows' 1 / l arrived (1 + tx)
   BAR_DRAIN = BAR_INV + 1,           // [2] all UMMAs of an issuer done
   BAR_X_HALF = BAR_DRAIN + 2,        // [2][32 rows] the peer's partial scores, keys 0 to 31 (1 + tx)
-  BAR_LANDED = BAR_X_HALF + 4,       // [stage] TMA bytes of the page (1 + tx); 8-bit: its cKV is there as bf16 (4 warps)
+  BAR_LANDED = BAR_X_HALF + 4,       // [stage] TMA bytes of the page (1 + tx); 8-bit: the first 64 of each 128 columns as bf16 (4 warps)
 };
 
 // What depends on the cache's type: pages in shared memory, and the barriers of their ring.
 template <bool kCodes8>
 struct Layout {
   static constexpr int kThreads = (kCodes8 ? 16 : 12) * 32;
-  static constexpr int kStages = kCodes8 ? 3 : 5;  // pages of bf16
-  static constexpr int kRaw = kCodes8 ? 4 : 0;     // pages of codes
+  static constexpr int kStages = kCodes8 ? 4 : 5;  // pages of bf16
+  static constexpr int kRaw = kCodes8 ? 2 : 0;     // pages of codes
   static constexpr uint32_t kRing = kStages * kSlab;  // pages in turn, for each 64 columns
   static constexpr int kQStage = kCodes8 ? 1 : 2;     // 4 slabs of Q's cKV columns at the start, in this stage and the next
   static constexpr uint32_t kOffQl = kOffKv + kQStage * kSlab;
@@ -134,7 +134,8 @@ struct Layout {
   static constexpr int BAR_RAW_FULL = BAR_FREE + kStages;  // 8-bit: [raw] TMA bytes of the codes (1 + tx)
   static constexpr int BAR_RAW_FREE = BAR_RAW_FULL + kRaw; // [raw] codes read (4 warps)
   static constexpr int BAR_KR = BAR_RAW_FREE + kRaw;       // [2] TMA bytes of k_r (1 + tx)
-  static constexpr int kBars = kCodes8 ? BAR_KR + 2 : BAR_CLEAR + kStages;
+  static constexpr int BAR_REST = BAR_KR + 2;               // 8-bit: [stage] the columns behind the first 64 of each 128 (4 warps)
+  static constexpr int kBars = kCodes8 ? BAR_REST + kStages : BAR_CLEAR + kStages;
   static_assert(kBM * 128 <= 2 * kSlab && kStages >= kQStage + 2, "Q's place");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kBars * 8 <= kOffTmem, "barrier area");
@@ -247,17 +248,13 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float corr) {
 
 // Four e4m3 codes as bf16 times the scale (a pair of bf16, 2^120 times the scale of the codes): a code's
 // sign and 7 bits, put where bf16 has sign, low exponent bits and first mantissa bits, are its value
-// times 2^-120, denormals included.
+// times 2^-120, denormals included.  The codes come as (0, 2) and (1, 3), which saves moving bytes: Q's
+// columns are put in the same order, and O's back.
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, __nv_bfloat162 scale) {
-  uint32_t r[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t t = __byte_perm(w, 0u, h ? 0x3424 : 0x1404);
-    const uint32_t u = (t >> 4 & 0x07f007f0u) | (t & 0x80008000u);
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), scale);
-    r[h] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return make_uint2(r[0], r[1]);
+  const uint32_t e = (w << 4 & 0x07f007f0u) | (w << 8 & 0x80008000u), o = (w >> 4 & 0x07f007f0u) | (w & 0x80008000u);
+  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e), scale);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o), scale);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
 template <bool kCodes8>
@@ -301,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(BAR_LANDED + s), kCodes8 ? kConvWarps : 1);
       mbar_init(bar(BAR_FREE + s), kCodes8 ? 1 : 2);
-      if (!kCodes8) mbar_init(bar(L::BAR_CLEAR + s), 1);
+      if (kCodes8) mbar_init(bar(L::BAR_REST + s), kConvWarps); else mbar_init(bar(L::BAR_CLEAR + s), 1);
     }
     if (kCodes8) {
       for (int s = 0; s < kRaw; ++s) {
@@ -385,7 +382,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffQl + slab * kRing + sw128_offset((uint32_t)m, (uint32_t)i));
+          uint4 v = *reinterpret_cast<const uint4*>(smem + kOffQl + slab * kRing + sw128_offset((uint32_t)m, (uint32_t)i));
+          if (kCodes8)  // columns 0, 2, 1, 3 of each four
+            v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                           __byte_perm(v.z, v.w, 0x7632));
           r[4 * i] = v.x;
           r[4 * i + 1] = v.y;
           r[4 * i + 2] = v.z;
@@ -615,20 +615,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
       const uint64_t aq = sdesc_sw64(sb + kOffQr, 512);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
-        if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+        if (!kCodes8 && !(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
         if (kCodes8 && !(ok = mbar_wait(bar(L::BAR_KR + set), (uint32_t)(j >> 1) & 1u, abort_flag))) break;
         if (j >= 2 && !(ok = mbar_wait(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(sb + kOffKr + (uint32_t)set * kKr, 512);
         const uint32_t d = tmem + kTmemS + 64u * (uint32_t)set;
+        auto rope = [&](uint32_t first) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int kk = 0; kk < 2; ++kk) umma_bf16(d, sdesc_add(aq, kk * 32), sdesc_add(bk, kk * 32), kIdescS, kk == 0 ? first : 1u);
+        };
+        auto slab = [&](int c, uint32_t first) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, sdesc_add(bd, c * kRing + kk * 32), kIdescS, (c | kk) ? 1u : 0u);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) umma_bf16(d, sdesc_add(aq, kk * 32), sdesc_add(bk, kk * 32), kIdescS, 1u);
+            umma_bf16_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, sdesc_add(bd, c * kRing + kk * 32), kIdescS, kk == 0 ? first : 1u);
+        };
+        if constexpr (kCodes8) {  // in the order in which they come
+          rope(0u);
+          if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+          tc_fence_after();
+          slab(0, 1u);
+          slab(2, 1u);
+          if (!(ok = mbar_wait(bar(L::BAR_REST + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+          tc_fence_after();
+          slab(1, 1u);
+          slab(3, 1u);
+        } else {
+          slab(0, 0u);
+          slab(1, 1u);
+          slab(2, 1u);
+          slab(3, 1u);
+          rope(1u);
+        }
         umma_commit(bar(BAR_S_FULL + set));
       }
       umma_commit(bar(BAR_DRAIN));
@@ -682,9 +701,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
     const int node0 = row0 / a.H, node1 = (row0 + rows_valid - 1) / a.H;
     const uint8_t* scales = a.kv8 + (int64_t)r * IRM_ROW_BYTES8 + IRM_ROW8_SCALES + 4 * (2 * rank + box);
     // a page's scale is read one page ahead, its index two (a page outside the cache reads as zeros)
-    auto page_at = [&](int j) -> int { return j < ntiles ? ptab[j] : -1; };
+    auto page_at = [&](int j) -> int {
+      int v = -1;
+      if (j < ntiles) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(ptab + j));
+      return v;
+    };
     auto scale_of = [&](int page) -> uint32_t {
-      return page >= 0 && page < a.n_pages ? __ldg(reinterpret_cast<const uint32_t*>(scales + (int64_t)page * (kPage * IRM_ROW_BYTES8))) : 0u;
+      uint32_t v = 0;  // volatile: it is not put off to where it is used
+      if (page >= 0 && page < a.n_pages)
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(scales + (int64_t)page * (kPage * IRM_ROW_BYTES8)));
+      return v;
     };
     uint32_t next = scale_of(page_at(0));
     int page = page_at(1);
@@ -702,28 +728,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         seen = ((warp & 1 ? hi : lo) >> lane & 1u) != 0;
       }
       if (!(ok = warp_wait(bar(L::BAR_RAW_FULL + raw), (uint32_t)(j / kRaw) & 1u, abort_flag))) break;
-      uint4 v[8];
-      const uint8_t* from = smem + L::kOffRaw + (uint32_t)raw * kCodes + (uint32_t)box * kSlab;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(from + sw128_offset((uint32_t)r, (uint32_t)i));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::BAR_RAW_FREE + raw));
       // the second and third page's places hold Q until it is in TMEM
       if (j == L::kQStage && !(ok = warp_wait(bar(BAR_Q), 0, abort_flag))) break;
       if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
-      const __nv_bfloat162 m = __float2bfloat162_rn(__uint_as_float(scale & 0xffff0000u) * 0x1p120f);
-      const uint32_t to = sb + kOffKv + (uint32_t)(2 * box) * kRing + (uint32_t)s * kSlab;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint2 a0 = codes_to_bf16(v[i].x, m), a1 = codes_to_bf16(v[i].y, m), a2 = codes_to_bf16(v[i].z, m), a3 = codes_to_bf16(v[i].w, m);
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t at = to + (uint32_t)(i >> 2) * kRing;
-        st_shared_v4(at + sw128_offset((uint32_t)r, (uint32_t)(2 * i & 7)), seen ? make_uint4(a0.x, a0.y, a1.x, a1.y) : zero);
-        st_shared_v4(at + sw128_offset((uint32_t)r, (uint32_t)(2 * i & 7) + 1u), seen ? make_uint4(a2.x, a2.y, a3.x, a3.y) : zero);
+      // zeros for an unseen row (a code's bits are a finite number, whatever it is)
+      const __nv_bfloat162 m = __float2bfloat162_rn(seen ? __uint_as_float(scale & 0xffff0000u) * 0x1p120f : 0.f);
+      const uint32_t from = sb + L::kOffRaw + (uint32_t)raw * kCodes + (uint32_t)box * kSlab + (uint32_t)r * 128u;
+      const uint32_t to = sb + kOffKv + (uint32_t)(2 * box) * kRing + (uint32_t)s * kSlab + (uint32_t)r * 128u;
+      uint4 v = ld_shared_v4(from + ((uint32_t)(r & 7) << 4));
+      // a loop: unrolled, the warps' different code does not fit the instruction caches
+#pragma unroll 2
+      for (uint32_t i = 0; i < 8; ++i) {
+        const uint4 w = v;
+        v = ld_shared_v4(from + (((i + 1u & 7u) ^ (uint32_t)(r & 7)) << 4));
+        const uint2 a0 = codes_to_bf16(w.x, m), a1 = codes_to_bf16(w.y, m), a2 = codes_to_bf16(w.z, m), a3 = codes_to_bf16(w.w, m);
+        const uint32_t at = to + (i >> 2) * kRing + ((2u * i & 7u ^ (uint32_t)(r & 7)) << 4);
+        st_shared_v4(at, make_uint4(a0.x, a0.y, a1.x, a1.y));
+        st_shared_v4(at ^ 16u, make_uint4(a2.x, a2.y, a3.x, a3.y));
+        if (i == 3) {
+          fence_proxy_async_smem();  // read by the tensor core
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BAR_LANDED + s));
+        }
       }
-      fence_proxy_async_smem();  // read by the tensor core
+      // The copy of a later page may overwrite the codes once they have been read: as with the received scores, the
+      // arrival that says so depends on what was read last (without that, loads were still under way in a full SM
+      // and read the later page's codes).
+      const uint32_t vote = __ballot_sync(kFull, v.x != 0u);
+      if (lane == 0) mbar_arrive(bar(L::BAR_RAW_FREE + raw) + (vote & a.zero));
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_LANDED + s));
+      if (lane == 0) mbar_arrive(bar(L::BAR_REST + s));
     }
     __syncwarp();
     cluster_wait();
@@ -845,6 +880,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 64; ++i) r[i] = inv != 0.f ? __float_as_uint(__uint_as_float(r[i]) * inv) : 0u;
+        if (kCodes8) {  // columns 0, 2, 1, 3 of each four
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const uint32_t x = r[i + 1];
+            r[i + 1] = r[i + 2];
+            r[i + 2] = x;
+          }
+        }
         const int col = 256 * rank + c;
         __syncwarp();
         if (split) {  // rows of 256 bytes, 16-byte pieces XOR-ed with the row
