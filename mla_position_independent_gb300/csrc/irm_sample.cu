@@ -21,6 +21,7 @@
 // A cluster of CTAs shares a row, which stays in shared memory as fp32 from its one read where it fits (51200
 // logits a CTA); longer rows are read again by each pass.
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -38,6 +39,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kBins = 1024;         // the last one holds what has no weight
 constexpr int kList = 448;          // elements that are ranked among themselves, a thread each (two CTAs' memory fits an SM)
+constexpr int kNear = 96;           // of which a top-p cut looks at that many around its guess (each is compared with each)
 constexpr int kGroup = 128;         // elements that a warp looks at at once
 constexpr int kGroups = kMaxVocab / kMaxCluster / kGroup;
 constexpr uint32_t kFull = 0xffffffffu;
@@ -50,6 +52,7 @@ struct SampleArgs {
   const void* logits;
   int64_t ld;
   int V, seg;  // logits of a row, and of a CTA's part of it (a multiple of 4)
+  int cap;     // candidates that a CTA can hold in shared memory, with their weights
   const float *temperature, *top_p, *min_p, *uniforms;
   const int32_t* top_k;
   int32_t* token;
@@ -64,24 +67,41 @@ struct __align__(16) Item {
   uint64_t w;
 };
 
+// 2^(i / 32): four more than its first 21 bits, and the rest
+__constant__ float kPow[2][32] = {
+    {0x1.4p+2f, 0x1.4166c4p+2f, 0x1.42d562p+2f, 0x1.444c08p+2f,
+     0x1.45caep+2f, 0x1.47521cp+2f, 0x1.48e1eap+2f, 0x1.4a7a78p+2f,
+     0x1.4c1bf8p+2f, 0x1.4dc69cp+2f, 0x1.4f7a9ap+2f, 0x1.513822p+2f,
+     0x1.52ff6cp+2f, 0x1.54d0aep+2f, 0x1.56ac2p+2f, 0x1.5891fap+2f,
+     0x1.5a827ap+2f, 0x1.5c7dd8p+2f, 0x1.5e8452p+2f, 0x1.609626p+2f,
+     0x1.62b396p+2f, 0x1.64dcdep+2f, 0x1.671246p+2f, 0x1.69540ep+2f,
+     0x1.6ba27ep+2f, 0x1.6dfddcp+2f, 0x1.70667p+2f, 0x1.72dc84p+2f,
+     0x1.756064p+2f, 0x1.77f25cp+2f, 0x1.7a92bep+2f, 0x1.7d41dap+2f},
+    {0x0p+0f, -0x1.6753d4p-23f, -0x1.30677p-24f, -0x1.7f6d26p-23f,
+     0x1.e3ea8cp-23f, 0x1.8b45cep-23f, -0x1.18a9dcp-24f, -0x1.5c0424p-25f,
+     0x1.4636e2p-25f, 0x1.b9d54ep-23f, -0x1.9f6e5ep-23f, -0x1.f9e76ep-24f,
+     -0x1.564eaep-23f, -0x1.4b1584p-23f, -0x1.15bd5ep-23f, 0x1.81d2acp-23f,
+     -0x1.980c44p-24f, -0x1.713a08p-24f, -0x1.829fdp-25f, 0x1.94cce2p-24f,
+     -0x1.eeaafap-23f, 0x1.866e3p-23f, 0x1.51f848p-27f, 0x1.91f12ap-23f,
+     0x1.95ad3ap-24f, -0x1.a09438p-25f, -0x1.13d56cp-23f, -0x1.18837cp-23f,
+     -0x1.1822dcp-23f, 0x1.9bdcdap-23f, 0x1.152486p-23f, -0x1.248dd6p-23f}};
+
 struct Shared {
   uint64_t part[kWarps][4];
   uint64_t tot[2][kMaxCluster][4];
   union {
-    struct {
-      uint32_t hist[kBins];
-      Item list[kList];
-    } s;
+    uint32_t hist[kBins];
     uint64_t gsum[kGroups];
   } u;
-  float th4[32], tl[32];  // 2^(i / 32): four more than its 21 bits, and the rest
-  uint32_t n_list, scan[kWarps];
-  float fscan[kWarps];
+  Item list[kList], own[kList];  // what is ranked: of the whole row, and what this CTA has of it
+  float th4[32], tl[32];  // kPow: read at an index of each lane's own
+  uint32_t n_own, scan[kWarps];
+  float fscan[kWarps], mass;
   // 1 / (h T) in two parts, and log2(e) / (h T).  h is 1; 1/2 for a temperature so high that differences of
   // logits that overflow still count; 2^24 for one so low that differences of denormal logits do
-  float ih, il, ch, h;
+  float ih, il, ch, h, m;
   int bin, cut_idx;
-  uint32_t bin_count, bin_above;
+  uint32_t bin_count, bin_above, near_lo, near_hi;
   float cut_l;
   uint64_t sum;
 };
@@ -90,6 +110,17 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
+}
+// floor(f x) for 0 <= f <= 1, and the same rounded up: the product of 24 and 64 bits.
+__device__ __forceinline__ uint64_t part_of_sum(float f, uint64_t x, bool up) {
+  const uint32_t b = __float_as_uint(f), e = b >> 23;  // f = m 2^(e - 150)
+  if (e == 0) return up && b != 0 && x != 0 ? 1ull : 0ull;  // a denormal times less than 2^64
+  const uint64_t m = (b & 0x7fffffu) | 0x800000u, lo = m * x, hi = __umul64hi(m, x);
+  const uint32_t k = 150u - e;  // 23 .. 149
+  if (k >= 128) return up && (hi | lo) != 0 ? 1ull : 0ull;
+  const uint64_t whole = k >= 64 ? hi >> (k - 64) : lo >> k | hi << (64 - k);
+  const bool rest = k >= 64 ? (lo | (k > 64 ? hi << (128 - k) : 0ull)) != 0 : lo << (64 - k) != 0;
+  return whole + (up && rest ? 1ull : 0ull);
 }
 __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 #pragma unroll
@@ -102,18 +133,20 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 __device__ __forceinline__ void st_peer_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-__device__ __forceinline__ void st_peer_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint64_t ld_peer_u64(uint32_t addr) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t add_peer_u32(uint32_t addr, uint32_t v) {
-  uint32_t r;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(addr), "r"(v) : "memory");
-  return r;
+__device__ __forceinline__ uint2 ld_peer_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_peer_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 // Order-preserving integer of a logit (no NaN, no -0), and back.
@@ -144,10 +177,11 @@ __device__ __forceinline__ uint64_t weight(float l, float m, const Shared& sh) {
   const float te = fmaf(dl, sh.ih, fmaf(d, sh.il, fmaf(d, sh.ih, -th)));
   // th + te = k ln2 / 32 + x: ln2 / 32 in 12 bits, whose products with k are exact, and the rest
   constexpr float kLn2Hi = 0x1.62ep-6f, kLn2Lo = 0x1.0bfbe8p-20f;
-  const float kf = rintf(th * 46.16624130844683f);
+  const float shifted = fmaf(th, 46.16624130844683f, 0x1.8p23f);  // to the nearest whole number
+  const float kf = shifted - 0x1.8p23f;
   const float x0 = fmaf(kf, -kLn2Hi, th), x1 = fmaf(kf, -kLn2Lo, te);
   const float xh = x0 + x1, xl = x1 - (xh - x0);
-  const int k = (int)kf, i = k & 31, n = -(k >> 5);
+  const int k = __float_as_int(shifted) - __float_as_int(0x1.8p23f), i = k & 31, n = -(k >> 5);
   // e^x - 1 = x + x^2 (1/2 + x/6 + x^2/24 + x^3/120), |x| < 0.011
   const float s = xh * xh;
   const float q = fmaf(xh, fmaf(xh, fmaf(xh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
@@ -161,6 +195,9 @@ __device__ __forceinline__ uint64_t weight(float l, float m, const Shared& sh) {
   const int64_t v = ((int64_t)(__float_as_int(a) - 0x40800000) << 21) + (__float_as_int(b) - __float_as_int(0x1.8p-19f));
   return (((uint64_t)v << 2 >> n) + 1) >> 1;
 }
+
+// The same, called: where few elements need it, so that the code of a row's one pass stays in the instruction caches.
+__device__ __noinline__ uint64_t weight_of(float l, float m, const Shared& sh) { return weight(l, m, sh); }
 
 template <bool BF16, bool RES>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
@@ -200,17 +237,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return make_float4(clean(x[0]), clean(x[1]), clean(x[2]), clean(x[3]));
   };
   auto four = [&](int i) -> float4 { return RES ? *reinterpret_cast<const float4*>(row_sh + i) : fetch(i); };
-  // f(logit, index) for the CTA's logits, four neighbours a lane; one that is behind the end is -infinity
+  auto one = [&](int i) -> float { return RES ? row_sh[i] : clean(BF16 ? __bfloat162float(b16[i]) : f32[i]); };
+  // A warp looks at a contiguous part of the CTA's logits, a group (four neighbours a lane) at a time.
+  const int wseg = (n_own + kWarps * kGroup - 1) / (kWarps * kGroup) * kGroup;
+  const int w0 = min(n_own, warp * wseg), w1 = min(n_own, w0 + wseg);
+  // f(logit, index, weight()) for the CTA's logits, or for the candidates once they are listed (in index order)
+  Item* cand = reinterpret_cast<Item*>(row_sh + (RES ? a.seg : 0));
+  int n_cand = -1;
   auto each = [&](auto f) {
-    for (int i = 4 * tid; i < n_own; i += 4 * kThreads) {
-      const float4 x = four(i);
-      f(x.x, v0 + i);
-      f(x.y, v0 + i + 1);
-      f(x.z, v0 + i + 2);
-      f(x.w, v0 + i + 3);
+    if (n_cand >= 0) {
+      for (int i = tid; i < n_cand; i += kThreads) {
+        const Item x = cand[i];
+        f(x.l, x.idx, [&] { return x.w; });
+      }
+      return;
+    }
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const float l = one(i);
+      f(l, v0 + i, [&] { return weight_of(l, sh.m, sh); });
     }
   };
 
+  auto cluster_sync = [&] {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  };
   int slot = 0;
   // sums over the cluster of N values a thread; `before`: of v[0], what the CTAs before this one have
   uint64_t before = 0;
@@ -253,35 +305,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float rf = a.uniforms ? fminf(fmaxf(a.uniforms[b], 0.f), 1.f) : 0.f;
   const bool first_alone = !(temp > 0.f) || top_k == 1 || top_p <= 0.f || min_p > 1.f;
   if (tid < 32) {
-    const double t = exp2((double)tid / 32.0);
-    const float hi = rintf((float)t * 0x1p21f) * 0x1p-21f;
-    sh.th4[tid] = hi + 4.f;
-    sh.tl[tid] = (float)(t - (double)hi);
+    sh.th4[tid] = kPow[0][tid];
+    sh.tl[tid] = kPow[1][tid];
   } else if (tid == 32) {
     const float h = temp > 0x1p100f ? 0.5f : temp < 0x1p-100f ? 0x1p24f : 1.f;
-    const double inv = 1.0 / ((double)h * (double)temp);
+    const float ht = h * temp, inv = 1.f / ht;  // h T is exact
     sh.h = h;
-    sh.ih = (float)inv;
-    sh.il = (float)(inv - (double)sh.ih);
-    sh.ch = (float)(inv * 1.4426950408889634);
+    sh.ih = inv;
+    sh.il = inv > 0.f ? fmaf(-inv, ht, 1.f) * inv : 0.f;  // T may be infinite
+    sh.ch = inv * 1.4426950408889634f;
   }
   // ---- the row, and its maximum ------------------------------------------------------------
-  uint64_t top[1] = {0};
-  for (int i = 4 * tid; i < n_own; i += 4 * kThreads) {
-    const float4 x = fetch(i);
-    if (RES) *reinterpret_cast<float4*>(row_sh + i) = x;
-    const float y[4] = {x.x, x.y, x.z, x.w};
+  float best = -INFINITY;
+  constexpr int kAhead = 4;
+  for (int i0 = w0 + 4 * lane; i0 - 4 * lane < w1; i0 += kAhead * kGroup) {
+    float4 x[kAhead];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < n_own) {
-        const uint64_t k = (uint64_t)order_key(y[e]) << 32 | (uint32_t)~(v0 + i + e);
-        top[0] = k > top[0] ? k : top[0];
-      }
+    for (int u = 0; u < kAhead; ++u) x[u] = fetch(min(i0 + u * kGroup, a.seg - 4));  // behind the end: -infinity
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (RES && i0 + u * kGroup < w1) *reinterpret_cast<float4*>(row_sh + i0 + u * kGroup) = x[u];
+      if (i0 + u * kGroup < w1) best = fmaxf(best, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
+    }
   }
   cluster_wait();
+  uint64_t top[1] = {order_key(best)};
   cluster_sum(top, true);
-  const float m = key_logit((uint32_t)(top[0] >> 32));
-  const int first = (int)~(uint32_t)top[0];
+  const float m = key_logit((uint32_t)top[0]);
+  if (tid == 0) sh.m = m;
+  __syncthreads();
   float* probs = a.probs ? a.probs + b * a.probs_ld + v0 : nullptr;
   // p(i) for the CTA's probabilities, four neighbours at a time
   auto write_probs = [&](auto p) {
@@ -301,12 +353,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   const bool none = m == -INFINITY;
   if (none || first_alone) {  // the same in every CTA of the cluster
+    int first = -1;
+    if (!none) {
+      uint64_t at[1] = {0};  // the lowest index, as the largest complement
+      each([&](float l, int idx, auto) {
+        if (l == m) at[0] = max(at[0], (unsigned long)(uint32_t)~idx);
+      });
+      cluster_sum(at, true);
+      first = (int)~(uint32_t)at[0];
+    }
     if (probs != nullptr) {
       zero_probs();
       __syncthreads();
-      if (tid == 0 && !none && first >= v0 && first < v0 + n_own) probs[first - v0] = 1.f;
+      if (tid == 0 && first >= v0 && first < v0 + n_own) probs[first - v0] = 1.f;
     }
-    if (a.token != nullptr && rank == 0 && tid == 0) a.token[b] = none ? -1 : first;
+    if (a.token != nullptr && rank == 0 && tid == 0) a.token[b] = first;
     cluster_arrive();  // no CTA ends while another may still store into it
     cluster_wait();
     return;
@@ -320,27 +381,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // Counts of the bins over the cluster, of what is kept; with `bin` >= 0 those inside that bin.  Each thread
   // gets its two bins' sums.
-  auto histogram = [&](int bin) -> uint2 {
+  auto clear_bins = [&] {
     __syncthreads();
-    for (int i = tid; i < kBins; i += kThreads) sh.u.s.hist[i] = 0;
-    if (tid == 0) sh.n_list = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.u.hist[i] = 0;
     __syncthreads();
-    each([&](float l, int idx) {
-      const float t = octaves(l, m, half, ch);
-      const int x = bin_of(t);
-      if (x < kBins - 1 && (bin < 0 || x == bin) && kept(l, idx)) atomicAdd(&sh.u.s.hist[bin < 0 ? x : fine_of(t, bin)], 1u);
-    });
-    __syncthreads();
-    cluster_arrive();
-    cluster_wait();
-    uint2 sum = make_uint2(0u, 0u);
-    const uint32_t mine = smem_u32(&sh.u.s.hist[2 * tid]);
-    for (uint32_t c = 0; c < C; ++c) {
-      const uint64_t x = ld_peer_u64(mapa_shared(mine, c));
-      sum.x += (uint32_t)x;
-      sum.y += (uint32_t)(x >> 32);
+  };
+  auto cluster_bins = [&]() -> uint2 {  // behind a cluster barrier
+    uint2 sum = make_uint2(0u, 0u), x[kMaxCluster];
+    const uint32_t mine = smem_u32(&sh.u.hist[2 * tid]);
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster; ++c) x[c] = c < C ? ld_peer_v2(mapa_shared(mine, c)) : sum;
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster; ++c) {
+      sum.x += x[c].x;
+      sum.y += x[c].y;
     }
     return sum;
+  };
+  auto histogram = [&](int bin) -> uint2 {
+    clear_bins();
+    each([&](float l, int idx, auto) {
+      const float t = octaves(l, m, half, ch);
+      const int x = bin_of(t);
+      if (x < kBins - 1 && (bin < 0 || x == bin) && kept(l, idx)) atomicAdd(&sh.u.hist[bin < 0 ? x : fine_of(t, bin)], 1u);
+    });
+    cluster_sync();
+    return cluster_bins();
+  };
+  // Of a thread's two bins the one where the running sum from `from` on reaches k, and the sum before it.
+  auto bin_at = [&](uint2 h, uint32_t from, uint32_t k) {
+    const bool second = from + h.x < k;
+    sh.bin = 2 * tid + (second ? 1 : 0);
+    sh.bin_count = second ? h.y : h.x;
+    sh.bin_above = from + (second ? h.x : 0u);
   };
   // Inclusive block scan of a thread's value.
   auto scan_u32 = [&](uint32_t v) -> uint32_t {
@@ -367,29 +440,94 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int w = 0; w < warp; ++w) v += sh.fscan[w];
     return v;
   };
-  // The elements for which pick(t) holds, to every CTA's list.
-  auto gather = [&](auto pick) {
-    each([&](float l, int idx) {
+  // The elements for which pick(t) holds (kList of the cluster at most): each CTA collects its own, and behind a
+  // cluster barrier all read all.
+  auto collect = [&](auto pick) {
+    __syncthreads();
+    if (tid == 0) sh.n_own = 0;
+    __syncthreads();
+    each([&](float l, int idx, auto w) {
       const float t = octaves(l, m, half, ch);
       if (t > -kOctaves && pick(t) && kept(l, idx)) {
-        const uint64_t w = weight(l, m, sh);
-        const uint32_t at = add_peer_u32(mapa_shared(smem_u32(&sh.n_list), 0), 1u);
-        const uint4 v = make_uint4(__float_as_uint(l), (uint32_t)idx, (uint32_t)w, (uint32_t)(w >> 32));
-        if (at < (uint32_t)kList)
-          for (uint32_t c = 0; c < C; ++c) st_peer_v4(mapa_shared(smem_u32(&sh.u.s.list[at]), c), v);
+        const uint32_t at = atomicAdd(&sh.n_own, 1u);
+        if (at < (uint32_t)kList) sh.own[at] = Item{l, idx, w()};
       }
     });
-    cluster_arrive();
-    cluster_wait();
+  };
+  auto read_all = [&] {
+    uint32_t n[kMaxCluster], at = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster; ++c) n[c] = c < C ? min(ld_peer_u32(mapa_shared(smem_u32(&sh.n_own), c)), (uint32_t)kList) : 0u;
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster; ++c) {
+      if (c < C && (uint32_t)tid < n[c] && at + tid < (uint32_t)kList)
+        *reinterpret_cast<uint4*>(&sh.list[at + tid]) = ld_peer_v4(mapa_shared(smem_u32(&sh.own[tid]), c));
+      at += n[c];
+    }
+    __syncthreads();
+  };
+  auto gather = [&](auto pick) {
+    collect(pick);
+    cluster_sync();
+    read_all();
+  };
+  // Lists the CTA's candidates, those up to bin `last`, in index order with their weights; where they are too many
+  // the row stays what is looked at.
+  auto list_candidates = [&](int last) {
+    if (!RES || n_cand >= 0) return;
+    auto in = [&](float l) -> bool {
+      const float t = octaves(l, m, half, ch);
+      return t > -kOctaves && bin_of(t) <= last;
+    };
+    uint32_t n = 0;
+    for (int i = w0 + 4 * lane; i < w1; i += kGroup) {
+      const float4 x = four(i);
+      n += (in(x.x) ? 1u : 0u) + (in(x.y) ? 1u : 0u) + (in(x.z) ? 1u : 0u) + (in(x.w) ? 1u : 0u);
+    }
+    n = __reduce_add_sync(kFull, n);
+    __syncthreads();
+    if (lane == 0) sh.scan[warp] = n;
+    __syncthreads();
+    uint32_t at = 0, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += sh.scan[w];
+      all += sh.scan[w];
+    }
+    if (all > (uint32_t)a.cap) return;
+    const uint32_t first = at;
+    for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += kGroup) {
+      const float4 x = i < w1 ? four(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      const float y[4] = {x.x, x.y, x.z, x.w};
+      bool p[4];
+      uint32_t c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c += (p[e] = in(y[e])) ? 1u : 0u;
+      uint32_t incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t z = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += z;
+      }
+      uint32_t to = at + incl - c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (p[e]) cand[to++] = Item{y[e], v0 + i + e, 0};
+      at += __shfl_sync(kFull, incl, 31);
+    }
+    __syncwarp();
+    for (uint32_t i = first + lane; i < at; i += 32) cand[i].w = weight_of(cand[i].l, m, sh);
+    n_cand = (int)all;
+    __syncthreads();
   };
   // Rank of the thread's element among the list's first n, and the weight before it.
   auto rank_in_list = [&](int n, uint64_t& w_before) -> int {
     int r = 0;
     w_before = 0;
     if (tid < n) {
-      const Item me = sh.u.s.list[tid];
+      const Item me = sh.list[tid];
+#pragma unroll 4
       for (int j = 0; j < n; ++j) {
-        const Item x = sh.u.s.list[j];
+        const Item x = sh.list[j];
         if (x.l > me.l || (x.l == me.l && x.idx < me.idx)) {
           ++r;
           w_before += x.w;
@@ -404,65 +542,71 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto finish_list = [&](int n, int k, uint64_t total) {
     uint64_t wb;
     const int r = rank_in_list(n, wb);
-    const Item me = sh.u.s.list[tid < n ? tid : 0];
+    const Item me = sh.list[tid < n ? tid : 0];
     if (tid < n && r == min(k, n) - 1) sh.sum = wb + me.w;
     __syncthreads();
     if (total == 0) total = sh.sum;
-    const uint64_t target = top_p < 1.f ? (uint64_t)ceil((double)top_p * (double)total) : ~0ull;
-    const uint64_t least = min_p > 0.f ? (uint64_t)ceil((double)min_p * (double)kOne) : 0ull;
+    const uint64_t target = top_p < 1.f ? part_of_sum(top_p, total, true) : ~0ull;
+    const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
     const bool stay = tid < n && r < k && (r == 0 || (wb < target && me.w >= least));
     uint64_t s = stay ? wb + me.w : 0ull;  // the last that stays has them all
     s = warp_max64(s);
     __syncthreads();
     if (lane == 0) sh.part[warp][0] = s;
-    if (tid < n && !stay) sh.u.s.list[tid].w = 0;
+    if (tid < n && !stay) sh.list[tid].w = 0;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) s = sh.part[w][0] > s ? sh.part[w][0] : s;
     if (probs != nullptr) {
       zero_probs();
       __syncthreads();
-      if (stay && me.idx >= v0 && me.idx < v0 + n_own) probs[me.idx - v0] = (float)((double)me.w / (double)s);
+      if (stay && me.idx >= v0 && me.idx < v0 + n_own) probs[me.idx - v0] = fast_exp2(octaves(me.l, m, half, ch)) * ((float)kOne / (float)s);
     }
     if (a.token != nullptr && rank == 0) {
-      uint64_t at = (uint64_t)((double)rf * (double)s);
+      uint64_t at = part_of_sum(rf, s, false);
       if (at >= s) at = s - 1;
       uint64_t x = 0;
       if (stay)
-        for (int j = 0; j < n; ++j) x += sh.u.s.list[j].idx < me.idx ? sh.u.s.list[j].w : 0ull;
+        for (int j = 0; j < n; ++j) x += sh.list[j].idx < me.idx ? sh.list[j].w : 0ull;
       if (stay && at >= x && at < x + me.w) a.token[b] = me.idx;
     }
     cluster_arrive();
     cluster_wait();
   };
 
-  // The cut at the element where the order's running value (1 an element, or its weight) reaches `target`, from
-  // what the bins before `bin` (and before its part `fine`) have, `above`.  Values: counts or weights.
-  auto value = [&](bool weights, float l) -> uint64_t { return weights ? weight(l, m, sh) : 1ull; };
+  // The cut at the list's element where the running value (1 an element, or its weight), from `above` on, reaches
+  // `target`; false where none does.
+  auto cut_in_list = [&](bool weights, uint64_t target, uint64_t above, uint32_t n) -> bool {
+    uint64_t wb;
+    const int r = rank_in_list((int)n, wb);
+    bool here = false;
+    if ((uint32_t)tid < n) {
+      const Item me = sh.list[tid];
+      const uint64_t x = above + (weights ? wb : (uint64_t)r);
+      here = x < target && x + (weights ? me.w : 1ull) >= target;
+      if (here) {
+        sh.cut_l = me.l;
+        sh.cut_idx = me.idx;
+      }
+    }
+    if (!__syncthreads_or(here)) return false;
+    cut_l = sh.cut_l;
+    cut_idx = sh.cut_idx;
+    return true;
+  };
+  // The same in a bin (or its part `fine`) of `count` elements, before which the bins have `above`.
   auto cut_in_bin = [&](bool weights, uint64_t target, uint64_t above, uint32_t count, int bin, int fine) {
     auto inside = [&](float t) { return bin_of(t) == bin && (fine < 0 || fine_of(t, bin) == fine); };
     if (count <= (uint32_t)kList) {
       gather(inside);
-      uint64_t wb;
-      const int n = (int)count, r = rank_in_list(n, wb);
-      if (tid < n) {
-        const Item me = sh.u.s.list[tid];
-        const uint64_t x = above + (weights ? wb : (uint64_t)r);
-        if (x < target && x + (weights ? me.w : 1ull) >= target) {
-          sh.cut_l = me.l;
-          sh.cut_idx = me.idx;
-        }
-      }
-      __syncthreads();
-      cut_l = sh.cut_l;
-      cut_idx = sh.cut_idx;
+      cut_in_list(weights, target, above, count);
       return;
     }
     // Too many alike: bit by bit, the largest key from which on the values reach the target, then the index.
     auto reach = [&](auto pick) -> uint64_t {
       uint64_t s[1] = {0};
-      each([&](float l, int idx) {
+      each([&](float l, int idx, auto w) {
         const float t = octaves(l, m, half, ch);
-        if (t > -kOctaves && inside(t) && kept(l, idx) && pick(order_key(l), idx)) s[0] += value(weights, l);
+        if (t > -kOctaves && inside(t) && kept(l, idx) && pick(order_key(l), idx)) s[0] += weights ? w() : 1ull;
       });
       cluster_sum(s);
       return above + s[0];
@@ -480,39 +624,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cut_l = key_logit(key);
     cut_idx = idx + 1;
   };
-  // The thread that holds the first bin for which reached(its running sum) says where the cut is.
-  auto publish = [&](int bin, uint32_t count, uint32_t above) {
-    sh.bin = bin;
-    sh.bin_count = count;
-    sh.bin_above = above;
-  };
-
   // ---- top-k ------------------------------------------------------------------------------
   if (top_k > 0 && top_k < a.V) {
     const uint32_t k = (uint32_t)top_k;
     uint2 h = histogram(-1);
-    uint32_t incl = scan_u32(h.x + h.y), excl = incl - h.x - h.y;
-    if (tid == 0) publish(-1, 0, 0);
+    uint32_t incl = scan_u32((h.x + h.y)), excl = incl - (h.x + h.y);
+    if (tid == 0) sh.bin = -1;
     __syncthreads();
-    if (excl < k && k <= incl) k <= excl + h.x ? publish(2 * tid, h.x, excl) : publish(2 * tid + 1, h.y, excl + h.x);
+    if (excl < k && k <= incl) bin_at(h, excl, k);
     __syncthreads();
-    int bin = sh.bin;  // -1: those with a weight are fewer than k
+    const int bin = sh.bin;  // -1: those with a weight are fewer than k
     uint32_t count = sh.bin_count, above = sh.bin_above;
-    if (bin >= 0) {
+    if (bin < 0) {
+      cluster_sync();  // the counts have been read
+    } else {
       if (above + count <= (uint32_t)kList) {
         gather([&](float t) { return bin_of(t) <= bin; });
         finish_list((int)(above + count), (int)k, 0);
         return;
       }
+      list_candidates(bin);
       int fine = -1;
       if (count > (uint32_t)kList) {
-        cluster_arrive();  // the counts have been read
-        cluster_wait();
+        cluster_sync();  // the counts have been read
         h = histogram(bin);
-        incl = scan_u32(h.x + h.y) + above;
-        excl = incl - h.x - h.y;
-        __syncthreads();
-        if (excl < k && k <= incl) k <= excl + h.x ? publish(2 * tid, h.x, excl) : publish(2 * tid + 1, h.y, excl + h.x);
+        incl = scan_u32((h.x + h.y)) + above;
+        excl = incl - (h.x + h.y);
+        if (excl < k && k <= incl) bin_at(h, excl, k);
         __syncthreads();
         fine = sh.bin;
         count = sh.bin_count;
@@ -524,39 +662,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- top-p ------------------------------------------------------------------------------
   if (top_p < 1.f) {
     uint64_t z[1] = {0};
-    each([&](float l, int idx) {
-      if (octaves(l, m, half, ch) > -kOctaves && kept(l, idx)) z[0] += weight(l, m, sh);
-    });
+    clear_bins();
+    auto add = [&](float l, int idx, auto w) {
+      const int x = bin_of(octaves(l, m, half, ch));
+      if (x < kBins - 1 && kept(l, idx)) {
+        atomicAdd(&sh.u.hist[x], 1u);
+        z[0] += w();
+      }
+    };
+    if (n_cand >= 0) {
+      each(add);
+    } else {
+#pragma unroll 2
+      for (int i = w0 + lane; i < w1; i += 32) {
+        const float l = one(i);
+        add(l, v0 + i, [&] { return weight(l, m, sh); });
+      }
+    }
     cluster_sum(z);
-    const uint64_t target = (uint64_t)ceil((double)top_p * (double)z[0]);
+    const uint64_t target = part_of_sum(top_p, z[0], true);
     int bin = -1, fine = -1;
     uint64_t above = 0;
     uint32_t count = 0;
+    bool done = false;
     for (int level = 0; level < 2; ++level) {
-      const uint2 h = histogram(bin);
+      const uint2 h = level == 0 ? cluster_bins() : histogram(bin);
       // the guess: counts times the weight at the bin's middle (inside one bin: of the bin)
-      const float w0 = exp2f(-((float)(level ? bin : 2 * tid) + 0.5f) / kBinScale);
-      const float w1 = level ? w0 : exp2f(-((float)(2 * tid + 1) + 0.5f) / kBinScale);
+      const float w0 = fast_exp2(-((float)(level ? bin : 2 * tid) + 0.5f) / kBinScale), w1 = level ? w0 : w0 * fast_exp2(-1.f / kBinScale);
       const float mass0 = w0 * (float)h.x, mass1 = w1 * (float)h.y;
-      const float at = (float)(target - above) * (1.f / (float)kOne);
-      const float incl = scan_f32(mass0 + mass1), excl = incl - mass0 - mass1;
-      const uint32_t c_incl = scan_u32(h.x + h.y);
+      const float incl = scan_f32(mass0 + mass1);
+      if (tid == kThreads - 1) sh.mass = incl;
+      const uint32_t c_incl = scan_u32(h.x + h.y), c_excl = c_incl - h.x - h.y;
       if (tid == 0) sh.bin = kBins - 1;
       __syncthreads();
-      if (at <= incl) atomicMin(&sh.bin, at <= excl + mass0 ? 2 * tid : 2 * tid + 1);  // the same in every CTA
+      // in whole rows the share of the same sum, so that what the middles are off by cancels
+      const float at = level == 0 ? top_p * sh.mass : (float)(target - above) * (1.f / (float)kOne);
+      if (at <= incl) atomicMin(&sh.bin, 2 * tid + (incl - mass1 < at ? 1 : 0));  // the first: the same in every CTA
       __syncthreads();
       int guess = min(sh.bin, kBins - 2);
-      if (level == 0 && sh.bin < kBins - 4) {
-        // few enough up to the bins behind the guess: they are the list, if they do reach the target
-        if (tid == (guess + 2) >> 1) sh.bin_above = c_incl;
+      if (level == 0) {
+        // a few bins behind the guess for its error; few enough up to there: they are the list, if they do reach
+        // the target
+        const int last = min(guess + 12 | 1, kBins - 1);
+        if (tid == last >> 1) sh.bin_above = c_incl;
+        if (tid == guess >> 1) {
+          sh.near_lo = c_excl;
+          sh.near_hi = c_incl;
+        }
         __syncthreads();
         const uint32_t n = sh.bin_above;
         if (n <= (uint32_t)kList) {
-          const int last = ((guess + 2) | 1);
           gather([&](float t) { return bin_of(t) <= last; });
-          uint64_t s = tid < (int)n ? sh.u.s.list[tid].w : 0ull;
+          uint64_t s = tid < (int)n ? sh.list[tid].w : 0ull;
           s = warp_sum64(s);
-          __syncthreads();
           if (lane == 0) sh.part[warp][0] = s;
           __syncthreads();
           s = 0;
@@ -565,8 +723,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             finish_list((int)n, INT_MAX, z[0]);
             return;
           }
-          if (tid == 0) sh.n_list = 0;  // stored into again behind the next exchange
-          __syncthreads();
+          cluster_sync();  // nothing else is collected before all have read
+        }
+        list_candidates(last);
+        // the bins around the guess, as many as fit, are ranked at once, and what lies before them summed
+        const uint32_t lo_c = sh.near_lo, hi_c = sh.near_hi, wing = kNear > hi_c - lo_c ? (kNear - (hi_c - lo_c)) / 2 : 0u;
+        __syncthreads();
+        if (tid == 0) {
+          sh.bin = kBins;
+          sh.bin_count = 0;
+        }
+        __syncthreads();
+        if (c_excl + wing >= lo_c) atomicMin(&sh.bin, 2 * tid);
+        if (c_incl <= hi_c + wing) atomicMax(&sh.bin_count, (uint32_t)(2 * tid + 1));
+        __syncthreads();
+        const int near_first = sh.bin, near_last = min((int)sh.bin_count, last);
+        if (tid == near_first >> 1) sh.near_lo = c_excl;
+        if (tid == near_last >> 1) sh.near_hi = c_incl;
+        __syncthreads();
+        const uint32_t near = sh.near_hi - sh.near_lo;
+        if (near <= (uint32_t)kList) {
+          uint64_t s[1] = {0};
+          collect([&](float t) {
+            const int x = bin_of(t);
+            return x >= near_first && x <= near_last;
+          });
+          each([&](float l, int idx, auto w) {
+            const float t = octaves(l, m, half, ch);
+            if (t > -kOctaves && bin_of(t) < near_first && kept(l, idx)) s[0] += w();
+          });
+          cluster_sum(s);
+          read_all();
+          if (cut_in_list(true, target, s[0], near)) {
+            done = true;
+            break;
+          }
+          cluster_sync();  // nothing else is collected before all have read
         }
       }
       // the exact sums around the guess
@@ -577,15 +769,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       uint64_t base = 0;
       for (int guard = 0; guard < kBins; ++guard) {
         uint64_t s[4] = {0, 0, 0, 0};
-        each([&](float l, int idx) {
+        each([&](float l, int idx, auto w) {
           const float t = octaves(l, m, half, ch);
           const int x = t > -kOctaves ? part_of(t) : kBins;
           if (x <= guess + 1 && x < kBins && kept(l, idx)) {
-            const uint64_t w = weight(l, m, sh);
-            if (x < guess - 1) s[0] += w;
-            else if (x == guess - 1) s[1] += w;
-            else if (x == guess) s[2] += w;
-            else s[3] += w;
+            const uint64_t y = w();
+            if (x < guess - 1) s[0] += y;
+            else if (x == guess - 1) s[1] += y;
+            else if (x == guess) s[2] += y;
+            else s[3] += y;
           }
         });
         cluster_sum(s);
@@ -602,40 +794,60 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           guess += 1;
           base = s[0] + s[1] + s[2];
           break;
-        } else {
+        } else {  // the candidates may end before it: the row has them all
           guess += 2;
+          n_cand = -1;
         }
       }
       above = base;
-      if (tid == (guess >> 1)) sh.bin_count = guess & 1 ? h.y : h.x;
+      if (tid == guess >> 1) sh.bin_count = guess & 1 ? h.y : h.x;
       __syncthreads();
       count = sh.bin_count;
       if (level == 0) bin = guess; else fine = guess;
       if (count <= (uint32_t)kList) break;
     }
-    cut_in_bin(true, target, above, count, bin, fine);
+    if (!done) cut_in_bin(true, target, above, count, bin, fine);
   }
   // ---- the sum of what is left, by groups of a warp's elements ------------------------------------
-  const uint64_t least = min_p > 0.f ? (uint64_t)ceil((double)min_p * (double)kOne) : 0ull;
+  const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
+  const bool listed = n_cand >= 0;
   auto left = [&](float l, int idx) -> uint64_t {
     if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, idx)) return 0ull;
     const uint64_t w = weight(l, m, sh);
     return w >= least ? w : 0ull;
   };
-  __syncthreads();
-  uint64_t s[1] = {0}, lowest[1] = {0};
-  for (int i = 4 * tid, g = warp; i - 4 * lane < n_own; i += 4 * kThreads, g += kWarps) {
-    uint64_t w = 0;
-    if (i < n_own) {
-      const float4 x = four(i);
-      const float y[4] = {x.x, x.y, x.z, x.w};
+  // the weights left of element group g: a lane's four neighbours
+  const int groups = ((listed ? n_cand : n_own) + kGroup - 1) / kGroup;
+  auto group = [&](int g, uint64_t (&x)[4], int (&at)[4]) {
+    const int i = g * kGroup + 4 * lane;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint64_t z = left(y[e], v0 + i + e);
-        w += z;
-        if (z != 0) lowest[0] = max(lowest[0], (unsigned long)~order_key(y[e]));
-      }
+    for (int e = 0; e < 4; ++e) {
+      x[e] = 0;
+      at[e] = v0 + i + e;
     }
+    if (listed) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < n_cand) {
+          const Item z = cand[i + e];
+          at[e] = z.idx;
+          x[e] = kept(z.l, z.idx) && z.w >= least ? z.w : 0ull;
+        }
+    } else if (i < n_own) {
+      const float4 y = four(i);
+      x[0] = left(y.x, v0 + i);
+      x[1] = left(y.y, v0 + i + 1);
+      x[2] = left(y.z, v0 + i + 2);
+      x[3] = left(y.w, v0 + i + 3);
+    }
+  };
+  __syncthreads();
+  uint64_t s[1] = {0};
+  for (int g = warp; g < groups; g += kWarps) {
+    uint64_t x[4];
+    int at[4];
+    group(g, x, at);
+    uint64_t w = x[0] + x[1] + x[2] + x[3];
     s[0] += w;
     w = __any_sync(kFull, w != 0) ? warp_sum64(w) : 0ull;
     if (lane == 0) sh.u.gsum[g] = w;
@@ -643,24 +855,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cluster_sum(s);
   const uint64_t total = s[0], start = before;
   if (probs != nullptr) {
-    cluster_sum(lowest, true);
-    const float last = key_logit(~(uint32_t)lowest[0]);  // min-p may have kept less than the cut
-    const float inv = (float)((double)kOne / (double)total);
-    write_probs([&](int i) {
-      const float4 x = four(i);
-      auto p = [&](float l, int idx) {
-        const float t = octaves(l, m, half, ch);
-        return t > -kOctaves && l >= last && kept(l, idx) ? fast_exp2(t) * inv : 0.f;
-      };
-      return make_float4(p(x.x, v0 + i), p(x.y, v0 + i + 1), p(x.z, v0 + i + 2), p(x.w, v0 + i + 3));
-    });
+    const float inv = (float)kOne / (float)total;
+    if (listed) {
+      zero_probs();
+      __syncthreads();
+      for (int i = tid; i < n_cand; i += kThreads) {
+        const Item z = cand[i];
+        if (kept(z.l, z.idx) && z.w >= least) probs[z.idx - v0] = fast_exp2(octaves(z.l, m, half, ch)) * inv;
+      }
+    } else {
+      // min-p in octaves: what is right at it goes by the weight itself
+      const float edge = min_p > 0.f ? log2f(min_p) : -INFINITY;
+      write_probs([&](int i) {
+        const float4 x = four(i);
+        auto p = [&](float l, int idx) {
+          const float t = octaves(l, m, half, ch);
+          bool stay = t > -kOctaves && kept(l, idx) && t >= edge - 0.001f;
+          if (stay && t < edge + 0.001f) stay = left(l, idx) != 0;
+          return stay ? fast_exp2(t) * inv : 0.f;
+        };
+        return make_float4(p(x.x, v0 + i), p(x.y, v0 + i + 1), p(x.z, v0 + i + 2), p(x.w, v0 + i + 3));
+      });
+    }
   }
   // ---- the token: the group, then the element, where the running sum passes r of the total ---------------
   if (a.token != nullptr && warp == 0) {
-    uint64_t at = (uint64_t)((double)rf * (double)total);
+    uint64_t at = part_of_sum(rf, total, false);
     if (at >= total) at = total - 1;
     uint64_t run = start;
-    const int groups = (n_own + kGroup - 1) / kGroup;
     for (int g0 = 0; g0 < groups; g0 += 32) {
       const uint64_t w = g0 + lane < groups ? sh.u.gsum[g0 + lane] : 0ull;
       const uint64_t all = warp_sum64(w);
@@ -675,17 +897,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (lane >= o) incl += x;
       }
       const unsigned hit = __ballot_sync(kFull, at >= run + incl - w && at < run + incl);
-      const int g = g0 + __ffs((int)hit) - 1;
       run += __shfl_sync(kFull, incl - w, __ffs((int)hit) - 1);
-      const int i = g * kGroup + 4 * lane;
-      uint64_t x[4] = {0, 0, 0, 0};
-      if (i < n_own) {
-        const float4 y = four(i);
-        x[0] = left(y.x, v0 + i);
-        x[1] = left(y.y, v0 + i + 1);
-        x[2] = left(y.z, v0 + i + 2);
-        x[3] = left(y.w, v0 + i + 3);
-      }
+      uint64_t x[4];
+      int idx[4];
+      group(g0 + __ffs((int)hit) - 1, x, idx);
       const uint64_t mine = x[0] + x[1] + x[2] + x[3];
       incl = mine;
 #pragma unroll
@@ -697,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (at >= z && at < z + mine) {
         int e = 0;
         while (at >= z + x[e]) z += x[e++];
-        a.token[b] = v0 + i + e;
+        a.token[b] = idx[e];
       }
       break;
     }
@@ -708,9 +923,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 using Kernel = void (*)(SampleArgs);
 
-// CTAs of a row: as many as a row's parts need to stay in shared memory with two CTAs on an SM (25600 logits
-// each), more where the batch leaves SMs empty.
-constexpr int kPart = 25600, kPartMost = 51200;
+// CTAs of a row: as many as let its parts stay in shared memory, with some candidates, with two CTAs on an SM
+// (16384 logits each), more where the batch leaves SMs empty.
+constexpr int kPart = 16384, kPartMost = 40960;
+constexpr size_t kSmemTwo = 233472 / 2 - 1024, kSmemOne = 232448;  // of a CTA, with another one on the SM and alone
 int cluster_size(int64_t rows, int V) {
   int C = 1;
   while (C < kMaxCluster && (int64_t)C * kPart < V) C *= 2;
@@ -727,7 +943,7 @@ cudaError_t raise_smem_limit(Kernel k, int which) {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
   if (dev >= 0 && dev < 128 && done[which][dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPartMost * (int)sizeof(float));
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemOne - sizeof(Shared)));
   if (e == cudaSuccess && dev >= 0 && dev < 128) done[which][dev] = true;
   return e;
 }
@@ -780,7 +996,11 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(n_rows * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = resident ? (size_t)a.seg * sizeof(float) : 0;
+  if (resident) {
+    const size_t row = (size_t)a.seg * sizeof(float), room = (a.seg <= kPart ? kSmemTwo : kSmemOne) - sizeof(Shared) - row;
+    a.cap = (int)std::min<size_t>((size_t)a.seg, room / sizeof(Item));
+    cfg.dynamicSmemBytes = row + a.cap * sizeof(Item);
+  }
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
