@@ -62,7 +62,7 @@ class CdcParams(ctypes.Structure):
 
 
 def _rope_ptr(rope):
-    return None if rope is None else ctypes.cast(ctypes.pointer(rope), ctypes.c_void_p)
+    return None if rope is None else ctypes.addressof(rope)  # the caller holds it
 
 
 class IrmError(RuntimeError):
@@ -630,11 +630,13 @@ def _take_rows(t, width, name, device):
     """(address, row stride, rows) of bf16 rows [T, width] that may lie in wider ones (each row contiguous, on 16 bytes)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-d torch.bfloat16 tensor on the GPU")
-    if t.shape[1] != width or t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if cols != width or one != 1:
         raise ValueError(f"{name} must have contiguous rows of {width}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width, t.shape[0]
+    return t.data_ptr(), ld if rows > 1 else width, rows
 
 
 def irm_pages_append(c_kv, k_rope, kv, page_table, row, request=None, position=None, rope: Rope | None = None, factor=1.0,
@@ -652,15 +654,18 @@ def irm_pages_append(c_kv, k_rope, kv, page_table, row, request=None, position=N
     k, k_ld, T_k = _take_rows(k_rope, 64, "k_rope", dev)
     if T_k != T:
         raise ValueError(f"c_kv has {T} rows, k_rope {T_k}")
-    n_slots, max_pages = _size(page_table, 0, "page_table"), _size(page_table, 1, "page_table")
-    pt = _take(page_table, torch.int32, (n_slots, max_pages), "page_table", dev)
-    ro = _take(row, torch.int32, (T,), "row", dev)
-    rq = None if request is None else _take(request, torch.int32, (T,), "request", dev)
-    po = None if position is None else _take(position, torch.int32, (T,), "position", dev)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a 2-d torch.int32 tensor on the GPU")
+    n_slots, max_pages = table = page_table.shape
+    each = (T,)
+    pt = _take(page_table, torch.int32, table, "page_table", dev)
+    ro = _take(row, torch.int32, each, "row", dev)
+    rq = None if request is None else _take(request, torch.int32, each, "request", dev)
+    po = None if position is None else _take(position, torch.int32, each, "position", dev)
     workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
     if T > 0:
-        _launch(getattr(lib(), "irm_pages_append" + eight), dev, stream, c, c_ld, k, k_ld, T, cache, n_pages, pt, n_slots, max_pages, ro,
-                rq, po, _rope_ptr(rope), factor, int(bool(encoded)), ws, ws_bytes)
+        _launch(lib().irm_pages_append8 if eight else lib().irm_pages_append, dev, stream, c, c_ld, k, k_ld, T, cache, n_pages, pt, n_slots,
+                max_pages, ro, rq, po, _rope_ptr(rope), factor, 1 if encoded else 0, ws, ws_bytes)
     return workspace
 
 
@@ -679,7 +684,11 @@ def irm_rope_apply(x, position, rope: Rope | None = None, factor=1.0, out=None, 
     if x.stride(2) != 1 or out.stride(2) != 1:
         raise ValueError("x and out must have contiguous rows of 64")
     if T > 0 and H > 0:
-        (xt, xh), (ot, oh) = ((t.stride(0) if T > 1 else 64, t.stride(1) if H > 1 else 64) for t in (x, out))
+        (xt, xh, _), (ot, oh, _) = x.stride(), out.stride()
+        if T == 1:
+            xt = ot = 64
+        if H == 1:
+            xh = oh = 64
         _launch(lib().irm_rope_apply, dev, stream, x.data_ptr(), xt, xh, T, H, po, _rope_ptr(rope), factor, out.data_ptr(), ot, oh)
     return out
 
@@ -696,15 +705,17 @@ def irm_sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p
     ld = logits.stride(0) if T > 1 else V
     if ld < V or (V > 1 and logits.stride(1) != 1):
         raise ValueError("logits must have contiguous rows that do not overlap")
-    te, tp, mp = (None if t is None else _take(t, torch.float32, (T,), n, dev)
-                  for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")))
-    tk = None if top_k is None else _take(top_k, torch.int32, (T,), "top_k", dev)
+    each = (T,)
+    te = None if temperature is None else _take(temperature, torch.float32, each, "temperature", dev)
+    tk = None if top_k is None else _take(top_k, torch.int32, each, "top_k", dev)
+    tp = None if top_p is None else _take(top_p, torch.float32, each, "top_p", dev)
+    mp = None if min_p is None else _take(min_p, torch.float32, each, "min_p", dev)
     un = to = pr = None
     pr_ld = 0
     if probs is not None:
         pr, pr_ld = _take_probs(probs, (T, V), "probs", dev)
     if uniforms is not None:
-        un = _take(uniforms, torch.float32, (T,), "uniforms", dev)
+        un = _take(uniforms, torch.float32, each, "uniforms", dev)
         if token is None:
             token = _make(lambda: torch.empty(T, dtype=torch.int32, device=dev), dev, stream)
     elif token is not None:
@@ -712,7 +723,7 @@ def irm_sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p
     elif probs is None:
         raise ValueError("neither uniforms nor probs: nothing to compute")
     if token is not None:
-        to = _take(token, torch.int32, (T,), "token", dev)
+        to = _take(token, torch.int32, each, "token", dev)
     workspace, ws, ws_bytes = _take_workspace(workspace, lambda: WORKSPACE_HEADER, dev, stream)
     if T > 0:
         _launch(lib().irm_sample, dev, stream, logits.data_ptr(), int(logits.dtype is torch.bfloat16), ld, T, V, te, tk, tp, mp, un, to, pr,
