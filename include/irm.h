@@ -164,8 +164,8 @@ irm_status irm_device_status(void* workspace, cudaStream_t stream);
 
 /*
  * Self-test of the bounded pipeline waits (the pages have no counterpart; for tests).  Launches
- * two warps on `stream`, one for each form of the wait, that wait on a barrier nothing ever
- * arrives on; both give up after their time limit (2 s), exactly as a stalled pipeline wait of
+ * a warp for each form of the wait on `stream`, which wait on a barrier nothing ever arrives
+ * on; all give up after their time limit (2 s), exactly as a stalled pipeline wait of
  * the other kernels would, and the timeout bit of the workspace status word is set.
  * irm_device_status() then returns IRM_ERR_DEVICE_TIMEOUT, and the context stays usable.
  *   workspace  device, 256-byte aligned, >= IRM_WORKSPACE_HEADER bytes (its status word is used)

@@ -44,6 +44,33 @@ __device__ __forceinline__ void bulk_to_peer(uint32_t cluster_addr, uint32_t src
                : "memory");
 }
 
+// The bounded waits of ptx.cuh in fewer instructions: the tree attention kernel's warps wait in some forty places, and
+// with those its code does not fit the SM's instruction cache (8-bit cache, 64 x 32768 rows: 1210 us, with these
+// 1110).  try_wait suspends the thread for a while, so the clock is read on every turn.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_wait_compact(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  uint64_t since = 0;
+#pragma unroll 1
+  while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+    const uint64_t now = globaltimer_ns();
+    if (since == 0) since = now;
+    if ((abort_flag != nullptr && *abort_flag) || now - since > kWaitLimitNs) return false;
+  }
+  return true;
+}
+// By a whole warp, which agrees on the verdict.
+template <bool kCluster>
+__device__ __forceinline__ bool warp_wait_compact(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait_compact<kCluster>(bar, parity, abort_flag));
+}
+
+// 16-byte load from this CTA's shared memory.
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
+  return v;
+}
+
 // Arrive (once) on the mbarrier at this offset in every CTA of `mask` when all UMMAs issued so
 // far are complete.
 __device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mask) {

@@ -115,7 +115,7 @@ enum : int {
   BAR_INV = BAR_Q + 1,               // the peer rows' 1 / l arrived (1 + tx)
   BAR_DRAIN = BAR_INV + 1,           // [2] all UMMAs of an issuer done
   BAR_X_HALF = BAR_DRAIN + 2,        // [2][32 rows] the peer's partial scores, keys 0 to 31 (1 + tx)
-  BAR_LANDED = BAR_X_HALF + 4,       // [stage] TMA bytes of the page (1 + tx); 8-bit: the first 64 of each 128 columns as bf16 (4 warps)
+  BAR_LANDED = BAR_X_HALF + 4,       // [stage] TMA bytes of the page (1 + tx); 8-bit: its cKV is there as bf16 (4 warps)
 };
 
 // What depends on the cache's type: pages in shared memory, and the barriers of their ring.
@@ -134,8 +134,7 @@ struct Layout {
   static constexpr int BAR_RAW_FULL = BAR_FREE + kStages;  // 8-bit: [raw] TMA bytes of the codes (1 + tx)
   static constexpr int BAR_RAW_FREE = BAR_RAW_FULL + kRaw; // [raw] codes read (4 warps)
   static constexpr int BAR_KR = BAR_RAW_FREE + kRaw;       // [2] TMA bytes of k_r (1 + tx)
-  static constexpr int BAR_REST = BAR_KR + 2;               // 8-bit: [stage] the columns behind the first 64 of each 128 (4 warps)
-  static constexpr int kBars = kCodes8 ? BAR_REST + kStages : BAR_CLEAR + kStages;
+  static constexpr int kBars = kCodes8 ? BAR_KR + 2 : BAR_CLEAR + kStages;
   static_assert(kBM * 128 <= 2 * kSlab && kStages >= kQStage + 2, "Q's place");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kBars * 8 <= kOffTmem, "barrier area");
@@ -298,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(BAR_LANDED + s), kCodes8 ? kConvWarps : 1);
       mbar_init(bar(BAR_FREE + s), kCodes8 ? 1 : 2);
-      if (kCodes8) mbar_init(bar(L::BAR_REST + s), kConvWarps); else mbar_init(bar(L::BAR_CLEAR + s), 1);
+      if (!kCodes8) mbar_init(bar(L::BAR_CLEAR + s), 1);
     }
     if (kCodes8) {
       for (int s = 0; s < kRaw; ++s) {
@@ -375,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
     const bool valid = m < rows_valid;
     // ---- Q, this CTA's cKV columns: from shared memory (where TMA put it) to TMEM; set h takes
     //      slabs 2h, 2h + 1
-    ok = warp_wait(bar(BAR_QIN), 0, abort_flag);
+    ok = warp_wait_compact<false>(bar(BAR_QIN), 0, abort_flag);
     if (live && ok) {
 #pragma unroll
       for (int slab = 2 * set; slab < 2 * set + 2; ++slab) {
@@ -420,11 +419,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
     // turn late, after it has shipped the scores of tile t + 2, so that the peer never waits for it;
     // P V waits for this only where a factor is not 1.
     auto take_factors = [&](int t) -> bool {
-      if (!warp_wait_cluster(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
+      if (!warp_wait_compact<true>(bar(BAR_PR_FULL + set), (uint32_t)(t >> 1) & 1u, abort_flag)) return false;
       if (lane == 0 && t + 2 < ntiles) mbar_arrive_expect_tx(bar(BAR_PR_FULL + set), kPrBytes);
       const float corr = corr_sh[(t & 3) * kHalf + mh];
       if (t > 0 && __any_sync(kFull, corr != 1.f)) {
-        if (!warp_wait(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
+        if (!warp_wait_compact<false>(bar(BAR_PV), (uint32_t)(t - 1) & 1u, abort_flag)) return false;
         tc_fence_after();
         rescale_o(tO, corr);
         tc_fence_before();
@@ -440,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
       uint32_t s[64];
       uint64_t see = 0;  // read before the waits
       if (own && j >= tail && valid) see = seen_rows(mask, a.mask_words, (kb + j) * kPage, ctx, n);
-      if (!(ok = warp_wait(bar(BAR_S_FULL + set), ph, abort_flag))) break;
+      if (!(ok = warp_wait_compact<false>(bar(BAR_S_FULL + set), ph, abort_flag))) break;
       tc_fence_after();
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
       tmem_ld32(tS + 32u, reinterpret_cast<uint32_t(&)[32]>(s[32]));
@@ -453,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         // ================= softmax of a row =================
         // the maximum is taken over each half of the scores as it comes
         float v[64];
-        if (!(ok = warp_wait_cluster(bar(BAR_X_HALF + xq), ph, abort_flag))) break;
+        if (!(ok = warp_wait_compact<true>(bar(BAR_X_HALF + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint4 x = X[i * kHalf + mh];
@@ -472,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         for (int i = 0; i < 10; ++i) u[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
         u[10] = fmaxf(v[30], v[31]);
         const float low = fmax3(fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmax3(u[6], u[7], u[8])), u[9], u[10]);
-        if (!(ok = warp_wait_cluster(bar(BAR_X_FULL + xq), ph, abort_flag))) break;
+        if (!(ok = warp_wait_compact<true>(bar(BAR_X_FULL + xq), ph, abort_flag))) break;
 #pragma unroll
         for (int i = 8; i < 16; ++i) {
           const uint4 x = X[i * kHalf + mh];
@@ -505,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
           }
           mbar_arrive_remote_relaxed(remXfree + (vote & a.zero));
         }
-        if (j > 0 && !(ok = warp_wait(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+        if (j > 0 && !(ok = warp_wait_compact<false>(bar(BAR_MAX + (quad & 1)), (uint32_t)(j - 1) & 1u, abort_flag))) break;
         const float before = j > 0 ? max_sh[mh] : -INFINITY;
         const bool up = top > before + 8.f;
         const float now = up ? top : before;
@@ -528,7 +527,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         }
         const float2 part = f2_unpack(f2_add(sum[0], sum[1]));
         l += part.x + part.y;
-        if (j >= 2 && !(ok = warp_wait_cluster(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = warp_wait_compact<true>(bar(BAR_P_FREE + set), ph ^ 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint4 w = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
@@ -542,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         const bool moved = __any_sync(kFull, corr != 1.f);
         if (lane == 0) st_async_b32(remFlag, moved ? 1u : 0u, remPfull);
         if (j > 0 && moved) {
-          if (!(ok = warp_wait(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
+          if (!(ok = warp_wait_compact<false>(bar(BAR_PV), (uint32_t)(j - 1) & 1u, abort_flag))) break;
           tc_fence_after();
           rescale_o(tO, corr);
         }
@@ -551,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         if (lane == 0) mbar_arrive(bar(BAR_GO + set));
       } else {
         // ================= partial scores of the peer's rows =================
-        if (j >= 1 && !(ok = warp_wait_cluster(bar(BAR_X_FREE + (xq ^ 2)), (uint32_t)((j - 1) >> 1) & 1u, abort_flag))) break;
+        if (j >= 1 && !(ok = warp_wait_compact<true>(bar(BAR_X_FREE + (xq ^ 2)), (uint32_t)((j - 1) >> 1) & 1u, abort_flag))) break;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           st_async_v4_b32(remX + (uint32_t)(i * kHalf + mh) * 16u, make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]),
@@ -575,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
       const int y = __shfl_sync(kFull, page, j & 31) * kPage;
       if constexpr (kCodes8) {
         const int r = j % kRaw;
-        if (j >= kRaw && !(ok = warp_wait(bar(L::BAR_RAW_FREE + r), ((uint32_t)(j / kRaw) & 1u) ^ 1u, abort_flag))) break;
+        if (j >= kRaw && !(ok = warp_wait_compact<false>(bar(L::BAR_RAW_FREE + r), ((uint32_t)(j / kRaw) & 1u) ^ 1u, abort_flag))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::BAR_RAW_FULL + r), kCodes);
 #pragma unroll
@@ -587,8 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
       }
       const int s = j % kStages;
       // stages 2 and 3 hold Q until it is in TMEM
-      if (j == 2 && !(ok = warp_wait(bar(BAR_Q), 0, abort_flag))) break;
-      if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
+      if (j == 2 && !(ok = warp_wait_compact<false>(bar(BAR_Q), 0, abort_flag))) break;
+      if (j >= kStages && !(ok = warp_wait_compact<false>(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         mbar_arrive_expect_tx(bar(BAR_LANDED + s), kStage + kKr);
@@ -597,27 +596,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
       }
       sent = j + 1;
       // the k_r buffer's last page has been through Q K^T
-      if (j >= 2 && !(ok = warp_wait(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+      if (j >= 2 && !(ok = warp_wait_compact<false>(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) tma_load_2d(sb + kOffKr + (uint32_t)(j & 1) * kKr, &a.map_rope, kDLat + 32 * rank, y, bar(BAR_LANDED + s));
     }
     // the copies in flight land before the CTA ends, whatever became of the others
-    ok = warp_wait(bar(BAR_QIN), 0, nullptr) && ok;
+    ok = warp_wait_compact<false>(bar(BAR_QIN), 0, nullptr) && ok;
     constexpr int kFlight = kCodes8 ? kRaw : kStages, kBar = kCodes8 ? L::BAR_RAW_FULL : BAR_LANDED;
     for (int j = max(0, sent - kFlight); j < sent; ++j)
-      ok = warp_wait(bar(kBar + j % kFlight), (uint32_t)(j / kFlight) & 1u, nullptr) && ok;
+      ok = warp_wait_compact<false>(bar(kBar + j % kFlight), (uint32_t)(j / kFlight) & 1u, nullptr) && ok;
     __syncwarp();
     cluster_wait();
   } else if (warp == kSWarp) {
     // ================= Q K^T (one thread) =================
     if (lane == 0) {
-      ok = mbar_wait(bar(BAR_QIN), 0, abort_flag) && mbar_wait(bar(BAR_Q), 0, abort_flag);
+      ok = mbar_wait_compact<false>(bar(BAR_QIN), 0, abort_flag) && mbar_wait_compact<false>(bar(BAR_Q), 0, abort_flag);
       tc_fence_after();
       const uint64_t aq = sdesc_sw64(sb + kOffQr, 512);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int s = j % kStages, set = j & 1;
-        if (!kCodes8 && !(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
-        if (kCodes8 && !(ok = mbar_wait(bar(L::BAR_KR + set), (uint32_t)(j >> 1) & 1u, abort_flag))) break;
-        if (j >= 2 && !(ok = mbar_wait(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+        if (!kCodes8 && !(ok = mbar_wait_compact<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+        if (kCodes8 && !(ok = mbar_wait_compact<false>(bar(L::BAR_KR + set), (uint32_t)(j >> 1) & 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = mbar_wait_compact<false>(bar(BAR_S_FREE + set), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         tc_fence_after();
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         const uint64_t bd = sdesc_sw128(st, 16, 1024), bk = sdesc_sw64(sb + kOffKr + (uint32_t)set * kKr, 512);
@@ -633,13 +632,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         };
         if constexpr (kCodes8) {  // in the order in which they come
           rope(0u);
-          if (!(ok = mbar_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+          if (!(ok = mbar_wait_compact<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
           tc_fence_after();
           slab(0, 1u);
-          slab(2, 1u);
-          if (!(ok = mbar_wait(bar(L::BAR_REST + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
-          tc_fence_after();
           slab(1, 1u);
+          slab(2, 1u);
           slab(3, 1u);
         } else {
           slab(0, 0u);
@@ -651,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         umma_commit(bar(BAR_S_FULL + set));
       }
       umma_commit(bar(BAR_DRAIN));
-      ok = mbar_wait(bar(BAR_DRAIN), 0, nullptr) && ok;
+      ok = mbar_wait_compact<false>(bar(BAR_DRAIN), 0, nullptr) && ok;
     }
     __syncwarp();
     cluster_wait();
@@ -663,19 +660,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         const int s = j % kStages, set = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
         if (!kCodes8 && j >= tail) {
-          if (!(ok = mbar_wait(bar(L::BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
+          if (!(ok = mbar_wait_compact<false>(bar(L::BAR_CLEAR + s), (uint32_t)((j - tail) / kStages) & 1u, abort_flag))) break;
           fence_proxy_async_smem();  // the cleared rows' plain stores
         }
-        if (live_own && !(ok = mbar_wait(bar(BAR_GO + set), ph, abort_flag))) break;
+        if (live_own && !(ok = mbar_wait_compact<false>(bar(BAR_GO + set), ph, abort_flag))) break;
         if (live_peer) {
-          if (!(ok = mbar_wait_cluster(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
+          if (!(ok = mbar_wait_compact<true>(bar(BAR_PR_FULL + set), ph, abort_flag))) break;
           uint32_t f0, f1;
           asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(f0), "=r"(f1) : "r"(sb + kOffFlag + 8u * (uint32_t)set) : "memory");
           // a rescaling waits for P V of the tile before, so these phases are passed one by one
           const uint32_t moved = j > 0 ? f0 | (live_peer > 1 ? 2u * f1 : 0u) : 0u;
           if (moved != 0) {
-            if (moved & 1u) ok = mbar_wait(bar(BAR_RESC), resc & 1u, abort_flag);
-            if (ok && moved & 2u) ok = mbar_wait(bar(BAR_RESC + 1), resc >> 1, abort_flag);
+            if (moved & 1u) ok = mbar_wait_compact<false>(bar(BAR_RESC), resc & 1u, abort_flag);
+            if (ok && moved & 2u) ok = mbar_wait_compact<false>(bar(BAR_RESC + 1), resc >> 1, abort_flag);
             resc ^= moved;
             if (!ok) break;
           }
@@ -691,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         umma_commit_multicast(bar(BAR_P_FREE + set), (uint16_t)3);
       }
       umma_commit(bar(BAR_DRAIN + 1));
-      ok = mbar_wait(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
+      ok = mbar_wait_compact<false>(bar(BAR_DRAIN + 1), 0, nullptr) && ok;
     }
     __syncwarp();
     cluster_wait();
@@ -727,10 +724,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         const uint32_t lo = __reduce_or_sync(kFull, (uint32_t)see), hi = __reduce_or_sync(kFull, (uint32_t)(see >> 32));
         seen = ((warp & 1 ? hi : lo) >> lane & 1u) != 0;
       }
-      if (!(ok = warp_wait(bar(L::BAR_RAW_FULL + raw), (uint32_t)(j / kRaw) & 1u, abort_flag))) break;
+      if (!(ok = warp_wait_compact<false>(bar(L::BAR_RAW_FULL + raw), (uint32_t)(j / kRaw) & 1u, abort_flag))) break;
       // the second and third page's places hold Q until it is in TMEM
-      if (j == L::kQStage && !(ok = warp_wait(bar(BAR_Q), 0, abort_flag))) break;
-      if (j >= kStages && !(ok = warp_wait(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
+      if (j == L::kQStage && !(ok = warp_wait_compact<false>(bar(BAR_Q), 0, abort_flag))) break;
+      if (j >= kStages && !(ok = warp_wait_compact<false>(bar(BAR_FREE + s), ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag))) break;
       // zeros for an unseen row (a code's bits are a finite number, whatever it is)
       const __nv_bfloat162 m = __float2bfloat162_rn(seen ? __uint_as_float(scale & 0xffff0000u) * 0x1p120f : 0.f);
       const uint32_t from = sb + L::kOffRaw + (uint32_t)raw * kCodes + (uint32_t)box * kSlab + (uint32_t)r * 128u;
@@ -745,20 +742,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         const uint32_t at = to + (i >> 2) * kRing + ((2u * i & 7u ^ (uint32_t)(r & 7)) << 4);
         st_shared_v4(at, make_uint4(a0.x, a0.y, a1.x, a1.y));
         st_shared_v4(at ^ 16u, make_uint4(a2.x, a2.y, a3.x, a3.y));
-        if (i == 3) {
-          fence_proxy_async_smem();  // read by the tensor core
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_LANDED + s));
-        }
       }
       // The copy of a later page may overwrite the codes once they have been read: as with the received scores, the
       // arrival that says so depends on what was read last (without that, loads were still under way in a full SM
       // and read the later page's codes).
       const uint32_t vote = __ballot_sync(kFull, v.x != 0u);
       if (lane == 0) mbar_arrive(bar(L::BAR_RAW_FREE + raw) + (vote & a.zero));
-      fence_proxy_async_smem();
+      fence_proxy_async_smem();  // read by the tensor core
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::BAR_REST + s));
+      if (lane == 0) mbar_arrive(bar(BAR_LANDED + s));
     }
     __syncwarp();
     cluster_wait();
@@ -786,14 +778,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         }
         const int y = __shfl_sync(kFull, page, j & 31) * kPage;
         // the buffer's last page has been through Q K^T
-        if (j >= 2 && !(ok = warp_wait(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
+        if (j >= 2 && !(ok = warp_wait_compact<false>(bar(BAR_S_FULL + (j & 1)), ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::BAR_KR + (j & 1)), kKr);
           tma_load_2d(sb + kOffKr + (uint32_t)(j & 1) * kKr, &a.map_rope, IRM_ROW8_ROPE / 2 + 32 * rank, y, bar(L::BAR_KR + (j & 1)));
         }
         sent = j + 1;
       }
-      for (int j = max(0, sent - 2); j < sent; ++j) ok = warp_wait(bar(L::BAR_KR + (j & 1)), (uint32_t)(j >> 1) & 1u, nullptr) && ok;
+      for (int j = max(0, sent - 2); j < sent; ++j) ok = warp_wait_compact<false>(bar(L::BAR_KR + (j & 1)), (uint32_t)(j >> 1) & 1u, nullptr) && ok;
     } else {
     // ================= rows that no node of the unit sees become zeros =================
     const int node0 = row0 / a.H, node1 = (row0 + rows_valid - 1) / a.H;
@@ -807,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
         lo = __reduce_or_sync(kFull, (uint32_t)see);
         hi = __reduce_or_sync(kFull, (uint32_t)(see >> 32));
       }
-      if (!(ok = warp_wait(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
+      if (!(ok = warp_wait_compact<false>(bar(BAR_LANDED + s), (uint32_t)(j / kStages) & 1u, abort_flag))) break;
       if (j >= tail) {
         const uint32_t st = sb + kOffKv + (uint32_t)s * kSlab;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -869,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kCodes8>::kTh
   if (warp < kScoreWarps) {
     const int quad = warp & 3, m = quad * 32 + lane;
     if (quad * 32 < rows_valid) {
-      if ((quad >> 1) != rank && !warp_wait_cluster(bar(BAR_INV), 0, abort_flag)) set_status(a.status, kDevErrTimeout);
+      if ((quad >> 1) != rank && !warp_wait_compact<true>(bar(BAR_INV), 0, abort_flag)) set_status(a.status, kDevErrTimeout);
       const float inv = inv_sh[m];
       uint8_t* stage = smem + kOffKv + warp * 8192;
       for (int c = 128 * (warp >> 2); c < 128 * (warp >> 2) + 128; c += 64) {

@@ -179,13 +179,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t saddr, uint4 v) {
                : "memory");
 }
 
-// and load from it
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
-  return v;
-}
-
 // 16-byte store into a peer CTA's shared memory; completion is counted in bytes on the
 // peer's mbarrier (complete_tx).
 __device__ __forceinline__ void st_async_v4_b32(uint32_t cluster_addr, uint4 v, uint32_t cluster_bar) {

@@ -102,6 +102,39 @@ def test_rows_shrink_with_their_bound():
         assert part.max() <= 1.0
 
 
+@pytest.mark.parametrize("B,H,ctx,n", [(64, 128, 4096, 2), (152, 16, 3000, 1)])
+def test_a_full_gpu_repeats_and_agrees_with_the_bf16_cache(B, H, ctx, n):
+    """Every SM busy at once, many pages in turn: runs are equal bit for bit, and each row is the bf16 cache's up to the
+    roundings that both make (the output's, 2^-8, once each; the scores' and probabilities' as in
+    tree_bounds, where a row's spread over ctx independent keys is below an eighth of its norm's bound)."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pages = B * (-(-(ctx + n) // 64))
+    c = torch.randn((pages * 64, 4, 128), generator=g, device="cuda")
+    s = torch.exp2(torch.ceil(torch.log2(c.abs().amax(2) / 448.0)))
+    codes = (c / s[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    k_r = torch.randn((pages * 64, 64), generator=g, device="cuda").to(torch.bfloat16)
+    raw = torch.cat([codes.reshape(-1, 512).view(torch.uint8), s.view(torch.uint8), k_r.view(torch.uint8)], 1).reshape(pages, 64, 656)
+    wide = torch.cat([(codes.float() * s[..., None]).reshape(-1, 512).to(torch.bfloat16), k_r], 1).reshape(pages, 64, 576)
+    table = torch.randperm(pages, generator=g, device="cuda").int().reshape(B, -1).contiguous()
+    ql, qr = (torch.randn((B * n, H, w), generator=g, device="cuda").div(13.9).to(torch.bfloat16) for w in (512, 64))
+    mask = torch.tensor([(1 << (i + 1)) - 1 for i in range(n)] * B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    args = (np.full(B, ctx), np.arange(B + 1) * n)
+    ws = irm.new_workspace(irm.tree_workspace_size(*args, H))
+    runs = []
+    for _ in range(4):
+        lse = torch.empty((B * n, H), device="cuda")
+        out, _, _ = irm.irm_mla_attn_tree(ql, qr, *args, raw, table, mask, SCALE, lse=lse, workspace=ws)
+        runs.append((out, lse))
+    lse = torch.empty((B * n, H), device="cuda")
+    want, _, _ = irm.irm_mla_attn_tree(ql, qr, *args, wide, table, mask, SCALE, lse=lse, workspace=ws)
+    irm.device_status(ws)
+    for o, l in runs:
+        assert torch.equal(o, runs[0][0]) and torch.equal(l, runs[0][1])
+    d = (runs[0][0].double() - want.double()).norm(dim=2) / want.double().norm(dim=2)
+    assert float(d.max()) <= 2 * 2.0 ** -8
+    assert float((runs[0][1] - lse).abs().max()) <= 2 * (576 * 2.0 ** -22 * 4 + 2.0 ** -16)
+
+
 def test_every_code_and_scale():
     """Each of the codes reaches the output as its value: one row seen by itself has weight 1, so O is the row (exact
     in bf16); scales over their whole range."""
