@@ -213,30 +213,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const __nv_bfloat16* b16 = static_cast<const __nv_bfloat16*>(a.logits) + b * a.ld + v0;
   cluster_arrive();  // waited for before the first store into a peer's shared memory
 
-  // four consecutive logits of the CTA's part (behind its end: -infinity)
-  auto fetch = [&](int i) -> float4 {
-    float x[4];
-    if (a.vec_in && i + 4 <= n_own) {
-      if (BF16) {
-        const uint2 w = *reinterpret_cast<const uint2*>(b16 + i);
-        x[0] = __uint_as_float(w.x << 16);
-        x[1] = __uint_as_float(w.x & 0xffff0000u);
-        x[2] = __uint_as_float(w.y << 16);
-        x[3] = __uint_as_float(w.y & 0xffff0000u);
-      } else {
-        const float4 w = *reinterpret_cast<const float4*>(f32 + i);
-        x[0] = w.x;
-        x[1] = w.y;
-        x[2] = w.z;
-        x[3] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = i + e < n_own ? (BF16 ? __bfloat162float(b16[i + e]) : f32[i + e]) : -INFINITY;
-    }
-    return make_float4(clean(x[0]), clean(x[1]), clean(x[2]), clean(x[3]));
-  };
-  auto four = [&](int i) -> float4 { return RES ? *reinterpret_cast<const float4*>(row_sh + i) : fetch(i); };
   auto one = [&](int i) -> float { return RES ? row_sh[i] : clean(BF16 ? __bfloat162float(b16[i]) : f32[i]); };
   // A warp looks at a contiguous part of the CTA's logits, a group (four neighbours a lane) at a time.
   const int wseg = (n_own + kWarps * kGroup - 1) / (kWarps * kGroup) * kGroup;
@@ -317,17 +293,43 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   // ---- the row, and its maximum ------------------------------------------------------------
   float best = -INFINITY;
-  constexpr int kAhead = 4;
-  for (int i0 = w0 + 4 * lane; i0 - 4 * lane < w1; i0 += kAhead * kGroup) {
-    float4 x[kAhead];
+  if (RES && a.vec_in) {
+    constexpr int kAhead = 4;
+    const int whole = w0 + (w1 - w0) / 4 * 4;  // w0 is a multiple of 4
+    for (int i = w0 + 4 * lane; i < whole; i += kAhead * kGroup) {
+      float4 x[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) x[u] = fetch(min(i0 + u * kGroup, a.seg - 4));  // behind the end: -infinity
+      for (int u = 0; u < kAhead; ++u) {
+        const int at = min(i + u * kGroup, whole - 4);  // the last one again: neither stored nor counted amiss
+        if (BF16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(b16 + at);
+          x[u] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                             __uint_as_float(w.y & 0xffff0000u));
+        } else {
+          x[u] = *reinterpret_cast<const float4*>(f32 + at);
+        }
+      }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (RES && i0 + u * kGroup < w1) *reinterpret_cast<float4*>(row_sh + i0 + u * kGroup) = x[u];
-      if (i0 + u * kGroup < w1) best = fmaxf(best, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
+      for (int u = 0; u < kAhead; ++u) {
+        x[u] = make_float4(clean(x[u].x), clean(x[u].y), clean(x[u].z), clean(x[u].w));
+        *reinterpret_cast<float4*>(row_sh + min(i + u * kGroup, whole - 4)) = x[u];
+        best = fmaxf(best, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
+      }
+    }
+    if (lane < w1 - whole) {
+      const float x = clean(BF16 ? __bfloat162float(b16[whole + lane]) : f32[whole + lane]);
+      row_sh[whole + lane] = x;
+      best = fmaxf(best, x);
+    }
+  } else {
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const float x = clean(BF16 ? __bfloat162float(b16[i]) : f32[i]);
+      if (RES) row_sh[i] = x;
+      best = fmaxf(best, x);
     }
   }
+  __syncwarp();  // a warp reads what its own lanes have stored
   cluster_wait();
   uint64_t top[1] = {order_key(best)};
   cluster_sum(top, true);
@@ -335,21 +337,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (tid == 0) sh.m = m;
   __syncthreads();
   float* probs = a.probs ? a.probs + b * a.probs_ld + v0 : nullptr;
-  // p(i) for the CTA's probabilities, four neighbours at a time
-  auto write_probs = [&](auto p) {
-    for (int i = 4 * tid; i < n_own; i += 4 * kThreads) {
-      const float4 y = p(i);
-      if (a.vec_out && i + 4 <= n_own) {
-        *reinterpret_cast<float4*>(probs + i) = y;
-      } else {
-        const float z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < n_own) probs[i + e] = z[e];
-      }
-    }
+  auto zero_probs = [&] {
+    const int whole = a.vec_out ? w0 + (w1 - w0) / 4 * 4 : w0;
+    for (int i = w0 + 4 * lane; i < whole; i += kGroup) *reinterpret_cast<float4*>(probs + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = whole + lane; i < w1; i += 32) probs[i] = 0.f;
   };
-  auto zero_probs = [&] { write_probs([](int) { return make_float4(0.f, 0.f, 0.f, 0.f); }); };
 
   const bool none = m == -INFINITY;
   if (none || first_alone) {  // the same in every CTA of the cluster
@@ -475,16 +467,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // the row stays what is looked at.
   auto list_candidates = [&](int last) {
     if (!RES || n_cand >= 0) return;
+    const float edge = (float)(last + 1);
     auto in = [&](float l) -> bool {
       const float t = octaves(l, m, half, ch);
-      return t > -kOctaves && bin_of(t) <= last;
+      return t > -kOctaves && -t * kBinScale < edge;  // bin_of(t) <= last
     };
     uint32_t n = 0;
-    for (int i = w0 + 4 * lane; i < w1; i += kGroup) {
-      const float4 x = four(i);
-      n += (in(x.x) ? 1u : 0u) + (in(x.y) ? 1u : 0u) + (in(x.z) ? 1u : 0u) + (in(x.w) ? 1u : 0u);
-    }
-    n = __reduce_add_sync(kFull, n);
+#pragma unroll 4
+    for (int i = w0; i < w1; i += 32) n += __popc(__ballot_sync(kFull, i + lane < w1 && in(one(i + lane))));
     __syncthreads();
     if (lane == 0) sh.scan[warp] = n;
     __syncthreads();
@@ -495,24 +485,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     if (all > (uint32_t)a.cap) return;
     const uint32_t first = at;
-    for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += kGroup) {
-      const float4 x = i < w1 ? four(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      const float y[4] = {x.x, x.y, x.z, x.w};
-      bool p[4];
-      uint32_t c = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c += (p[e] = in(y[e])) ? 1u : 0u;
-      uint32_t incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t z = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += z;
-      }
-      uint32_t to = at + incl - c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (p[e]) cand[to++] = Item{y[e], v0 + i + e, 0};
-      at += __shfl_sync(kFull, incl, 31);
+#pragma unroll 4
+    for (int i = w0; i < w1; i += 32) {
+      const float l = i + lane < w1 ? one(i + lane) : -INFINITY;
+      const bool p = in(l);
+      const uint32_t mask = __ballot_sync(kFull, p);
+      if (p) cand[at + __popc(mask & ((1u << lane) - 1u))] = Item{l, v0 + i + lane, 0};
+      at += __popc(mask);
     }
     __syncwarp();
     for (uint32_t i = first + lane; i < at; i += 32) cand[i].w = weight_of(cand[i].l, m, sh);
@@ -525,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     w_before = 0;
     if (tid < n) {
       const Item me = sh.list[tid];
-#pragma unroll 4
+#pragma unroll 2
       for (int j = 0; j < n; ++j) {
         const Item x = sh.list[j];
         if (x.l > me.l || (x.l == me.l && x.idx < me.idx)) {
@@ -576,15 +555,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // The cut at the list's element where the running value (1 an element, or its weight), from `above` on, reaches
   // `target`; false where none does.
   auto cut_in_list = [&](bool weights, uint64_t target, uint64_t above, uint32_t n) -> bool {
-    uint64_t wb;
-    const int r = rank_in_list((int)n, wb);
     bool here = false;
-    if ((uint32_t)tid < n) {
-      const Item me = sh.list[tid];
-      const uint64_t x = above + (weights ? wb : (uint64_t)r);
-      here = x < target && x + (weights ? me.w : 1ull) >= target;
-      if (here) {
-        sh.cut_l = me.l;
+    constexpr uint32_t kLanes = 4;  // of an element
+    for (uint32_t e0 = 0; e0 < n; e0 += kThreads / kLanes) {
+      const uint32_t e = e0 + tid / kLanes;
+      const Item me = sh.list[e < n ? e : 0];
+      uint64_t x = 0;
+#pragma unroll 2
+      for (uint32_t j = tid % kLanes; j < n; j += kLanes) {
+        const Item y = sh.list[j];
+        if (y.l > me.l || (y.l == me.l && y.idx < me.idx)) x += weights ? y.w : 1ull;
+      }
+      x += __shfl_xor_sync(kFull, x, 1);
+      x += __shfl_xor_sync(kFull, x, 2) + above;
+      if (e < n && x < target && x + (weights ? me.w : 1ull) >= target) {
+        here = true;
+        sh.cut_l = me.l;  // all lanes of the one element
         sh.cut_idx = me.idx;
       }
     }
@@ -811,43 +797,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the sum of what is left, by groups of a warp's elements ------------------------------------
   const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
   const bool listed = n_cand >= 0;
-  auto left = [&](float l, int idx) -> uint64_t {
-    if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, idx)) return 0ull;
-    const uint64_t w = weight(l, m, sh);
+  const int n_left = listed ? n_cand : n_own, groups = (n_left + kGroup - 1) / kGroup;
+  // the weight left of element i of what is looked at (behind its end: none)
+  auto left = [&](int i, auto weigh) -> uint64_t {
+    if (i >= n_left) return 0ull;
+    if (listed) {
+      const Item z = cand[i];
+      return kept(z.l, z.idx) && z.w >= least ? z.w : 0ull;
+    }
+    const float l = one(i);
+    if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, v0 + i)) return 0ull;
+    const uint64_t w = weigh(l);
     return w >= least ? w : 0ull;
   };
-  // the weights left of element group g: a lane's four neighbours
-  const int groups = ((listed ? n_cand : n_own) + kGroup - 1) / kGroup;
-  auto group = [&](int g, uint64_t (&x)[4], int (&at)[4]) {
-    const int i = g * kGroup + 4 * lane;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = 0;
-      at[e] = v0 + i + e;
-    }
-    if (listed) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < n_cand) {
-          const Item z = cand[i + e];
-          at[e] = z.idx;
-          x[e] = kept(z.l, z.idx) && z.w >= least ? z.w : 0ull;
-        }
-    } else if (i < n_own) {
-      const float4 y = four(i);
-      x[0] = left(y.x, v0 + i);
-      x[1] = left(y.y, v0 + i + 1);
-      x[2] = left(y.z, v0 + i + 2);
-      x[3] = left(y.w, v0 + i + 3);
-    }
-  };
+  auto called = [&](float l) -> uint64_t { return weight_of(l, m, sh); };
   __syncthreads();
   uint64_t s[1] = {0};
   for (int g = warp; g < groups; g += kWarps) {
-    uint64_t x[4];
-    int at[4];
-    group(g, x, at);
-    uint64_t w = x[0] + x[1] + x[2] + x[3];
+    uint64_t w = 0;
+#pragma unroll 2
+    for (int e = 0; e < kGroup; e += 32) w += left(g * kGroup + e + lane, [&](float l) -> uint64_t { return weight(l, m, sh); });
     s[0] += w;
     w = __any_sync(kFull, w != 0) ? warp_sum64(w) : 0ull;
     if (lane == 0) sh.u.gsum[g] = w;
@@ -866,16 +835,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     } else {
       // min-p in octaves: what is right at it goes by the weight itself
       const float edge = min_p > 0.f ? log2f(min_p) : -INFINITY;
-      write_probs([&](int i) {
-        const float4 x = four(i);
-        auto p = [&](float l, int idx) {
-          const float t = octaves(l, m, half, ch);
-          bool stay = t > -kOctaves && kept(l, idx) && t >= edge - 0.001f;
-          if (stay && t < edge + 0.001f) stay = left(l, idx) != 0;
-          return stay ? fast_exp2(t) * inv : 0.f;
-        };
-        return make_float4(p(x.x, v0 + i), p(x.y, v0 + i + 1), p(x.z, v0 + i + 2), p(x.w, v0 + i + 3));
-      });
+      auto p = [&](int i) -> float {
+        const float l = one(i), t = octaves(l, m, half, ch);
+        bool stay = t > -kOctaves && kept(l, v0 + i) && t >= edge - 0.001f;
+        if (stay && t < edge + 0.001f) stay = left(i, called) != 0;
+        return stay ? fast_exp2(t) * inv : 0.f;
+      };
+#pragma unroll 4
+      for (int i = w0 + lane; i < w1; i += 32) probs[i] = p(i);
     }
   }
   // ---- the token: the group, then the element, where the running sum passes r of the total ---------------
@@ -883,36 +850,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     uint64_t at = part_of_sum(rf, total, false);
     if (at >= total) at = total - 1;
     uint64_t run = start;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-      const uint64_t w = g0 + lane < groups ? sh.u.gsum[g0 + lane] : 0ull;
-      const uint64_t all = warp_sum64(w);
-      if (at < run || at >= run + all) {
-        run += all;
-        continue;
-      }
-      uint64_t incl = w;
+    // inclusive sums over the warp's lanes; true where the one that `at` falls to is among them
+    auto scan = [&](uint64_t w, uint64_t& incl) -> bool {
+      incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t x = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += x;
       }
-      const unsigned hit = __ballot_sync(kFull, at >= run + incl - w && at < run + incl);
-      run += __shfl_sync(kFull, incl - w, __ffs((int)hit) - 1);
-      uint64_t x[4];
-      int idx[4];
-      group(g0 + __ffs((int)hit) - 1, x, idx);
-      const uint64_t mine = x[0] + x[1] + x[2] + x[3];
-      incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t z = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += z;
-      }
-      uint64_t z = run + incl - mine;
-      if (at >= z && at < z + mine) {
-        int e = 0;
-        while (at >= z + x[e]) z += x[e++];
-        a.token[b] = idx[e];
+      const uint64_t all = __shfl_sync(kFull, incl, 31);
+      if (at >= run && at < run + all) return true;
+      run += all;
+      return false;
+    };
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      const uint64_t w = g0 + lane < groups ? sh.u.gsum[g0 + lane] : 0ull;
+      uint64_t incl;
+      if (!scan(w, incl)) continue;
+      const int src = __ffs((int)__ballot_sync(kFull, at >= run + incl - w && at < run + incl)) - 1;
+      run += __shfl_sync(kFull, incl - w, src);
+      for (int e = 0; e < kGroup; e += 32) {
+        const int i = (g0 + src) * kGroup + e + lane;
+        const uint64_t x = left(i, called);
+        if (!scan(x, incl)) continue;
+        if (at >= run + incl - x && at < run + incl) a.token[b] = listed ? cand[i].idx : v0 + i;
+        break;
       }
       break;
     }
