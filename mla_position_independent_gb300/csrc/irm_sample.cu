@@ -51,8 +51,8 @@ static_assert(kList <= kThreads && 2 * kThreads == kBins, "a thread an element, 
 struct SampleArgs {
   const void* logits;
   int64_t ld;
-  int V, seg;  // logits of a row, and of a CTA's part of it (a multiple of 4)
-  int cap;     // candidates that a CTA can hold in shared memory, with their weights
+  int V, seg;    // logits of a row, and of a CTA's part of it (a multiple of 4)
+  int cap;       // candidates that a CTA can hold in shared memory, with their weights
   const float *temperature, *top_p, *min_p, *uniforms;
   const int32_t* top_k;
   int32_t* token;
@@ -218,13 +218,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int wseg = (n_own + kWarps * kGroup - 1) / (kWarps * kGroup) * kGroup;
   const int w0 = min(n_own, warp * wseg), w1 = min(n_own, w0 + wseg);
   // f(logit, index, weight()) for the CTA's logits, or for the candidates once they are listed (in index order)
-  Item* cand = reinterpret_cast<Item*>(row_sh + (RES ? a.seg : 0));
+  uint64_t* cand_w = reinterpret_cast<uint64_t*>(row_sh + (RES ? a.seg : 0));  // their weights, and where in the row they are
+  uint16_t* cand_at = reinterpret_cast<uint16_t*>(cand_w + a.cap);
   int n_cand = -1;
   auto each = [&](auto f) {
     if (n_cand >= 0) {
       for (int i = tid; i < n_cand; i += kThreads) {
-        const Item x = cand[i];
-        f(x.l, x.idx, [&] { return x.w; });
+        const int at = cand_at[i];
+        f(row_sh[at], v0 + at, [&] { return cand_w[i]; });
       }
       return;
     }
@@ -490,11 +491,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const float l = i + lane < w1 ? one(i + lane) : -INFINITY;
       const bool p = in(l);
       const uint32_t mask = __ballot_sync(kFull, p);
-      if (p) cand[at + __popc(mask & ((1u << lane) - 1u))] = Item{l, v0 + i + lane, 0};
+      if (p) cand_at[at + __popc(mask & ((1u << lane) - 1u))] = (uint16_t)(i + lane);
       at += __popc(mask);
     }
     __syncwarp();
-    for (uint32_t i = first + lane; i < at; i += 32) cand[i].w = weight_of(cand[i].l, m, sh);
+    for (uint32_t i = first + lane; i < at; i += 32) cand_w[i] = weight_of(row_sh[cand_at[i]], m, sh);
     n_cand = (int)all;
     __syncthreads();
   };
@@ -674,11 +675,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int level = 0; level < 2; ++level) {
       const uint2 h = level == 0 ? cluster_bins() : histogram(bin);
       // the guess: counts times the weight at the bin's middle (inside one bin: of the bin)
-      const float w0 = fast_exp2(-((float)(level ? bin : 2 * tid) + 0.5f) / kBinScale), w1 = level ? w0 : w0 * fast_exp2(-1.f / kBinScale);
-      const float mass0 = w0 * (float)h.x, mass1 = w1 * (float)h.y;
+      const float mid = fast_exp2(-((float)(level ? bin : 2 * tid) + 0.5f) / kBinScale), mid1 = level ? mid : mid * fast_exp2(-1.f / kBinScale);
+      const float mass0 = mid * (float)h.x, mass1 = mid1 * (float)h.y;
       const float incl = scan_f32(mass0 + mass1);
       if (tid == kThreads - 1) sh.mass = incl;
-      const uint32_t c_incl = scan_u32(h.x + h.y), c_excl = c_incl - h.x - h.y;
+      const uint32_t c_incl = scan_u32(h.x + h.y), c_mid = c_incl - h.y, c_excl = c_mid - h.x;
       if (tid == 0) sh.bin = kBins - 1;
       __syncthreads();
       // in whole rows the share of the same sum, so that what the middles are off by cancels
@@ -691,10 +692,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         // the target
         const int last = min(guess + 12 | 1, kBins - 1);
         if (tid == last >> 1) sh.bin_above = c_incl;
-        if (tid == guess >> 1) {
-          sh.near_lo = c_excl;
-          sh.near_hi = c_incl;
-        }
+        // elements before and up to a bin, told by the thread that has it
+        auto tell_before = [&](int of) {
+          if (tid == of >> 1) sh.near_lo = of & 1 ? c_mid : c_excl;
+        };
+        auto tell_upto = [&](int of) {
+          if (tid == of >> 1) sh.near_hi = of & 1 ? c_incl : c_mid;
+        };
+        tell_before(guess);
+        tell_upto(guess);
         __syncthreads();
         const uint32_t n = sh.bin_above;
         if (n <= (uint32_t)kList) {
@@ -720,12 +726,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           sh.bin_count = 0;
         }
         __syncthreads();
-        if (c_excl + wing >= lo_c) atomicMin(&sh.bin, 2 * tid);
-        if (c_incl <= hi_c + wing) atomicMax(&sh.bin_count, (uint32_t)(2 * tid + 1));
+        if (c_mid + wing >= lo_c) atomicMin(&sh.bin, c_excl + wing >= lo_c ? 2 * tid : 2 * tid + 1);
+        if (c_mid <= hi_c + wing) atomicMax(&sh.bin_count, (uint32_t)(c_incl <= hi_c + wing ? 2 * tid + 1 : 2 * tid));
         __syncthreads();
-        const int near_first = sh.bin, near_last = min((int)sh.bin_count, last);
-        if (tid == near_first >> 1) sh.near_lo = c_excl;
-        if (tid == near_last >> 1) sh.near_hi = c_incl;
+        const int near_first = min(sh.bin, guess), near_last = max(guess, min((int)sh.bin_count, last));
+        tell_before(near_first);
+        tell_upto(near_last);
         __syncthreads();
         const uint32_t near = sh.near_hi - sh.near_lo;
         if (near <= (uint32_t)kList) {
@@ -802,8 +808,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto left = [&](int i, auto weigh) -> uint64_t {
     if (i >= n_left) return 0ull;
     if (listed) {
-      const Item z = cand[i];
-      return kept(z.l, z.idx) && z.w >= least ? z.w : 0ull;
+      const int at = cand_at[i];
+      return kept(row_sh[at], v0 + at) && cand_w[i] >= least ? cand_w[i] : 0ull;
     }
     const float l = one(i);
     if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, v0 + i)) return 0ull;
@@ -829,8 +835,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       zero_probs();
       __syncthreads();
       for (int i = tid; i < n_cand; i += kThreads) {
-        const Item z = cand[i];
-        if (kept(z.l, z.idx) && z.w >= least) probs[z.idx - v0] = fast_exp2(octaves(z.l, m, half, ch)) * inv;
+        const int at = cand_at[i];
+        const float l = row_sh[at];
+        if (kept(l, v0 + at) && cand_w[i] >= least) probs[at] = fast_exp2(octaves(l, m, half, ch)) * inv;
       }
     } else {
       // min-p in octaves: what is right at it goes by the weight itself
@@ -873,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const int i = (g0 + src) * kGroup + e + lane;
         const uint64_t x = left(i, called);
         if (!scan(x, incl)) continue;
-        if (at >= run + incl - x && at < run + incl) a.token[b] = listed ? cand[i].idx : v0 + i;
+        if (at >= run + incl - x && at < run + incl) a.token[b] = v0 + (listed ? (int)cand_at[i] : i);
         break;
       }
       break;
@@ -960,8 +967,9 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   cfg.blockDim = dim3(kThreads);
   if (resident) {
     const size_t row = (size_t)a.seg * sizeof(float), room = (a.seg <= kPart ? kSmemTwo : kSmemOne) - sizeof(Shared) - row;
-    a.cap = (int)std::min<size_t>((size_t)a.seg, room / sizeof(Item));
-    cfg.dynamicSmemBytes = row + a.cap * sizeof(Item);
+    constexpr size_t kCand = sizeof(uint64_t) + sizeof(uint16_t);
+    a.cap = (int)std::min<size_t>((size_t)a.seg, room / kCand);
+    cfg.dynamicSmemBytes = row + a.cap * kCand;
   }
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
