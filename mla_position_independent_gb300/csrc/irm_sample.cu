@@ -6,20 +6,34 @@
 //   of their sum;  min-p of those the ones with w >= min_p;  token = lowest v with
 //   cumsum(w)(v) > r sum(w) in index order over what is left.
 // What is kept is a run of the order from its start, so it is described by its last element, a cut
-// (logit, index), and no row is sorted: a histogram of the logits' distance from the maximum (1023 bins of
-// 1 / 23 octave of w) finds the bin that holds the cut, and the few hundred elements of that bin are
-// ranked among themselves.
+// (logit, index), and no row is sorted: a histogram of the logits' distance from the maximum (1023 bins, 23
+// an octave of w) finds the bin that holds the cut.  Up to 448 elements that may be kept are ranked among
+// themselves and finished at once.  Else the candidates up to a few bins behind the cut are listed with their
+// weights (where they fit shared memory), the elements of the bins around the guess ranked (a
+// top-p cut: the histogram with each bin's middle weight only guesses, the exact sum before them decides;
+// a wrong guess moves on), and the draw is an inverse of the sums of 128-element groups, then of one group.  More
+// equal logits than can be ranked: bit by bit on the logit, then on the index.
 //
 // Arithmetic.  Which token comes out must not depend on the split or the order of addition, and a flat
 // row of 100k entries has cumulative sums 1e-5 apart, so weights are integers in units of 2^-43 and
 // their sums are exact.  fp32 exponentials (2^-23) would move 100k boundaries by 1e-7 each, so that one
 // draw in a hundred came out wrong; here a weight is good to 2^-37 of the largest: the distance from the
-// maximum and its product with 1 / T in two fp32 parts, 32 table values and a polynomial of degree 5.
-// fp64 runs at 1 / 64 of the fp32 rate on this GPU.  The histogram only guesses the bin of a top-p cut; the exact
-// sums above and inside decide, and move the guess where it was off.
+// maximum and its product with 1 / T in two fp32 parts, 32 table values and a polynomial of degree 5, some
+// 70 instructions.  fp64 runs at 1 / 64 of the fp32 rate on this GPU.  Thresholds (p of a sum, r of a sum) are
+// exact products of 24 and 64 bits.  Probabilities are fp32 exponentials over the exact sum.
 //
-// A cluster of CTAs shares a row, which stays in shared memory as fp32 from its one read where it fits (51200
+// A cluster of CTAs shares a row, which stays in shared memory as fp32 from its one read where it fits (40960
 // logits a CTA); longer rows are read again by each pass.
+//
+// What bounds it.  One row: latency, 17.2 us for 102400 logits with top-k 50 and top-p 0.9 (the row and its
+// maximum 2.6 us, the histogram and its exchange 4.1, collecting the candidates 3.2, reading the other CTAs' 2.4,
+// ranking 3.3).  Many rows with top-p alone: instructions, 384 rows with probabilities 390 us (35 by their
+// bytes), 0.61 instructions a clock and scheduler.  A quarter of that are the weights of all elements, whose
+// sum a top-p cut needs; a first sum of fp32 exponentials with a bound on its error takes a third of that
+// pass, but the rows near whose target an element lies (a tenth and more, all of a flat distribution) need the exact
+// one as well: 440 us instead of 409, not kept.  Steps that were: a pass over all elements, and one over those
+// near the cut, for each sum 635; the candidates listed with their weights 475; one element a lane and ranks by
+// four lanes an element 409; fewer neighbours and shorter lists 390.
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>

@@ -28,7 +28,17 @@
 //   - Rows that no node of the unit sees (masked drafts, rows behind the last one) may hold NaN.
 //     Their scores are replaced whatever they are; a warp clears their cKV columns in shared memory,
 //     beside Q K^T, before P V reads them.
-// Warps: 0-7 scores, 8 TMA, 9 Q K^T issue and TMEM, 10 P V issue, 11 Q and the clearing.
+// Warps: 0-7 scores, 8 TMA, 9 Q K^T issue and TMEM, 10 P V issue, 11 Q and the clearing (8-bit: Q and k_r),
+// and over an 8-bit cache 12-15 the conversion.
+//
+// 8-bit cache (tree_attn_kernel<true>; rows of 512 e4m3 codes, a scale for 128 columns, and k_r in bf16).  The
+// same kernel, but TMA brings codes (16 KiB a page and CTA, two pages in flight), and four warps turn them into
+// the bf16 tile that the tensor core reads, a thread a row of 128 columns: with a power of two as scale that
+// is exact, so scores, probabilities and O are rounded nowhere else than over a bf16 cache.  The tensor core's
+// own 8-bit form was not taken: it would need P in 8 bits, whose 2^-9 to 448 lose the many small probabilities
+// next to one large one.  A code takes 4 instructions with its loads, stores and waits; unseen rows are
+// converted with scale 0, which clears them.  Pages wait as codes, so four pages of bf16 do.
+//
 // Long contexts are cut into pieces of equal length (the rest last, so that the short ones fill the
 // gaps); their normalised fp32 partials are merged by a second kernel.
 // Every wait is bounded (2 s) and reports a timeout in the status word.
@@ -51,6 +61,16 @@
 // Few rows (16 heads, one node, 76 requests) stream 0.88 us a further page, 6.3 TB/s, 0.93 of the
 // measured copy rate.  One short request (512 rows, 16 heads) takes 12.1 us, of which one tile alone
 // (63 rows) is 8.4: it is set-up, the chain of one tile and the way out.
+// The 8-bit cache: 64 x 32768 rows, 128 heads, two nodes 1060 us (1.10 PFLOP/s, 0.57 of the measured rate; a bf16
+// cache of twice the bytes 856 on the same GPU); 8 x 8192, 16 heads, one node 25.8 us.  The conversion is as many
+// instructions again as all other warps execute (ncu: 40.3 to 19.3 million for 38 x 8192 rows of 128 heads), and the
+// tile's chain has four pages to hide in, not five.  What it spent its time on first was fetching instructions: with the conversion
+// unrolled (1880 us) 3.5 warps waited for one at each issue, the SM's instruction cache hit 82% and the next
+// level ran at 82% of its rate.  A short loop 1320, half a page's columns handed over early and two pages of
+// codes with four of bf16 1186, waits in fewer instructions 1108, one hand-over 1062.  Not taken: eight converting
+// warps with registers moved to the score warps 1400; the converting warps on the schedulers of the warps
+// that only ship scores 1280; idle score warps that convert where there are few rows, with a third page of
+// codes in flight, 140 instead of 132 us (64 x 8192, 16 heads).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
