@@ -332,7 +332,8 @@ irm_status irm_mla_attn_prefill_rope(const void* q_lat, const void* q_rope, int 
  *   position device int32 [n_tokens]
  *   rope     the model's frequencies and pairing (NULL: the default)
  *   factor   finite; the magnitude that some scaled tables bring along, else 1
- *   out      as x, of its own strides; x itself, or memory that does not overlap it
+ *   out      as x, of its own strides, which do not let rows meet (one steps over all rows of the
+ *            other); x itself, or memory that does not overlap it
  * n_tokens < 2^31, n_heads <= 65535.
  */
 irm_status irm_rope_apply(const void* x, int64_t x_token, int64_t x_head, int64_t n_tokens, int n_heads,
@@ -345,7 +346,8 @@ irm_status irm_rope_apply(const void* x, int64_t x_token, int64_t x_head, int64_
  *   kv[page_table[s, i / 64], i % 64] = [c_kv[t] | factor * R(p) k_rope[t]]
  *
  *   c_kv     device bf16, row t at t * c_stride (elements, a multiple of 8), 16-byte aligned;
- *   k_rope   the same, t * k_stride (both may be columns of one projection's output [T, 576])
+ *   k_rope   the same, t * k_stride (both may be columns of one projection's output [T, 576]; not
+ *            rows of kv that the call writes)
  *   kv       irm_pages_append: device bf16 [n_pages, 64, 576]
  *            irm_pages_append8: device bytes [n_pages, 64, 656], the 8-bit cache (below)
  *   page_table device int32 [n_slots, max_pages]
@@ -442,7 +444,8 @@ irm_status irm_mla_attn_tree8(const void* q_lat, const void* q_rope, int B, int 
  *   probs    device fp32, row t at t * probs_stride, or NULL (one of the two is needed); such a row's
  *            are zeros
  * Weights are held in units of 2^-43 of the largest and summed as integers, so that nothing depends on
- * the order of addition.  logits and probs must not overlap.  vocab at most 2^20, n_rows below 2^28.  Workspace: IRM_WORKSPACE_HEADER bytes (status word).
+ * the order of addition.  logits and probs must not overlap (columns of one buffer's rows may be both).
+ * vocab at most 2^20, n_rows below 2^28.  Workspace: IRM_WORKSPACE_HEADER bytes (status word).
  */
 #define IRM_FP32 0
 #define IRM_BF16 1

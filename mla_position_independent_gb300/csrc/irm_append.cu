@@ -283,7 +283,11 @@ irm_status irm_rope_apply(const void* x, int64_t x_token, int64_t x_head, int64_
   if (!x || !out || !position) return fail(IRM_ERR_INVALID_ARG, "null device pointer");
   if (!aligned(x, 16) || !aligned(out, 16) || (x_token | x_head | out_token | out_head) % 8 != 0)
     return fail(IRM_ERR_INVALID_ARG, "rows of x and out must start on 16 bytes");
-  if ((n_heads > 1 && out_head < kDRope) || (n_tokens > 1 && out_token < kDRope)) return fail(IRM_ERR_INVALID_ARG, "rows of out overlap");
+  // one of the strides steps over all of the other's rows
+  if ((n_heads > 1 && out_head < kDRope) || (n_tokens > 1 && out_token < kDRope) ||
+      (n_heads > 1 && n_tokens > 1 && (__int128)out_head * (n_heads - 1) + kDRope > out_token &&
+       (__int128)out_token * (n_tokens - 1) + kDRope > out_head))
+    return fail(IRM_ERR_INVALID_ARG, "rows of out overlap");
   if (!aligned(position, 4)) return fail(IRM_ERR_INVALID_ARG, "misaligned device pointer");
   if (!std::isfinite(factor)) return fail(IRM_ERR_INVALID_ARG, "factor must be finite");
   RopeArgs a{};

@@ -931,6 +931,17 @@ cudaError_t raise_smem_limit(Kernel k, int which) {
   return e;
 }
 
+// Whether rows of `a` bytes at p share a byte with rows of `b` bytes at q: not where their spans lie apart, nor where
+// both are columns of rows of the same stride.
+bool rows_overlap(const void* p, int64_t p_stride, int64_t a, const void* q, int64_t q_stride, int64_t b, int64_t rows) {
+  using wide = __int128;
+  const wide x = (wide)(uintptr_t)p, y = (wide)(uintptr_t)q;
+  if (x + (wide)p_stride * (rows - 1) + a <= y || y + (wide)q_stride * (rows - 1) + b <= x) return false;
+  if (rows == 1 || p_stride != q_stride) return true;
+  const wide d = ((y - x) % p_stride + p_stride) % p_stride;
+  return d < a || d + b > p_stride;
+}
+
 }  // namespace
 }  // namespace irm
 
@@ -955,6 +966,10 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < IRM_WORKSPACE_HEADER)
     return fail(IRM_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %d bytes", IRM_WORKSPACE_HEADER);
   if (n_rows == 0) return IRM_OK;
+  const int64_t each = half ? 2 : 4;
+  if (row_stride > INT64_MAX / 8 || probs_stride > INT64_MAX / 8) return fail(IRM_ERR_INVALID_ARG, "rows are too far apart");
+  if (probs != nullptr && rows_overlap(logits, row_stride * each, vocab * each, probs, probs_stride * 4, vocab * int64_t(4), n_rows))
+    return fail(IRM_ERR_INVALID_ARG, "logits and probs overlap");
   const int C = cluster_size(n_rows, vocab);
   SampleArgs a{};
   a.logits = logits;

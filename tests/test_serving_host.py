@@ -98,6 +98,22 @@ def test_sampling_of_nothing_is_no_launch(irm):
     assert irm.lib().irm_sample(None, 0, 100, 0, 100, None, None, None, None, None, FAKE, None, 0, WS, 256, None) == 0
 
 
+@pytest.mark.parametrize("off,type,ld,pld,T", [
+    (0, 0, 100, 100, 3), (0, 0, 100, 100, 1), (4 * 299, 0, 100, 100, 3), (-4, 0, 100, 100, 1), (4 * 100, 0, 100, 120, 3), (4 * 50, 0, 250, 250, 3),
+    (4 * 160, 0, 250, 250, 3), (-4 * 100, 0, 199, 199, 3), (2 * 98, 1, 400, 200, 3), (2 * 99, 1, 400, 200, 3), (2 * 2 * 150, 1, 402, 201, 3),
+])
+def test_probabilities_over_logits_are_refused(irm, off, type, ld, pld, T):
+    probs = ctypes.c_void_p(FAKE.value + off)
+    assert irm.lib().irm_sample(FAKE, type, ld, T, 100, None, None, None, None, FAKE, FAKE, probs, pld, WS, 256, None) == -1
+    assert (b"overlap" if off % 4 == 0 else b"misaligned") in irm.lib().irm_last_error()
+
+
+@pytest.mark.parametrize("T,H,ot,oh", [(4, 16, 960, 64), (4, 16, 64, 64), (4, 16, 64, 128), (4, 16, 192, 64), (4, 2, 96, 64), (2, 2, 64, 64)])
+def test_rotated_rows_that_meet_are_refused(irm, T, H, ot, oh):
+    assert irm.lib().irm_rope_apply(FAKE, 1024, 64, T, H, FAKE, None, 1.0, FAKE, ot, oh, None) == -1
+    assert b"overlap" in irm.lib().irm_last_error()
+
+
 def test_calls_over_the_8_bit_cache_refuse_as_the_others(irm):
     L, i32 = irm.lib(), lambda *x: np.array(x, np.int32)  # noqa: E731
     c, p = i32(100), i32(0, 3)
