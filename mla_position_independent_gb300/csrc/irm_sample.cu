@@ -39,6 +39,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "irm_common.cuh"
 #include "irm_host_util.h"
@@ -215,7 +216,9 @@ __device__ __noinline__ uint64_t weight_of(float l, float m, const Shared& sh) {
 
 template <bool BF16, bool RES>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
-  extern __shared__ __align__(16) float row_sh[];
+  extern __shared__ __align__(16) uint8_t row_bytes[];
+  using Held = typename std::conditional<BF16, uint16_t, float>::type;
+  Held* row_sh = reinterpret_cast<Held*>(row_bytes);  // the CTA's logits, in the type in which they came
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t C;
@@ -227,7 +230,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const __nv_bfloat16* b16 = static_cast<const __nv_bfloat16*>(a.logits) + b * a.ld + v0;
   cluster_arrive();  // waited for before the first store into a peer's shared memory
 
-  auto one = [&](int i) -> float { return RES ? row_sh[i] : clean(BF16 ? __bfloat162float(b16[i]) : f32[i]); };
+  auto one = [&](int i) -> float {
+    if (!RES) return clean(BF16 ? __bfloat162float(b16[i]) : f32[i]);
+    return BF16 ? __uint_as_float((uint32_t)row_sh[i] << 16) : (float)row_sh[i];
+  };
   // A warp looks at a contiguous part of the CTA's logits, a group (four neighbours a lane) at a time.
   const int wseg = (n_own + kWarps * kGroup - 1) / (kWarps * kGroup) * kGroup;
   const int w0 = min(n_own, warp * wseg), w1 = min(n_own, w0 + wseg);
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (n_cand >= 0) {
       for (int i = tid; i < n_cand; i += kThreads) {
         const int at = cand_at[i];
-        f(row_sh[at], v0 + at, [&] { return cand_w[i]; });
+        f(one(at), v0 + at, [&] { return cand_w[i]; });
       }
       return;
     }
@@ -307,6 +313,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     sh.ch = inv * 1.4426950408889634f;
   }
   // ---- the row, and its maximum ------------------------------------------------------------
+  auto hold = [&](int i, float x) {
+    if (BF16) reinterpret_cast<uint16_t*>(row_bytes)[i] = (uint16_t)(__float_as_uint(x) >> 16);
+    else reinterpret_cast<float*>(row_bytes)[i] = x;
+  };
   float best = -INFINITY;
   if (RES && a.vec_in) {
     constexpr int kAhead = 4;
@@ -327,20 +337,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         x[u] = make_float4(clean(x[u].x), clean(x[u].y), clean(x[u].z), clean(x[u].w));
-        *reinterpret_cast<float4*>(row_sh + min(i + u * kGroup, whole - 4)) = x[u];
+        Held* to = row_sh + min(i + u * kGroup, whole - 4);
+        if (BF16)
+          *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(__float_as_uint(x[u].x), __float_as_uint(x[u].y), 0x7632),
+                                                     __byte_perm(__float_as_uint(x[u].z), __float_as_uint(x[u].w), 0x7632));
+        else
+          *reinterpret_cast<float4*>(to) = x[u];
         best = fmaxf(best, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
       }
     }
     if (lane < w1 - whole) {
       const float x = clean(BF16 ? __bfloat162float(b16[whole + lane]) : f32[whole + lane]);
-      row_sh[whole + lane] = x;
+      hold(whole + lane, x);
       best = fmaxf(best, x);
     }
   } else {
 #pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
       const float x = clean(BF16 ? __bfloat162float(b16[i]) : f32[i]);
-      if (RES) row_sh[i] = x;
+      if (RES) hold(i, x);
       best = fmaxf(best, x);
     }
   }
@@ -509,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       at += __popc(mask);
     }
     __syncwarp();
-    for (uint32_t i = first + lane; i < at; i += 32) cand_w[i] = weight_of(row_sh[cand_at[i]], m, sh);
+    for (uint32_t i = first + lane; i < at; i += 32) cand_w[i] = weight_of(one(cand_at[i]), m, sh);
     n_cand = (int)all;
     __syncthreads();
   };
@@ -823,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (i >= n_left) return 0ull;
     if (listed) {
       const int at = cand_at[i];
-      return kept(row_sh[at], v0 + at) && cand_w[i] >= least ? cand_w[i] : 0ull;
+      return kept(one(at), v0 + at) && cand_w[i] >= least ? cand_w[i] : 0ull;
     }
     const float l = one(i);
     if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, v0 + i)) return 0ull;
@@ -850,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       __syncthreads();
       for (int i = tid; i < n_cand; i += kThreads) {
         const int at = cand_at[i];
-        const float l = row_sh[at];
+        const float l = one(at);
         if (kept(l, v0 + at) && cand_w[i] >= least) probs[at] = fast_exp2(octaves(l, m, half, ch)) * inv;
       }
     } else {
@@ -906,29 +921,72 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 using Kernel = void (*)(SampleArgs);
 
-// CTAs of a row: as many as let its parts stay in shared memory, with some candidates, with two CTAs on an SM
-// (16384 logits each), more where the batch leaves SMs empty.
-constexpr int kPart = 16384, kPartMost = 40960;
 constexpr size_t kSmemTwo = 233472 / 2 - 1024, kSmemOne = 232448;  // of a CTA, with another one on the SM and alone
-int cluster_size(int64_t rows, int V) {
-  int C = 1;
-  while (C < kMaxCluster && (int64_t)C * kPart < V) C *= 2;
-  while (C < kMaxCluster && rows * C * 2 <= 2 * 152 && V > C * 1024) C *= 2;
-  return C;
-}
+constexpr size_t kCand = sizeof(uint64_t) + sizeof(uint16_t);      // a candidate's bytes
+constexpr int kCandLeast = 512;  // candidates that a CTA has room for where two share an SM
 
-// A kernel's dynamic shared memory limit belongs to the device: raised once on each.
-cudaError_t raise_smem_limit(Kernel k, int which) {
+// What a device has room for at once, clusters of 1 to 8 CTAs with two CTAs on an SM and with one (clusters do
+// not cross the SM groups, so it is less than the SMs divided), and whether the kernels' limits are raised.
+struct Device {
+  bool ready;
+  int two[kMaxCluster + 1], one[kMaxCluster + 1];
+};
+Kernel kernel_of(bool half, bool resident) {
+  return resident ? (half ? sample_kernel<true, true> : sample_kernel<false, true>)
+                  : (half ? sample_kernel<true, false> : sample_kernel<false, false>);
+}
+cudaError_t device_of(Device& out) {
   static std::mutex mu;
-  static bool done[2][128];
+  static Device known[128];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
-  if (dev >= 0 && dev < 128 && done[which][dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemOne - sizeof(Shared)));
-  if (e == cudaSuccess && dev >= 0 && dev < 128) done[which][dev] = true;
-  return e;
+  const bool keep = dev >= 0 && dev < 128;
+  if (keep && known[dev].ready) {
+    out = known[dev];
+    return cudaSuccess;
+  }
+  for (const bool half : {false, true}) {
+    e = cudaFuncSetAttribute(kernel_of(half, true), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemOne - sizeof(Shared)));
+    if (e != cudaSuccess) return e;
+  }
+  for (int C = 1; C <= kMaxCluster; ++C) {
+    for (const bool two : {false, true}) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(C);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = (two ? kSmemTwo : kSmemOne) - sizeof(Shared);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {(unsigned)C, 1, 1};
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(two ? &out.two[C] : &out.one[C], kernel_of(true, true), &cfg);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  out.ready = true;
+  if (keep) known[dev] = out;
+  return cudaSuccess;
+}
+
+int part_of_row(int V, int C) { return ((V + C - 1) / C + 3) / 4 * 4; }
+
+// CTAs of a row.  Many rows: as few as let two CTAs share an SM (what a CTA does beside its part of the row
+// is the larger half: 384 rows of 102400 fp32 logits, top-p with probabilities, 304 us with 5, 383 with 8; bf16
+// 280 with 3, 287 with 4, 393 with 8).  Few rows: more, as long as all rows are worked on at once, with an SM for each
+// CTA (one row 27.6 us with 8, 31.5 with 5; 20 rows 35.9 with 6, 38.7 with 8, which share SMs) or else two on
+// one (44 rows 49.5 with 6, 65 with 8).
+int cluster_size(int64_t rows, int V, size_t bytes, const Device& dev) {
+  int least = 1;
+  while (least < kMaxCluster && part_of_row(V, least) * bytes + kCandLeast * kCand + sizeof(Shared) > kSmemTwo) ++least;
+  const int most = std::max(least, std::min(kMaxCluster, V / 1024));
+  for (int C = most; C >= std::max(least, 5); --C)
+    if (rows <= dev.one[C]) return C;
+  for (int C = most; C > least; --C)
+    if (rows <= dev.two[C]) return C;
+  return least;
 }
 
 // Whether rows of `a` bytes at p share a byte with rows of `b` bytes at q: not where their spans lie apart, nor where
@@ -970,12 +1028,15 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   if (row_stride > INT64_MAX / 8 || probs_stride > INT64_MAX / 8) return fail(IRM_ERR_INVALID_ARG, "rows are too far apart");
   if (probs != nullptr && rows_overlap(logits, row_stride * each, vocab * each, probs, probs_stride * 4, vocab * int64_t(4), n_rows))
     return fail(IRM_ERR_INVALID_ARG, "logits and probs overlap");
-  const int C = cluster_size(n_rows, vocab);
+  Device dev{};
+  cudaError_t e = device_of(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "sampling set-up");
+  const int C = cluster_size(n_rows, vocab, each, dev);
   SampleArgs a{};
   a.logits = logits;
   a.ld = row_stride;
   a.V = vocab;
-  a.seg = ((vocab + C - 1) / C + 3) / 4 * 4;
+  a.seg = part_of_row(vocab, C);
   a.temperature = temperature;
   a.top_k = top_k;
   a.top_p = top_p;
@@ -986,18 +1047,16 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   a.probs_ld = probs_stride;
   a.vec_in = row_stride % 4 == 0 && aligned(logits, half ? 8 : 16);
   a.vec_out = probs_stride % 4 == 0 && aligned(probs, 16);
-  const bool resident = a.seg <= kPartMost;
-  const Kernel kernel = resident ? (half ? sample_kernel<true, true> : sample_kernel<false, true>)
-                                 : (half ? sample_kernel<true, false> : sample_kernel<false, false>);
-  cudaError_t e = resident ? raise_smem_limit(kernel, half) : cudaSuccess;
-  if (e != cudaSuccess) return cuda_fail(e, "sampling set-up");
+  // in shared memory, where a place in the part has 16 bits
+  const size_t row = (size_t)a.seg * each;
+  const bool resident = a.seg <= 1 << 16 && row + kCandLeast * kCand + sizeof(Shared) <= kSmemOne;
+  const Kernel kernel = kernel_of(half, resident);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(n_rows * C));
   cfg.blockDim = dim3(kThreads);
   if (resident) {
-    const size_t row = (size_t)a.seg * sizeof(float), room = (a.seg <= kPart ? kSmemTwo : kSmemOne) - sizeof(Shared) - row;
-    constexpr size_t kCand = sizeof(uint64_t) + sizeof(uint16_t);
-    a.cap = (int)std::min<size_t>((size_t)a.seg, room / kCand);
+    const bool two = row + kCandLeast * kCand + sizeof(Shared) <= kSmemTwo;
+    a.cap = (int)std::min<size_t>((size_t)a.seg, ((two ? kSmemTwo : kSmemOne) - sizeof(Shared) - row) / kCand);
     cfg.dynamicSmemBytes = row + a.cap * kCand;
   }
   cfg.stream = stream;
