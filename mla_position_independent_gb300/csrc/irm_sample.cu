@@ -54,6 +54,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kBins = 1024;         // the last one holds what has no weight
 constexpr int kList = 448;          // elements that are ranked among themselves, a thread each (two CTAs' memory fits an SM)
+constexpr int kFew = 128;           // elements from which a row is finished at once (each is compared with each, twice)
 constexpr int kNear = 96;           // of which a top-p cut looks at that many around its guess (each is compared with each)
 constexpr int kGroup = 128;         // elements that a warp looks at at once
 constexpr int kGroups = kMaxVocab / kMaxCluster / kGroup;
@@ -255,6 +256,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
   };
 
+  // The same for the passes that most rows take: four neighbours a lane at a time.
+  auto each4 = [&](auto f) {
+    if (n_cand >= 0 || !RES) {
+      each(f);
+      return;
+    }
+    for (int i = w0 + 4 * lane; i < w1; i += kGroup) {
+      float x[4];
+      if (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(row_sh + i);
+        x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
+        x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
+      } else {
+        const float4 w = *reinterpret_cast<const float4*>(row_sh + i);
+        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < w1) f(x[e], v0 + i + e, [&] { return weight_of(x[e], sh.m, sh); });
+    }
+  };
+
   auto cluster_sync = [&] {
     __syncwarp();
     cluster_arrive();
@@ -422,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
   auto histogram = [&](int bin) -> uint2 {
     clear_bins();
-    each([&](float l, int idx, auto) {
+    each4([&](float l, int idx, auto) {
       const float t = octaves(l, m, half, ch);
       const int x = bin_of(t);
       if (x < kBins - 1 && (bin < 0 || x == bin) && kept(l, idx)) atomicAdd(&sh.u.hist[bin < 0 ? x : fine_of(t, bin)], 1u);
@@ -462,6 +485,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int w = 0; w < warp; ++w) v += sh.fscan[w];
     return v;
   };
+  // Up to bin `last`, which has everything with a weight where it is the last one of those: a comparison.
+  auto edge_of = [](int last) -> float { return last < kBins - 2 ? (float)(last + 1) : (float)(2 * kBins); };
+  auto before_edge = [&](float l, float edge) -> bool {
+    const float t = octaves(l, m, half, ch);
+    return t > -kOctaves && -t * kBinScale < edge;  // bin_of(t) <= last
+  };
   // The elements for which pick(t) holds (kList of the cluster at most): each CTA collects its own, and behind a
   // cluster barrier all read all.
   auto collect = [&](auto pick) {
@@ -475,6 +504,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (at < (uint32_t)kList) sh.own[at] = Item{l, idx, w()};
       }
     });
+  };
+  auto collect_to = [&](int last) {
+    __syncthreads();
+    if (tid == 0) sh.n_own = 0;
+    __syncthreads();
+    const float edge = edge_of(last);
+    each4([&](float l, int idx, auto w) {
+      if (before_edge(l, edge) && kept(l, idx)) {
+        const uint32_t at = atomicAdd(&sh.n_own, 1u);
+        if (at < (uint32_t)kList) sh.own[at] = Item{l, idx, w()};
+      }
+    });
+    cluster_sync();
   };
   auto read_all = [&] {
     uint32_t n[kMaxCluster], at = 0;
@@ -497,14 +539,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // the row stays what is looked at.
   auto list_candidates = [&](int last) {
     if (!RES || n_cand >= 0) return;
-    const float edge = (float)(last + 1);
-    auto in = [&](float l) -> bool {
-      const float t = octaves(l, m, half, ch);
-      return t > -kOctaves && -t * kBinScale < edge;  // bin_of(t) <= last
-    };
-    uint32_t n = 0;
+    const float edge = edge_of(last);
+    // which of 32 neighbours are: lane j keeps the mask of the warp's j-th 32, of the (32 + j)-th, ...
+    constexpr int kMasks = (1 << 16) / kWarps / 1024;
+    uint32_t masks[kMasks] = {}, n = 0;
+#pragma unroll
+    for (int c = 0; c < kMasks; ++c) {
+      const int to = min(w1, w0 + 1024 * (c + 1));
 #pragma unroll 4
-    for (int i = w0; i < w1; i += 32) n += __popc(__ballot_sync(kFull, i + lane < w1 && in(one(i + lane))));
+      for (int i = w0 + 1024 * c; i < to; i += 32) {
+        const uint32_t mask = __ballot_sync(kFull, i + lane < w1 && before_edge(one(i + lane), edge));
+        if (lane == ((i - w0) >> 5 & 31)) masks[c] = mask;
+      }
+      n += __popc(masks[c]);
+    }
+    n = __reduce_add_sync(kFull, n);
     __syncthreads();
     if (lane == 0) sh.scan[warp] = n;
     __syncthreads();
@@ -515,67 +564,72 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     if (all > (uint32_t)a.cap) return;
     const uint32_t first = at;
-#pragma unroll 4
-    for (int i = w0; i < w1; i += 32) {
-      const float l = i + lane < w1 ? one(i + lane) : -INFINITY;
-      const bool p = in(l);
-      const uint32_t mask = __ballot_sync(kFull, p);
-      if (p) cand_at[at + __popc(mask & ((1u << lane) - 1u))] = (uint16_t)(i + lane);
-      at += __popc(mask);
+#pragma unroll
+    for (int c = 0; c < kMasks; ++c) {
+      uint32_t mask = masks[c], incl = __popc(mask);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+      }
+      for (uint32_t to = at + incl - __popc(mask); mask != 0; mask &= mask - 1) cand_at[to++] = (uint16_t)(w0 + 1024 * c + 32 * lane + __ffs(mask) - 1);
+      at += __shfl_sync(kFull, incl, 31);
     }
     __syncwarp();
     for (uint32_t i = first + lane; i < at; i += 32) cand_w[i] = weight_of(one(cand_at[i]), m, sh);
     n_cand = (int)all;
     __syncthreads();
   };
-  // Rank of the thread's element among the list's first n, and the weight before it.
-  auto rank_in_list = [&](int n, uint64_t& w_before) -> int {
-    int r = 0;
-    w_before = 0;
-    if (tid < n) {
-      const Item me = sh.list[tid];
+  // Everything that may be kept is in the list (kFew at most): the rest of the work is four lanes an element.  Of
+  // the list's order the first k stay; top-p of `total` (0: of what stays).
+  auto finish_list = [&](int n, int k, uint64_t total) {
+    constexpr int lanes = kThreads / kFew;
+    const int me_at = tid / lanes, part = tid % lanes;
+    const bool in = me_at < n;
+    const Item me = sh.list[in ? me_at : 0];
+    auto of_lanes = [&](uint64_t x) -> uint64_t {
+#pragma unroll
+      for (int o = 1; o < lanes; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+      return x;
+    };
+    // its rank, and the weight before it
+    uint32_t r = 0;
+    uint64_t wb = 0;
 #pragma unroll 2
-      for (int j = 0; j < n; ++j) {
-        const Item x = sh.list[j];
-        if (x.l > me.l || (x.l == me.l && x.idx < me.idx)) {
-          ++r;
-          w_before += x.w;
-        }
+    for (int j = in ? part : n; j < n; j += lanes) {
+      const Item x = sh.list[j];
+      if (x.l > me.l || (x.l == me.l && x.idx < me.idx)) {
+        ++r;
+        wb += x.w;
       }
     }
-    return r;
-  };
-
-  // Everything that may be kept is in the list: the rest of the work is a thread an element.  Of the list's
-  // order the first k stay; top-p of `total` (0: of what stays).
-  auto finish_list = [&](int n, int k, uint64_t total) {
-    uint64_t wb;
-    const int r = rank_in_list(n, wb);
-    const Item me = sh.list[tid < n ? tid : 0];
-    if (tid < n && r == min(k, n) - 1) sh.sum = wb + me.w;
+    wb = of_lanes(wb);
+    r = (uint32_t)of_lanes(r);
+    if (in && (int)r == min(k, n) - 1) sh.sum = wb + me.w;  // all lanes of the one element
     __syncthreads();
     if (total == 0) total = sh.sum;
     const uint64_t target = top_p < 1.f ? part_of_sum(top_p, total, true) : ~0ull;
     const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
-    const bool stay = tid < n && r < k && (r == 0 || (wb < target && me.w >= least));
+    const bool stay = in && (int)r < k && (r == 0 || (wb < target && me.w >= least));
     uint64_t s = stay ? wb + me.w : 0ull;  // the last that stays has them all
     s = warp_max64(s);
-    __syncthreads();
     if (lane == 0) sh.part[warp][0] = s;
-    if (tid < n && !stay) sh.list[tid].w = 0;
+    if (in && !stay) sh.list[me_at].w = 0;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) s = sh.part[w][0] > s ? sh.part[w][0] : s;
     if (probs != nullptr) {
       zero_probs();
       __syncthreads();
-      if (stay && me.idx >= v0 && me.idx < v0 + n_own) probs[me.idx - v0] = fast_exp2(octaves(me.l, m, half, ch)) * ((float)kOne / (float)s);
+      if (stay && part == 0 && me.idx >= v0 && me.idx < v0 + n_own)
+        probs[me.idx - v0] = fast_exp2(octaves(me.l, m, half, ch)) * ((float)kOne / (float)s);
     }
     if (a.token != nullptr && rank == 0) {
       uint64_t at = part_of_sum(rf, s, false);
       if (at >= s) at = s - 1;
       uint64_t x = 0;
-      if (stay)
-        for (int j = 0; j < n; ++j) x += sh.list[j].idx < me.idx ? sh.list[j].w : 0ull;
+#pragma unroll 2
+      for (int j = stay ? part : n; j < n; j += lanes) x += sh.list[j].idx < me.idx ? sh.list[j].w : 0ull;
+      x = of_lanes(x);
       if (stay && at >= x && at < x + me.w) a.token[b] = me.idx;
     }
     cluster_arrive();
@@ -654,8 +708,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (bin < 0) {
       cluster_sync();  // the counts have been read
     } else {
-      if (above + count <= (uint32_t)kList) {
-        gather([&](float t) { return bin_of(t) <= bin; });
+      if (above + count <= (uint32_t)kFew) {
+        collect_to(bin);
+        read_all();
         finish_list((int)(above + count), (int)k, 0);
         return;
       }
@@ -732,8 +787,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         tell_upto(guess);
         __syncthreads();
         const uint32_t n = sh.bin_above;
-        if (n <= (uint32_t)kList) {
-          gather([&](float t) { return bin_of(t) <= last; });
+        if (n <= (uint32_t)kFew) {
+          collect_to(last);
+          read_all();
           uint64_t s = tid < (int)n ? sh.list[tid].w : 0ull;
           s = warp_sum64(s);
           if (lane == 0) sh.part[warp][0] = s;
