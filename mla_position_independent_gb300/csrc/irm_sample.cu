@@ -53,11 +53,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kBins = 1024;         // the last one holds what has no weight
-constexpr int kList = 448;          // elements that are ranked among themselves, a thread each (two CTAs' memory fits an SM)
+constexpr int kList = 256;          // elements that are ranked among themselves, a thread each (two CTAs' memory fits an SM)
 constexpr int kFew = 128;           // elements from which a row is finished at once (each is compared with each, twice)
 constexpr int kNear = 96;           // of which a top-p cut looks at that many around its guess (each is compared with each)
 constexpr int kGroup = 128;         // elements that a warp looks at at once
-constexpr int kGroups = kMaxVocab / kMaxCluster / kGroup;
+constexpr int kGroups = 512;        // sums of a CTA's logits that are kept, of 128 each (in rows that do not stay in shared memory 256)
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kOctaves = 43.9f;   // below 2^-43.9 a weight rounds to nothing
 constexpr float kBinScale = (kBins - 1) / kOctaves;
@@ -68,7 +68,7 @@ struct SampleArgs {
   const void* logits;
   int64_t ld;
   int V, seg;    // logits of a row, and of a CTA's part of it (a multiple of 4)
-  int cap;       // candidates that a CTA can hold in shared memory, with their weights
+  int cap, cap_bare;  // candidates that a CTA can hold in shared memory with their weights, and without
   const float *temperature, *top_p, *min_p, *uniforms;
   const int32_t* top_k;
   int32_t* token;
@@ -240,22 +240,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int w0 = min(n_own, warp * wseg), w1 = min(n_own, w0 + wseg);
   // f(logit, index, weight()) for the CTA's logits, or for the candidates once they are listed (in index order)
   uint64_t* cand_w = reinterpret_cast<uint64_t*>(row_sh + (RES ? a.seg : 0));  // their weights, and where in the row they are
-  uint16_t* cand_at = reinterpret_cast<uint16_t*>(cand_w + a.cap);
+  uint16_t* cand_at = reinterpret_cast<uint16_t*>(cand_w + a.cap);  // (too many for the weights: in their place)
   int n_cand = -1;
+  bool weighed = true;
   auto each = [&](auto f) {
-    if (n_cand >= 0) {
+    if (n_cand >= 0 && weighed) {
       for (int i = tid; i < n_cand; i += kThreads) {
         const int at = cand_at[i];
         f(one(at), v0 + at, [&] { return cand_w[i]; });
       }
       return;
     }
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const float l = one(i);
-      f(l, v0 + i, [&] { return weight_of(l, sh.m, sh); });
+    const bool bare = n_cand >= 0;
+    for (int i = bare ? tid : w0 + lane; i < (bare ? n_cand : w1); i += bare ? kThreads : 32) {
+      const int at = bare ? cand_at[i] : i;
+      const float l = one(at);
+      f(l, v0 + at, [&] { return weight_of(l, sh.m, sh); });
     }
   };
-
   // The same for the passes that most rows take: four neighbours a lane at a time.
   auto each4 = [&](auto f) {
     if (n_cand >= 0 || !RES) {
@@ -536,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     read_all();
   };
   // Lists the CTA's candidates, those up to bin `last`, in index order with their weights; where they are too many
-  // the row stays what is looked at.
+  // without them (64 rows with some flat distributions 150 us when those went on with the whole row, 83 so), and where
+  // they are too many for that as well the row stays what is looked at.
   auto list_candidates = [&](int last) {
     if (!RES || n_cand >= 0) return;
     const float edge = edge_of(last);
@@ -562,7 +565,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (w < warp) at += sh.scan[w];
       all += sh.scan[w];
     }
-    if (all > (uint32_t)a.cap) return;
+    if (all > (uint32_t)a.cap_bare) return;
+    weighed = all <= (uint32_t)a.cap;
+    if (!weighed) cand_at = reinterpret_cast<uint16_t*>(cand_w);
     const uint32_t first = at;
 #pragma unroll
     for (int c = 0; c < kMasks; ++c) {
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       at += __shfl_sync(kFull, incl, 31);
     }
     __syncwarp();
-    for (uint32_t i = first + lane; i < at; i += 32) cand_w[i] = weight_of(one(cand_at[i]), m, sh);
+    for (uint32_t i = weighed ? first + lane : at; i < at; i += 32) cand_w[i] = weight_of(one(cand_at[i]), m, sh);
     n_cand = (int)all;
     __syncthreads();
   };
@@ -671,28 +676,66 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       cut_in_list(weights, target, above, count);
       return;
     }
-    // Too many alike: bit by bit, the largest key from which on the values reach the target, then the index.
-    auto reach = [&](auto pick) -> uint64_t {
+    // Too many: the largest key from which on the values reach the target, bit by bit where the bin's keys differ (few,
+    // or none).
+    auto in_bin = [&](float l, int idx) -> bool {
+      const float t = octaves(l, m, half, ch);
+      return t > -kOctaves && inside(t) && kept(l, idx);
+    };
+    auto reach = [&](uint32_t from) -> uint64_t {
       uint64_t s[1] = {0};
       each([&](float l, int idx, auto w) {
-        const float t = octaves(l, m, half, ch);
-        if (t > -kOctaves && inside(t) && kept(l, idx) && pick(order_key(l), idx)) s[0] += weights ? w() : 1ull;
+        if (in_bin(l, idx) && order_key(l) >= from) s[0] += weights ? w() : 1ull;
       });
       cluster_sum(s);
       return above + s[0];
     };
-    uint32_t key = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t want = key | 1u << bit;
-      if (reach([&](uint32_t k, int) { return k >= want; }) >= target) key = want;
+    uint64_t ends[2] = {0, 0};
+    each([&](float l, int idx, auto) {
+      if (!in_bin(l, idx)) return;
+      ends[0] = max(ends[0], (unsigned long)order_key(l));
+      ends[1] = max(ends[1], (unsigned long)~order_key(l));
+    });
+    cluster_sum(ends, true);
+    uint32_t key = (uint32_t)ends[0];
+    int bits = 32 - __clz(key ^ ~(uint32_t)ends[1]);
+    for (int bit = bits - 1; bit >= 0; --bit) key &= ~(1u << bit);
+    const bool differ = bits > 0;
+    while (--bits >= 0) {
+      const uint32_t want = key | 1u << bits;
+      if (reach(want) >= target) key = want;
     }
-    int idx = -1;  // the largest index up to which the target is not reached
-    for (int bit = 20; bit >= 0; --bit) {
-      const int want = idx + (1 << bit);
-      if (want < a.V && reach([&](uint32_t k, int i) { return k > key || (k == key && i <= want); }) < target) idx = want;
+    // of those with this key the first in index order that reach it: a count
+    const uint64_t base = differ ? reach(key + 1) : above;
+    const uint64_t each_has = weights ? weight_of(key_logit(key), m, sh) : 1ull, nth = (target - base + each_has - 1) / each_has;
+    const int items = n_cand >= 0 ? n_cand : n_own, part = (items + kThreads - 1) / kThreads * 32;
+    const int i0 = min(items, warp * part), i1 = min(items, i0 + part);
+    auto index_of = [&](int i) -> int {  // of an item that is one of them; else -1
+      if (i >= i1) return -1;
+      const int at = n_cand >= 0 ? cand_at[i] : i;
+      const float l = one(at);
+      return order_key(l) == key && kept(l, v0 + at) ? v0 + at : -1;
+    };
+    uint32_t mine = 0;
+    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(kFull, index_of(i + lane) >= 0));
+    __syncthreads();
+    if (lane == 0) sh.scan[warp] = mine;
+    uint64_t c[1] = {lane == 0 ? mine : 0u};
+    cluster_sum(c);
+    uint64_t run = before;
+    for (int w = 0; w < warp; ++w) run += sh.scan[w];
+    uint64_t found[1] = {0};
+    if (nth > run && nth <= run + mine) {
+      for (int i = i0; i < i1; i += 32) {
+        const int idx = index_of(i + lane);
+        const uint32_t mask = __ballot_sync(kFull, idx >= 0);
+        if (idx >= 0 && run + __popc(mask & ((1u << lane) - 1u)) + 1 == nth) found[0] = (uint64_t)idx;
+        run += __popc(mask);
+      }
     }
+    cluster_sum(found);
     cut_l = key_logit(key);
-    cut_idx = idx + 1;
+    cut_idx = (int)found[0];
   };
   // ---- top-k ------------------------------------------------------------------------------
   if (top_k > 0 && top_k < a.V) {
@@ -888,16 +931,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the sum of what is left, by groups of a warp's elements ------------------------------------
   const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
   const bool listed = n_cand >= 0;
-  const int n_left = listed ? n_cand : n_own, groups = (n_left + kGroup - 1) / kGroup;
+  constexpr int kSummed = RES ? kGroup : 2 * kGroup;
+  static_assert(kGroups * kSummed >= (RES ? 1 << 16 : kMaxVocab / kMaxCluster), "a sum for every group");
+  const int n_left = listed ? n_cand : n_own, groups = (n_left + kSummed - 1) / kSummed;
   // the weight left of element i of what is looked at (behind its end: none)
   auto left = [&](int i, auto weigh) -> uint64_t {
     if (i >= n_left) return 0ull;
-    if (listed) {
-      const int at = cand_at[i];
-      return kept(one(at), v0 + at) && cand_w[i] >= least ? cand_w[i] : 0ull;
-    }
-    const float l = one(i);
-    if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, v0 + i)) return 0ull;
+    const int at = listed ? cand_at[i] : i;
+    const float l = one(at);
+    if (listed && weighed) return kept(l, v0 + at) && cand_w[i] >= least ? cand_w[i] : 0ull;
+    if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, v0 + at)) return 0ull;
     const uint64_t w = weigh(l);
     return w >= least ? w : 0ull;
   };
@@ -907,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   for (int g = warp; g < groups; g += kWarps) {
     uint64_t w = 0;
 #pragma unroll 2
-    for (int e = 0; e < kGroup; e += 32) w += left(g * kGroup + e + lane, [&](float l) -> uint64_t { return weight(l, m, sh); });
+    for (int e = 0; e < kSummed; e += 32) w += left(g * kSummed + e + lane, [&](float l) -> uint64_t { return weight(l, m, sh); });
     s[0] += w;
     w = __any_sync(kFull, w != 0) ? warp_sum64(w) : 0ull;
     if (lane == 0) sh.u.gsum[g] = w;
@@ -922,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int i = tid; i < n_cand; i += kThreads) {
         const int at = cand_at[i];
         const float l = one(at);
-        if (kept(l, v0 + at) && cand_w[i] >= least) probs[at] = fast_exp2(octaves(l, m, half, ch)) * inv;
+        if (kept(l, v0 + at) && (least == 0 || left(i, called) != 0)) probs[at] = fast_exp2(octaves(l, m, half, ch)) * inv;
       }
     } else {
       // min-p in octaves: what is right at it goes by the weight itself
@@ -961,8 +1004,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (!scan(w, incl)) continue;
       const int src = __ffs((int)__ballot_sync(kFull, at >= run + incl - w && at < run + incl)) - 1;
       run += __shfl_sync(kFull, incl - w, src);
-      for (int e = 0; e < kGroup; e += 32) {
-        const int i = (g0 + src) * kGroup + e + lane;
+      for (int e = 0; e < kSummed; e += 32) {
+        const int i = (g0 + src) * kSummed + e + lane;
         const uint64_t x = left(i, called);
         if (!scan(x, incl)) continue;
         if (at >= run + incl - x && at < run + incl) a.token[b] = v0 + (listed ? (int)cand_at[i] : i);
@@ -1030,19 +1073,22 @@ cudaError_t device_of(Device& out) {
 int part_of_row(int V, int C) { return ((V + C - 1) / C + 3) / 4 * 4; }
 
 // CTAs of a row.  Many rows: as few as let two CTAs share an SM (what a CTA does beside its part of the row
-// is the larger half: 384 rows of 102400 fp32 logits, top-p with probabilities, 304 us with 5, 383 with 8; bf16
-// 280 with 3, 287 with 4, 393 with 8).  Few rows: more, as long as all rows are worked on at once, with an SM for each
-// CTA (one row 27.6 us with 8, 31.5 with 5; 20 rows 35.9 with 6, 38.7 with 8, which share SMs) or else two on
-// one (44 rows 49.5 with 6, 65 with 8).
+// is the larger half: 384 rows of 102400 fp32 logits, top-p with probabilities, 302 us with 5, 387 with 8; bf16
+// 259 with 3, 272 with 4, 380 with 8).  Few rows: more, as long as each CTA has an SM (one row 27.6 us with
+// 8, 31.5 with 5; 20 rows 35.9 with 6, 38.7 with 8, which share SMs); then as many as do not make the batch
+// take another turn (44 rows 49.5 with 6, 65 with 8; 64 rows, two turns either way, 57 with 8 and 83 with 5 where a few
+// of the rows have flat distributions, which take longest, 79 and 73 where all are alike).
 int cluster_size(int64_t rows, int V, size_t bytes, const Device& dev) {
   int least = 1;
   while (least < kMaxCluster && part_of_row(V, least) * bytes + kCandLeast * kCand + sizeof(Shared) > kSmemTwo) ++least;
   const int most = std::max(least, std::min(kMaxCluster, V / 1024));
   for (int C = most; C >= std::max(least, 5); --C)
     if (rows <= dev.one[C]) return C;
-  for (int C = most; C > least; --C)
-    if (rows <= dev.two[C]) return C;
-  return least;
+  auto turns = [&](int C) -> int64_t { return (rows + dev.two[C] - 1) / std::max(1, dev.two[C]); };
+  int best = most;
+  for (int C = most; C >= least; --C)
+    if (turns(C) < turns(best)) best = C;
+  return best;
 }
 
 // Whether rows of `a` bytes at p share a byte with rows of `b` bytes at q: not where their spans lie apart, nor where
@@ -1112,7 +1158,9 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   cfg.blockDim = dim3(kThreads);
   if (resident) {
     const bool two = row + kCandLeast * kCand + sizeof(Shared) <= kSmemTwo;
-    a.cap = (int)std::min<size_t>((size_t)a.seg, ((two ? kSmemTwo : kSmemOne) - sizeof(Shared) - row) / kCand);
+    const size_t room = (two ? kSmemTwo : kSmemOne) - sizeof(Shared) - row;
+    a.cap = (int)std::min<size_t>((size_t)a.seg, room / kCand);
+    a.cap_bare = (int)std::min<size_t>((size_t)a.seg, a.cap * kCand / sizeof(uint16_t));
     cfg.dynamicSmemBytes = row + a.cap * kCand;
   }
   cfg.stream = stream;

@@ -222,3 +222,14 @@ def test_drawn_tokens_follow_the_probabilities():
     token, probs, _ = irm.irm_sample(l.expand(n, V).contiguous(), f32(r), top_k=i32(np.full(n, 20)), probs=probs)
     got = np.bincount(token.cpu().numpy(), minlength=V)
     assert (np.abs(got - n * probs[0].double().cpu().numpy()) <= 1.1).all()
+
+
+@pytest.mark.parametrize("V,std", [(600000, 3.0), (102400, 0.3), (400000, 0.02), (30000, 0.01)])
+@pytest.mark.parametrize("s", [dict(p=0.95), dict(p=0.5), dict(k=1000), dict(k=20000, p=0.9)])
+def test_many_equal_logits_at_the_cut(V, std, s):
+    """bf16 logits, of which hundreds to thousands share a value; and beside them fp32 ones a few steps apart."""
+    l, r = normal(3, V, seed=V, std=std, dtype=torch.bfloat16)
+    full = {k: np.full(3, v) for k, v in s.items()}
+    check(l, r, **full)
+    near = (1.0 + torch.randint(0, 3, l.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) * 2.0 ** -20).float()
+    check(near, r, **full)
