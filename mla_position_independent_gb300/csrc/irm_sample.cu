@@ -801,8 +801,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     bool done = false;
     for (int level = 0; level < 2; ++level) {
       const uint2 h = level == 0 ? cluster_bins() : histogram(bin);
-      // the guess: counts times the weight at the bin's middle (inside one bin: of the bin)
-      const float mid = fast_exp2(-((float)(level ? bin : 2 * tid) + 0.5f) / kBinScale), mid1 = level ? mid : mid * fast_exp2(-1.f / kBinScale);
+      // the guess: counts times the weight at the bin's middle
+      const float width = level ? 1.f / kBins : 1.f, mid = fast_exp2(-((level ? (float)bin : 0.f) + (2.f * tid + 0.5f) * width) / kBinScale);
+      const float mid1 = mid * fast_exp2(-width / kBinScale);
       const float mass0 = mid * (float)h.x, mass1 = mid1 * (float)h.y;
       const float incl = scan_f32(mass0 + mass1);
       if (tid == kThreads - 1) sh.mass = incl;
@@ -888,35 +889,48 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       };
       uint64_t base = 0;
       for (int guard = 0; guard < kBins; ++guard) {
+        // the bins next to it that have something: equal logits leave most of them empty
+        __syncthreads();
+        if (tid == 0) {
+          sh.bin = -1;
+          sh.bin_count = kBins;
+        }
+        __syncthreads();
+        if (h.x != 0 && 2 * tid < guess) atomicMax(&sh.bin, 2 * tid);
+        if (h.y != 0 && 2 * tid + 1 < guess) atomicMax(&sh.bin, 2 * tid + 1);
+        if (h.x != 0 && 2 * tid > guess) atomicMin(&sh.bin_count, 2u * tid);
+        if (h.y != 0 && 2 * tid + 1 > guess) atomicMin(&sh.bin_count, 2u * tid + 1u);
+        __syncthreads();
+        const int prev = sh.bin, next = (int)sh.bin_count;
         uint64_t s[4] = {0, 0, 0, 0};
         each([&](float l, int idx, auto w) {
           const float t = octaves(l, m, half, ch);
           const int x = t > -kOctaves ? part_of(t) : kBins;
-          if (x <= guess + 1 && x < kBins && kept(l, idx)) {
+          if (x <= next && x < kBins && kept(l, idx)) {
             const uint64_t y = w();
-            if (x < guess - 1) s[0] += y;
-            else if (x == guess - 1) s[1] += y;
+            if (x < prev) s[0] += y;
+            else if (x == prev) s[1] += y;
             else if (x == guess) s[2] += y;
-            else s[3] += y;
+            else s[x < guess ? 0 : 3] += y;
           }
         });
         cluster_sum(s);
         if (target <= s[0]) {
-          guess -= 2;
+          guess = prev;
         } else if (target <= s[0] + s[1]) {
-          guess -= 1;
+          guess = prev;
           base = s[0];
           break;
         } else if (target <= s[0] + s[1] + s[2]) {
           base = s[0] + s[1];
           break;
         } else if (target <= s[0] + s[1] + s[2] + s[3]) {
-          guess += 1;
+          guess = next;
           base = s[0] + s[1] + s[2];
           break;
-        } else {  // the candidates may end before it: the row has them all
-          guess += 2;
-          n_cand = -1;
+        } else {
+          guess = next;
+          if (level == 0) n_cand = -1;  // the candidates may end before it: the row has them all
         }
       }
       above = base;
@@ -1075,20 +1089,19 @@ int part_of_row(int V, int C) { return ((V + C - 1) / C + 3) / 4 * 4; }
 // CTAs of a row.  Many rows: as few as let two CTAs share an SM (what a CTA does beside its part of the row
 // is the larger half: 384 rows of 102400 fp32 logits, top-p with probabilities, 302 us with 5, 387 with 8; bf16
 // 259 with 3, 272 with 4, 380 with 8).  Few rows: more, as long as each CTA has an SM (one row 27.6 us with
-// 8, 31.5 with 5; 20 rows 35.9 with 6, 38.7 with 8, which share SMs); then as many as do not make the batch
-// take another turn (44 rows 49.5 with 6, 65 with 8; 64 rows, two turns either way, 57 with 8 and 83 with 5 where a few
-// of the rows have flat distributions, which take longest, 79 and 73 where all are alike).
+// 8, 31.5 with 5; 20 rows 35.9 with 6, 38.7 with 8, which share SMs); then as many as let the batch be worked on at
+// once (44 rows 49 with 6, 63 with 8), or 8 if fewer do not save a turn (64 rows 58 with 8 and 84 with 5 where some of
+// the rows have flat distributions, which take longest, 79 and 74 where all are alike; 128 rows 92 and 75, 141 and 115).
 int cluster_size(int64_t rows, int V, size_t bytes, const Device& dev) {
   int least = 1;
   while (least < kMaxCluster && part_of_row(V, least) * bytes + kCandLeast * kCand + sizeof(Shared) > kSmemTwo) ++least;
   const int most = std::max(least, std::min(kMaxCluster, V / 1024));
   for (int C = most; C >= std::max(least, 5); --C)
     if (rows <= dev.one[C]) return C;
+  for (int C = most; C > least; --C)
+    if (rows <= dev.two[C]) return C;
   auto turns = [&](int C) -> int64_t { return (rows + dev.two[C] - 1) / std::max(1, dev.two[C]); };
-  int best = most;
-  for (int C = most; C >= least; --C)
-    if (turns(C) < turns(best)) best = C;
-  return best;
+  return turns(most) <= turns(least) ? most : least;
 }
 
 // Whether rows of `a` bytes at p share a byte with rows of `b` bytes at q: not where their spans lie apart, nor where
