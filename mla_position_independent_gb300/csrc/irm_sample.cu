@@ -7,12 +7,12 @@
 //   cumsum(w)(v) > r sum(w) in index order over what is left.
 // What is kept is a run of the order from its start, so it is described by its last element, a cut
 // (logit, index), and no row is sorted: a histogram of the logits' distance from the maximum (1023 bins, 23
-// an octave of w) finds the bin that holds the cut.  Up to 448 elements that may be kept are ranked among
-// themselves and finished at once.  Else the candidates up to a few bins behind the cut are listed with their
-// weights (where they fit shared memory), the elements of the bins around the guess ranked (a
-// top-p cut: the histogram with each bin's middle weight only guesses, the exact sum before them decides;
-// a wrong guess moves on), and the draw is an inverse of the sums of 128-element groups, then of one group.  More
-// equal logits than can be ranked: bit by bit on the logit, then on the index.
+// an octave of w) finds the bin that holds the cut.  Up to 128 elements that may be kept are ranked among
+// themselves and the row finished from them.  Else the candidates, up to a few bins behind the cut, are listed
+// where shared memory holds them, and the cut's bin (top-p: some 96 elements around a guess from the histogram
+// and each bin's middle weight, which the exact sum before them confirms or moves) is ranked, after a
+// second histogram inside the bin if it has more than 256; the draw is an inverse of the sums of 128 elements each, then
+// of one group.  More than 256 in a bin's 1024th part are mostly equal logits, of which a count finds the last.
 //
 // Arithmetic.  Which token comes out must not depend on the split or the order of addition, and a flat
 // row of 100k entries has cumulative sums 1e-5 apart, so weights are integers in units of 2^-43 and
@@ -22,18 +22,21 @@
 // 70 instructions.  fp64 runs at 1 / 64 of the fp32 rate on this GPU.  Thresholds (p of a sum, r of a sum) are
 // exact products of 24 and 64 bits.  Probabilities are fp32 exponentials over the exact sum.
 //
-// A cluster of CTAs shares a row, which stays in shared memory as fp32 from its one read where it fits (40960
-// logits a CTA); longer rows are read again by each pass.
+// A cluster of 1 to 8 CTAs shares a row, which stays in shared memory from its one read, in the type in which it
+// came, where a CTA's part fits (53376 logits of fp32, 65536 of bf16); longer rows are read again by each pass.
 //
-// What bounds it.  One row: latency, 17.2 us for 102400 logits with top-k 50 and top-p 0.9 (the row and its
-// maximum 2.6 us, the histogram and its exchange 4.1, collecting the candidates 3.2, reading the other CTAs' 2.4,
-// ranking 3.3).  Many rows with top-p alone: instructions, 384 rows with probabilities 390 us (35 by their
-// bytes), 0.61 instructions a clock and scheduler.  A quarter of that are the weights of all elements, whose
-// sum a top-p cut needs; a first sum of fp32 exponentials with a bound on its error takes a third of that
-// pass, but the rows near whose target an element lies (a tenth and more, all of a flat distribution) need the exact
-// one as well: 440 us instead of 409, not kept.  Steps that were: a pass over all elements, and one over those
-// near the cut, for each sum 635; the candidates listed with their weights 475; one element a lane and ranks by
-// four lanes an element 409; fewer neighbours and shorter lists 390.
+// What bounds it.  One row: latency, 15 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
+// maximum take 2.6, the histogram and its exchange 4, the list and its exchange 4, the ranks 3.  Many rows:
+// instructions, 384 bf16 rows with top-p and probabilities 260 us (35 by their bytes) at 0.67 instructions a clock
+// and scheduler, two CTAs of 512 threads on an SM; a third of them are the weights of all elements, whose
+// sum a top-p cut needs, a fifth the list of candidates, the rest what a CTA does whatever its part's length
+// (scans, exchanges, ranks), which is why few CTAs a row are best.  Steps that were, for these 384 rows: a pass
+// over all elements, and one over those near the cut, for each sum 635; the candidates listed with their weights
+// 475; one element a lane, ranks by four lanes an element 409; fewer neighbours and shorter lists 390; bf16 rows held as
+// bf16 by clusters of 4 instead of 8 285, of 3 279; four logits a lane and lists by masks 270, rows finished from
+// lists of 128 instead of 448 elements 259.  Not taken: a first sum of fp32 exponentials with a bound on its error
+// (a third of the exact one's time, but the rows near whose target an element lies, a tenth and more, need that as
+// well: 440 instead of 409); lists sorted by a bitonic network instead of ranked (270 instead of 259).
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>
@@ -53,9 +56,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kBins = 1024;         // the last one holds what has no weight
-constexpr int kList = 256;          // elements that are ranked among themselves, a thread each (two CTAs' memory fits an SM)
+constexpr int kList = 256;          // elements that are ranked among themselves
 constexpr int kFew = 128;           // elements from which a row is finished at once (each is compared with each, twice)
-constexpr int kNear = 96;           // of which a top-p cut looks at that many around its guess (each is compared with each)
+constexpr int kNear = 96;           // elements around its guess that a top-p cut ranks at once
 constexpr int kGroup = 128;         // elements that a warp looks at at once
 constexpr int kGroups = 512;        // sums of a CTA's logits that are kept, of 128 each (in rows that do not stay in shared memory 256)
 constexpr uint32_t kFull = 0xffffffffu;
