@@ -20,7 +20,8 @@
 // draw in a hundred came out wrong; here a weight is good to 2^-37 of the largest: the distance from the
 // maximum and its product with 1 / T in two fp32 parts, 32 table values and a polynomial of degree 5, some
 // 70 instructions.  fp64 runs at 1 / 64 of the fp32 rate on this GPU.  Thresholds (p of a sum, r of a sum) are
-// exact products of 24 and 64 bits.  Probabilities are fp32 exponentials over the exact sum.
+// exact products of 24 and 64 bits.  Probabilities are fp32 exponentials (2^-21) over the exact
+// sum.
 //
 // A cluster of 1 to 8 CTAs shares a row, which stays in shared memory from its one read, in the type in which it
 // came, where a CTA's part fits (53376 logits of fp32, 65536 of bf16); longer rows are read again by each pass.
@@ -217,6 +218,21 @@ __device__ __forceinline__ uint64_t weight(float l, float m, const Shared& sh) {
 
 // The same, called: where few elements need it, so that the code of a row's one pass stays in the instruction caches.
 __device__ __noinline__ uint64_t weight_of(float l, float m, const Shared& sh) { return weight(l, m, sh); }
+
+// exp((l - m) / T) in fp32, to 2^-21 of itself: the exponent in two parts, since 44 octaves times a rounding or two of
+// it would be 2^-17.
+__device__ __forceinline__ float share(float l, float m, const Shared& sh) {
+  if (l == m) return 1.f;
+  const float hl = sh.h * l, hm = sh.h * m, d = hl - hm;
+  const bool low = fabsf(l) > fabsf(m);
+  const float big = low ? hl : -hm, small = low ? -hm : hl;
+  const float dl = small - (d - big);
+  const float th = d * sh.ih, te = fmaf(dl, sh.ih, fmaf(d, sh.il, fmaf(d, sh.ih, -th)));
+  constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = (float)(1.4426950408889634 - (double)kLog2e);
+  const float y = th * kLog2e, rest = fmaf(th, kLog2e, -y) + fmaf(th, kLog2eLo, te * kLog2e);
+  const float w = fast_exp2(y);
+  return fmaf(w, rest * 0.6931472f, w);
+}
 
 template <bool BF16, bool RES>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
@@ -629,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       zero_probs();
       __syncthreads();
       if (stay && part == 0 && me.idx >= v0 && me.idx < v0 + n_own)
-        probs[me.idx - v0] = fast_exp2(octaves(me.l, m, half, ch)) * ((float)kOne / (float)s);
+        probs[me.idx - v0] = share(me.l, m, sh) * ((float)kOne / (float)s);
     }
     if (a.token != nullptr && rank == 0) {
       uint64_t at = part_of_sum(rf, s, false);
@@ -982,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int i = tid; i < n_cand; i += kThreads) {
         const int at = cand_at[i];
         const float l = one(at);
-        if (kept(l, v0 + at) && (least == 0 || left(i, called) != 0)) probs[at] = fast_exp2(octaves(l, m, half, ch)) * inv;
+        if (kept(l, v0 + at) && (least == 0 || left(i, called) != 0)) probs[at] = share(l, m, sh) * inv;
       }
     } else {
       // min-p in octaves: what is right at it goes by the weight itself
@@ -991,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const float l = one(i), t = octaves(l, m, half, ch);
         bool stay = t > -kOctaves && kept(l, v0 + i) && t >= edge - 0.001f;
         if (stay && t < edge + 0.001f) stay = left(i, called) != 0;
-        return stay ? fast_exp2(t) * inv : 0.f;
+        return stay ? share(l, m, sh) * inv : 0.f;
       };
 #pragma unroll 4
       for (int i = w0 + lane; i < w1; i += 32) probs[i] = p(i);

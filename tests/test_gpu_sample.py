@@ -233,3 +233,11 @@ def test_many_equal_logits_at_the_cut(V, std, s):
     check(l, r, **full)
     near = (1.0 + torch.randint(0, 3, l.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) * 2.0 ** -20).float()
     check(near, r, **full)
+
+
+@pytest.mark.parametrize("temperature", [0.3, 0.7, 0.8, 1.0, 1.3, 3.0, 20.0])
+def test_small_probabilities(temperature):
+    """Wide rows, whose probabilities go down to 2^-42 and are still good to 2^-18 of themselves."""
+    l, r = normal(6, 20000, seed=11, std=14.0)
+    check(l, r, temperature=np.full(6, temperature))
+    check(l + 1000.0, r, temperature=np.full(6, temperature))
