@@ -120,6 +120,7 @@ struct Shared {
   // 1 / (h T) in two parts, and log2(e) / (h T).  h is 1; 1/2 for a temperature so high that differences of
   // logits that overflow still count; 2^24 for one so low that differences of denormal logits do
   float ih, il, ch, h, m;
+  float ch_off;  // what ch is off by, so that exp2(t) has to be changed by ch_off |t| of itself
   int bin, cut_idx;
   uint32_t bin_count, bin_above, near_lo, near_hi;
   float cut_l;
@@ -354,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     sh.h = h;
     sh.ih = inv;
     sh.il = inv > 0.f ? fmaf(-inv, ht, 1.f) * inv : 0.f;  // T may be infinite
-    sh.ch = inv * 1.4426950408889634f;
+    constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = (float)(1.4426950408889634 - (double)kLog2e);
+    sh.ch = inv * kLog2e;
+    const float lost = fmaf(inv, kLog2e, -sh.ch) + fmaf(inv, kLog2eLo, sh.il * kLog2e);
+    sh.ch_off = sh.ch > 0.f ? -0.6931472f * lost / sh.ch : 0.f;
   }
   // ---- the row, and its maximum ------------------------------------------------------------
   auto hold = [&](int i, float x) {
@@ -559,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // Lists the CTA's candidates, those up to bin `last`, in index order with their weights; where they are too many
   // without them (64 rows with some flat distributions 150 us when those went on with the whole row, 83 so), and where
   // they are too many for that as well the row stays what is looked at.
-  auto list_candidates = [&](int last) {
+  // `others`: of what is not listed its sum, and what that may be off by (not meant where nothing is listed).
+  auto list_candidates = [&](int last, auto sum_others, uint64_t (&others)[2]) {
     if (!RES || n_cand >= 0) return;
     const float edge = edge_of(last);
     // which of 32 neighbours are: lane j keeps the mask of the warp's j-th 32, of the (32 + j)-th, ...
@@ -568,10 +573,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
     for (int c = 0; c < kMasks; ++c) {
       const int to = min(w1, w0 + 1024 * (c + 1));
-#pragma unroll 4
-      for (int i = w0 + 1024 * c; i < to; i += 32) {
-        const uint32_t mask = __ballot_sync(kFull, i + lane < w1 && before_edge(one(i + lane), edge));
-        if (lane == ((i - w0) >> 5 & 31)) masks[c] = mask;
+      float rest[4] = {}, slope = 0.f;
+      for (int i = w0 + 1024 * c; i < to; i += 128) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = i + 32 * u + lane;
+          const float t = at < w1 ? octaves(one(at), m, half, ch) : -INFINITY;
+          const bool counts = t > -kOctaves, in = counts && -t * kBinScale < edge;  // bin_of(t) <= last
+          const uint32_t mask = __ballot_sync(kFull, in);
+          if (lane == ((i - w0) >> 5 & 31) + u) masks[c] = mask;
+          if (decltype(sum_others)::value) {
+            const float w = counts && !in ? fast_exp2(t) : 0.f;
+            rest[u] += w;
+            slope = fmaf(w, counts ? -t : 0.f, slope);
+          }
+        }
+      }
+      if (decltype(sum_others)::value) {
+        // What rounding took from 1 / T goes by the octaves.  Else off by at most: an exponential 2^-22 of itself, its
+        // exponent two roundings; ten additions, each 2^-24; an exact weight 2^-34 of itself and half a unit.
+        const float raw = (rest[0] + rest[1]) + (rest[2] + rest[3]), all = fmaf(slope, sh.ch_off, raw);
+        const float off = 1.01f * (raw * (0x1p-22f + 12.f * 0x1p-24f) + slope * (0.6931472f * 2.f * 0x1p-24f));
+        others[0] += (uint64_t)(all * (float)kOne);
+        others[1] += (uint64_t)(off * (float)kOne) + 18u;
       }
       n += __popc(masks[c]);
     }
@@ -586,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     if (all > (uint32_t)a.cap_bare) return;
     weighed = all <= (uint32_t)a.cap;
-    if (!weighed) cand_at = reinterpret_cast<uint16_t*>(cand_w);
+    cand_at = reinterpret_cast<uint16_t*>(cand_w + (weighed ? a.cap : 0));
     const uint32_t first = at;
 #pragma unroll
     for (int c = 0; c < kMasks; ++c) {
@@ -606,7 +630,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
   // Everything that may be kept is in the list (kFew at most): the rest of the work is four lanes an element.  Of
   // the list's order the first k stay; top-p of `total` (0: of what stays).
-  auto finish_list = [&](int n, int k, uint64_t total) {
+  // The running weight that has to be reached is given by its bounds (0: top-p of what stays); false where they
+  // do not decide.
+  auto finish_list = [&](int n, int k, uint64_t target, uint64_t target_hi) -> bool {
     constexpr int lanes = kThreads / kFew;
     const int me_at = tid / lanes, part = tid % lanes;
     const bool in = me_at < n;
@@ -629,10 +655,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     wb = of_lanes(wb);
     r = (uint32_t)of_lanes(r);
-    if (in && (int)r == min(k, n) - 1) sh.sum = wb + me.w;  // all lanes of the one element
-    __syncthreads();
-    if (total == 0) total = sh.sum;
-    const uint64_t target = top_p < 1.f ? part_of_sum(top_p, total, true) : ~0ull;
+    if (target == 0) {
+      if (in && (int)r == min(k, n) - 1) sh.sum = wb + me.w;  // all lanes of the one element
+      __syncthreads();
+      target = top_p < 1.f ? part_of_sum(top_p, sh.sum, true) : ~0ull;
+    } else if (target != target_hi && __syncthreads_or(in && r > 0 && wb >= target && wb < target_hi)) {
+      return false;
+    }
     const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
     const bool stay = in && (int)r < k && (r == 0 || (wb < target && me.w >= least));
     uint64_t s = stay ? wb + me.w : 0ull;  // the last that stays has them all
@@ -658,11 +687,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     cluster_arrive();
     cluster_wait();
+    return true;
   };
 
   // The cut at the list's element where the running value (1 an element, or its weight), from `above` on, reaches
-  // `target`; false where none does.
-  auto cut_in_list = [&](bool weights, uint64_t target, uint64_t above, uint32_t n) -> bool {
+  // the target, of which bounds are given; false where none does for both.
+  auto cut_in_list = [&](bool weights, uint64_t target, uint64_t target_hi, uint64_t above, uint32_t n) -> bool {
     bool here = false;
     constexpr uint32_t kLanes = 4;  // of an element
     for (uint32_t e0 = 0; e0 < n; e0 += kThreads / kLanes) {
@@ -676,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       x += __shfl_xor_sync(kFull, x, 1);
       x += __shfl_xor_sync(kFull, x, 2) + above;
-      if (e < n && x < target && x + (weights ? me.w : 1ull) >= target) {
+      if (e < n && x < target && x + (weights ? me.w : 1ull) >= target_hi) {
         here = true;
         sh.cut_l = me.l;  // all lanes of the one element
         sh.cut_idx = me.idx;
@@ -692,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     auto inside = [&](float t) { return bin_of(t) == bin && (fine < 0 || fine_of(t, bin) == fine); };
     if (count <= (uint32_t)kList) {
       gather(inside);
-      cut_in_list(weights, target, above, count);
+      cut_in_list(weights, target, target, above, count);
       return;
     }
     // Too many: the largest key from which on the values reach the target, bit by bit where the bin's keys differ (few,
@@ -773,10 +803,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (above + count <= (uint32_t)kFew) {
         collect_to(bin);
         read_all();
-        finish_list((int)(above + count), (int)k, 0);
+        finish_list((int)(above + count), (int)k, 0, 0);
         return;
       }
-      list_candidates(bin);
+      uint64_t unused[2];
+      list_candidates(bin, std::false_type(), unused);
       int fine = -1;
       if (count > (uint32_t)kList) {
         cluster_sync();  // the counts have been read
@@ -794,26 +825,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   // ---- top-p ------------------------------------------------------------------------------
   if (top_p < 1.f) {
-    uint64_t z[1] = {0};
+    // The sum of all weights: of rows that stay in shared memory, and from which top-k has taken nothing, exactly
+    // that of the candidates, once they are listed, and bounds of what the others add, which nearly always decide;
+    // else (and where they do not) exactly.
+    uint64_t target = 0, target_hi = 0;
+    const bool bounded = RES && n_cand < 0 && cut_idx == INT_MAX;
     clear_bins();
-    auto add = [&](float l, int idx, auto w) {
-      const int x = bin_of(octaves(l, m, half, ch));
-      if (x < kBins - 1 && kept(l, idx)) {
-        atomicAdd(&sh.u.hist[x], 1u);
-        z[0] += w();
-      }
-    };
-    if (n_cand >= 0) {
-      each(add);
+    if (bounded) {
+      each4([&](float l, int, auto) {
+        const int x = bin_of(octaves(l, m, half, ch));
+        if (x < kBins - 1) atomicAdd(&sh.u.hist[x], 1u);
+      });
+      cluster_sync();
     } else {
+      uint64_t z[1] = {0};
+      auto add = [&](float l, int idx, auto w) {
+        const int x = bin_of(octaves(l, m, half, ch));
+        if (x < kBins - 1 && kept(l, idx)) {
+          atomicAdd(&sh.u.hist[x], 1u);
+          z[0] += w();
+        }
+      };
+      if (n_cand >= 0) {
+        each(add);
+      } else {
 #pragma unroll 2
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const float l = one(i);
-        add(l, v0 + i, [&] { return weight(l, m, sh); });
+        for (int i = w0 + lane; i < w1; i += 32) {
+          const float l = one(i);
+          add(l, v0 + i, [&] { return weight(l, m, sh); });
+        }
       }
+      cluster_sum(z);
+      target = target_hi = part_of_sum(top_p, z[0], true);
     }
-    cluster_sum(z);
-    const uint64_t target = part_of_sum(top_p, z[0], true);
     int bin = -1, fine = -1;
     uint64_t above = 0;
     uint32_t count = 0;
@@ -846,60 +890,110 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         auto tell_upto = [&](int of) {
           if (tid == of >> 1) sh.near_hi = of & 1 ? c_incl : c_mid;
         };
-        tell_before(guess);
-        tell_upto(guess);
+        if (tid == guess >> 1) sh.bin_count = guess & 1 ? h.y : h.x;
         __syncthreads();
         const uint32_t n = sh.bin_above;
-        if (n <= (uint32_t)kFew) {
-          collect_to(last);
-          read_all();
-          uint64_t s = tid < (int)n ? sh.list[tid].w : 0ull;
-          s = warp_sum64(s);
+        bool exactly = bounded && sh.bin_count > (uint32_t)kList;
+        uint64_t z[2] = {0, 0};
+        list_candidates(last, std::true_type(), z);
+        if (bounded && !exactly) {
+          // where they do not fit, all of them
+          if (n_cand < 0) z[0] = z[1] = 0;
+          each([&](float l, int, auto w) {
+            if (octaves(l, m, half, ch) > -kOctaves) z[0] += w();
+          });
+          cluster_sum(z);
+          target = part_of_sum(top_p, z[0] - z[1], true);
+          target_hi = part_of_sum(top_p, z[0] + z[1], true);
+        }
+        // the sum of the list's weights
+        auto listed_sum = [&](uint32_t n) -> uint64_t {
+          uint64_t s = warp_sum64(tid < (int)n ? sh.list[tid].w : 0ull);
           if (lane == 0) sh.part[warp][0] = s;
           __syncthreads();
           s = 0;
           for (int w = 0; w < kWarps; ++w) s += sh.part[w][0];
-          if (s >= target) {
-            finish_list((int)n, INT_MAX, z[0]);
-            return;
+          return s;
+        };
+        int tries = 0;
+        for (bool few = n <= (uint32_t)kFew;;) {
+          if (exactly) {  // the bounds do not decide, or are not worth it
+            uint64_t z[1] = {0};
+#pragma unroll 2
+            for (int i = w0 + lane; i < w1; i += 32) {
+              const float l = one(i);
+              if (octaves(l, m, half, ch) > -kOctaves) z[0] += weight(l, m, sh);
+            }
+            cluster_sum(z);
+            target = target_hi = part_of_sum(top_p, z[0], true);
+            exactly = false;
           }
-          cluster_sync();  // nothing else is collected before all have read
-        }
-        list_candidates(last);
-        // the bins around the guess, as many as fit, are ranked at once, and what lies before them summed
-        const uint32_t lo_c = sh.near_lo, hi_c = sh.near_hi, wing = kNear > hi_c - lo_c ? (kNear - (hi_c - lo_c)) / 2 : 0u;
-        __syncthreads();
-        if (tid == 0) {
-          sh.bin = kBins;
-          sh.bin_count = 0;
-        }
-        __syncthreads();
-        if (c_mid + wing >= lo_c) atomicMin(&sh.bin, c_excl + wing >= lo_c ? 2 * tid : 2 * tid + 1);
-        if (c_mid <= hi_c + wing) atomicMax(&sh.bin_count, (uint32_t)(c_incl <= hi_c + wing ? 2 * tid + 1 : 2 * tid));
-        __syncthreads();
-        const int near_first = min(sh.bin, guess), near_last = max(guess, min((int)sh.bin_count, last));
-        tell_before(near_first);
-        tell_upto(near_last);
-        __syncthreads();
-        const uint32_t near = sh.near_hi - sh.near_lo;
-        if (near <= (uint32_t)kList) {
-          uint64_t s[1] = {0};
-          collect([&](float t) {
-            const int x = bin_of(t);
-            return x >= near_first && x <= near_last;
-          });
-          each([&](float l, int idx, auto w) {
-            const float t = octaves(l, m, half, ch);
-            if (t > -kOctaves && bin_of(t) < near_first && kept(l, idx)) s[0] += w();
-          });
-          cluster_sum(s);
-          read_all();
-          if (cut_in_list(true, target, s[0], near)) {
-            done = true;
-            break;
+          if (few) {
+            collect_to(last);
+            read_all();
+            if (listed_sum(n) < target_hi) {  // the row may reach it behind them
+              few = false;
+              cluster_sync();  // nothing else is collected before all have read
+              continue;
+            }
+            if (finish_list((int)n, INT_MAX, target, target_hi)) return;
+          } else {
+            // the bins around the guess, as many as fit, are ranked at once, and what lies before them summed
+            tell_before(guess);
+            tell_upto(guess);
+            __syncthreads();
+            const uint32_t lo_c = sh.near_lo, hi_c = sh.near_hi, wing = kNear > hi_c - lo_c ? (kNear - (hi_c - lo_c)) / 2 : 0u;
+            __syncthreads();
+            if (tid == 0) {
+              sh.bin = kBins;
+              sh.bin_count = 0;
+            }
+            __syncthreads();
+            if (c_mid + wing >= lo_c) atomicMin(&sh.bin, c_excl + wing >= lo_c ? 2 * tid : 2 * tid + 1);
+            if (c_mid <= hi_c + wing) atomicMax(&sh.bin_count, (uint32_t)(c_incl <= hi_c + wing ? 2 * tid + 1 : 2 * tid));
+            __syncthreads();
+            const int near_first = min(sh.bin, guess), near_last = max(guess, min((int)sh.bin_count, last));
+            tell_before(near_first);
+            tell_upto(near_last);
+            if (tid == near_first >> 1) sh.mass = incl - mass1 - (near_first & 1 ? 0.f : mass0);
+            __syncthreads();
+            const uint32_t near = sh.near_hi - sh.near_lo;
+            if (near <= (uint32_t)kList) {
+              uint64_t s[1] = {0};
+              collect([&](float t) {
+                const int x = bin_of(t);
+                return x >= near_first && x <= near_last;
+              });
+              each([&](float l, int idx, auto w) {
+                const float t = octaves(l, m, half, ch);
+                if (t > -kOctaves && bin_of(t) < near_first && kept(l, idx)) s[0] += w();
+              });
+              cluster_sum(s);
+              read_all();
+              if (cut_in_list(true, target, target_hi, s[0], near)) {
+                done = true;
+                break;
+              }
+              const uint64_t end = s[0] + listed_sum(near);
+              cluster_sync();
+              if (tries++ < 2 && (target_hi <= s[0] || target > end)) {  // outside: from the exact sum on, by the histogram
+                if (tid == 0) sh.bin = kBins - 1;
+                __syncthreads();
+                const float from = sh.mass + (float)(int64_t)(target - s[0]) * (1.f / (float)kOne);
+                if (from <= incl) atomicMin(&sh.bin, 2 * tid + (incl - mass1 < from ? 1 : 0));
+                __syncthreads();
+                const int moved = sh.bin;
+                if (moved <= last && moved < kBins - 1 && moved != guess) {
+                  guess = moved;
+                  continue;
+                }
+              }
+            }
+            if (target == target_hi) break;
           }
-          cluster_sync();  // nothing else is collected before all have read
+          exactly = true;
         }
+        if (done) break;
       }
       // the exact sums around the guess
       auto part_of = [&](float t) -> int {  // -1: before the bin that is looked into; kBins: behind
