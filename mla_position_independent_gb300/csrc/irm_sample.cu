@@ -9,9 +9,12 @@
 // (logit, index), and no row is sorted: a histogram of the logits' distance from the maximum (1023 bins, 23
 // an octave of w) finds the bin that holds the cut.  Up to 128 elements that may be kept are ranked among
 // themselves and the row finished from them.  Else the candidates, up to a few bins behind the cut, are listed
-// where shared memory holds them, and the cut's bin (top-p: some 96 elements around a guess from the histogram
-// and each bin's middle weight, which the exact sum before them confirms or moves) is ranked, after a
-// second histogram inside the bin if it has more than 256; the draw is an inverse of the sums of 128 elements each, then
+// where shared memory holds them, and the cut's bin ranked, after a second histogram inside the bin if it has more
+// than 256.  A top-p cut: some 96 elements are ranked around a guess from the histogram and each bin's middle
+// weight, with the exact sum before them, which confirms the guess or moves it.  p of the sum of all weights is
+// known by bounds: the candidates' exactly, the others' in fp32 with what rounding may have done to it; where an
+// element's running weight lies between the bounds (one row in a hundred), or bins are so full that
+// passes repeat, that sum too is made exact.  The draw is an inverse of the sums of 128 elements each, then
 // of one group.  More than 256 in a bin's 1024th part are mostly equal logits, of which a count finds the last.
 //
 // Arithmetic.  Which token comes out must not depend on the split or the order of addition, and a flat
@@ -26,18 +29,18 @@
 // A cluster of 1 to 8 CTAs shares a row, which stays in shared memory from its one read, in the type in which it
 // came, where a CTA's part fits (53376 logits of fp32, 65536 of bf16); longer rows are read again by each pass.
 //
-// What bounds it.  One row: latency, 15 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
+// What bounds it.  One row: latency, 15.8 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
 // maximum take 2.6, the histogram and its exchange 4, the list and its exchange 4, the ranks 3.  Many rows:
-// instructions, 384 bf16 rows with top-p and probabilities 260 us (35 by their bytes) at 0.67 instructions a clock
-// and scheduler, two CTAs of 512 threads on an SM; a third of them are the weights of all elements, whose
-// sum a top-p cut needs, a fifth the list of candidates, the rest what a CTA does whatever its part's length
-// (scans, exchanges, ranks), which is why few CTAs a row are best.  Steps that were, for these 384 rows: a pass
+// instructions and what a CTA does whatever its part's length (scans, exchanges, ranks), which is why few CTAs
+// a row are best: 384 bf16 rows with top-p and probabilities 210 us (35 by their bytes), 112 instructions a warp and
+// 32 logits at 0.57 a clock and scheduler, two CTAs of 512 threads on an SM.  Steps that were, for these 384 rows: a pass
 // over all elements, and one over those near the cut, for each sum 635; the candidates listed with their weights
 // 475; one element a lane, ranks by four lanes an element 409; fewer neighbours and shorter lists 390; bf16 rows held as
 // bf16 by clusters of 4 instead of 8 285, of 3 279; four logits a lane and lists by masks 270, rows finished from
-// lists of 128 instead of 448 elements 259.  Not taken: a first sum of fp32 exponentials with a bound on its error
-// (a third of the exact one's time, but the rows near whose target an element lies, a tenth and more, need that as
-// well: 440 instead of 409); lists sorted by a bitonic network instead of ranked (270 instead of 259).
+// lists of 128 instead of 448 elements 262; the sum of what is not listed by bounds, and a missed window
+// moved, 210 (fp32 302 -> 268, 64 rows with some flat distributions 56 -> 57).  Not taken: all of the sum by bounds,
+// which decide too seldom (440 instead of 409); lists sorted by a bitonic network instead of ranked (270 instead
+// of 259); bounds also where the cut's bin has more than 256 (64 rows with flat ones 62).
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>
