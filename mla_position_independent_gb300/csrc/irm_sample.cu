@@ -262,15 +262,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int wseg = (n_own + kWarps * kGroup - 1) / (kWarps * kGroup) * kGroup;
   const int w0 = min(n_own, warp * wseg), w1 = min(n_own, w0 + wseg);
   // f(logit, index, weight()) for the CTA's logits, or for the candidates once they are listed (in index order)
-  uint64_t* cand_w = reinterpret_cast<uint64_t*>(row_sh + (RES ? a.seg : 0));  // their weights, and where in the row they are
-  uint16_t* cand_at = reinterpret_cast<uint16_t*>(cand_w + a.cap);  // (too many for the weights: in their place)
+  // Candidates: the weight (44 bits) and behind it the place in the CTA's part; too many for that: the places alone.
+  uint64_t* cand = reinterpret_cast<uint64_t*>(row_sh + (RES ? a.seg : 0));
+  uint16_t* cand_at = reinterpret_cast<uint16_t*>(cand);
   int n_cand = -1;
   bool weighed = true;
+  auto place = [&](int i) -> int { return weighed ? (int)(cand[i] & 0xffffu) : cand_at[i]; };
   auto each = [&](auto f) {
     if (n_cand >= 0 && weighed) {
       for (int i = tid; i < n_cand; i += kThreads) {
-        const int at = cand_at[i];
-        f(one(at), v0 + at, [&] { return cand_w[i]; });
+        const uint64_t x = cand[i];
+        const int at = (int)(x & 0xffffu);
+        f(one(at), v0 + at, [&] { return x >> 16; });
       }
       return;
     }
@@ -613,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     if (all > (uint32_t)a.cap_bare) return;
     weighed = all <= (uint32_t)a.cap;
-    cand_at = reinterpret_cast<uint16_t*>(cand_w + (weighed ? a.cap : 0));
     const uint32_t first = at;
 #pragma unroll
     for (int c = 0; c < kMasks; ++c) {
@@ -623,11 +625,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const uint32_t x = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += x;
       }
-      for (uint32_t to = at + incl - __popc(mask); mask != 0; mask &= mask - 1) cand_at[to++] = (uint16_t)(w0 + 1024 * c + 32 * lane + __ffs(mask) - 1);
+      for (uint32_t to = at + incl - __popc(mask); mask != 0; mask &= mask - 1) {
+        const uint32_t x = w0 + 1024 * c + 32 * lane + __ffs(mask) - 1;
+        if (weighed) cand[to++] = x;
+        else cand_at[to++] = (uint16_t)x;
+      }
       at += __shfl_sync(kFull, incl, 31);
     }
     __syncwarp();
-    for (uint32_t i = weighed ? first + lane : at; i < at; i += 32) cand_w[i] = weight_of(one(cand_at[i]), m, sh);
+    for (uint32_t i = weighed ? first + lane : at; i < at; i += 32) cand[i] |= weight_of(one((int)cand[i]), m, sh) << 16;
     n_cand = (int)all;
     __syncthreads();
   };
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int i0 = min(items, warp * part), i1 = min(items, i0 + part);
     auto index_of = [&](int i) -> int {  // of an item that is one of them; else -1
       if (i >= i1) return -1;
-      const int at = n_cand >= 0 ? cand_at[i] : i;
+      const int at = n_cand >= 0 ? place(i) : i;
       const float l = one(at);
       return order_key(l) == key && kept(l, v0 + at) ? v0 + at : -1;
     };
@@ -1067,9 +1073,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // the weight left of element i of what is looked at (behind its end: none)
   auto left = [&](int i, auto weigh) -> uint64_t {
     if (i >= n_left) return 0ull;
+    if (listed && weighed) {
+      const uint64_t x = cand[i];
+      const int at = (int)(x & 0xffffu);
+      return kept(one(at), v0 + at) && x >> 16 >= least ? x >> 16 : 0ull;
+    }
     const int at = listed ? cand_at[i] : i;
     const float l = one(at);
-    if (listed && weighed) return kept(l, v0 + at) && cand_w[i] >= least ? cand_w[i] : 0ull;
     if (!(octaves(l, m, half, ch) > -kOctaves) || !kept(l, v0 + at)) return 0ull;
     const uint64_t w = weigh(l);
     return w >= least ? w : 0ull;
@@ -1093,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       zero_probs();
       __syncthreads();
       for (int i = tid; i < n_cand; i += kThreads) {
-        const int at = cand_at[i];
+        const int at = place(i);
         const float l = one(at);
         if (kept(l, v0 + at) && (least == 0 || left(i, called) != 0)) probs[at] = share(l, m, sh) * inv;
       }
@@ -1138,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const int i = (g0 + src) * kSummed + e + lane;
         const uint64_t x = left(i, called);
         if (!scan(x, incl)) continue;
-        if (at >= run + incl - x && at < run + incl) a.token[b] = v0 + (listed ? (int)cand_at[i] : i);
+        if (at >= run + incl - x && at < run + incl) a.token[b] = v0 + (listed ? place(i) : i);
         break;
       }
       break;
@@ -1151,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 using Kernel = void (*)(SampleArgs);
 
 constexpr size_t kSmemTwo = 233472 / 2 - 1024, kSmemOne = 232448;  // of a CTA, with another one on the SM and alone
-constexpr size_t kCand = sizeof(uint64_t) + sizeof(uint16_t);      // a candidate's bytes
+constexpr size_t kCand = sizeof(uint64_t);  // a candidate's bytes
 constexpr int kCandLeast = 512;  // candidates that a CTA has room for where two share an SM
 
 // What a device has room for at once, clusters of 1 to 8 CTAs with two CTAs on an SM and with one (clusters do
