@@ -29,16 +29,16 @@
 // A cluster of 1 to 8 CTAs shares a row, which stays in shared memory from its one read, in the type in which it
 // came, where a CTA's part fits (53376 logits of fp32, 65536 of bf16); longer rows are read again by each pass.
 //
-// What bounds it.  One row: latency, 15.8 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
+// What bounds it.  One row: latency, 14.7 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
 // maximum take 2.6, the histogram and its exchange 4, the list and its exchange 4, the ranks 3.  Many rows:
 // instructions and what a CTA does whatever its part's length (scans, exchanges, ranks), which is why few CTAs
-// a row are best: 384 bf16 rows with top-p and probabilities 210 us (35 by their bytes), 112 instructions a warp and
-// 32 logits at 0.57 a clock and scheduler, two CTAs of 512 threads on an SM.  Steps that were, for these 384 rows: a pass
+// a row are best: 384 bf16 rows with top-p and probabilities 206 us (35 by their bytes), 111 instructions a warp and
+// 32 logits at 0.58 a clock and scheduler, two CTAs of 512 threads on an SM.  Steps that were, for these 384 rows: a pass
 // over all elements, and one over those near the cut, for each sum 635; the candidates listed with their weights
 // 475; one element a lane, ranks by four lanes an element 409; fewer neighbours and shorter lists 390; bf16 rows held as
 // bf16 by clusters of 4 instead of 8 285, of 3 279; four logits a lane and lists by masks 270, rows finished from
 // lists of 128 instead of 448 elements 262; the sum of what is not listed by bounds, and a missed window
-// moved, 210 (fp32 302 -> 268, 64 rows with some flat distributions 56 -> 57).  Not taken: all of the sum by bounds,
+// moved, 217 (fp32 302 -> 268, 64 rows with some flat distributions 56 -> 57), a candidate in one word 206 to 213.  Not taken: all of the sum by bounds,
 // which decide too seldom (440 instead of 409); lists sorted by a bitonic network instead of ranked (270 instead
 // of 259); bounds also where the cut's bin has more than 256 (64 rows with flat ones 62).
 #include <cuda_runtime.h>
