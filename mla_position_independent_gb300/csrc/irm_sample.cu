@@ -27,7 +27,7 @@
 // sum.
 //
 // A cluster of 1 to 8 CTAs shares a row, which stays in shared memory from its one read, in the type in which it
-// came, where a CTA's part fits (53376 logits of fp32, 65536 of bf16); longer rows are read again by each pass.
+// came, where a CTA's part fits (some 53600 logits of fp32, 65536 of bf16); longer rows are read again by each pass.
 //
 // What bounds it.  One row: latency, 14.7 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
 // maximum take 2.6, the histogram and its exchange 4, the list and its exchange 4, the ranks 3.  Many rows:
@@ -38,9 +38,10 @@
 // 475; one element a lane, ranks by four lanes an element 409; fewer neighbours and shorter lists 390; bf16 rows held as
 // bf16 by clusters of 4 instead of 8 285, of 3 279; four logits a lane and lists by masks 270, rows finished from
 // lists of 128 instead of 448 elements 262; the sum of what is not listed by bounds, and a missed window
-// moved, 217 (fp32 302 -> 268, 64 rows with some flat distributions 56 -> 57), a candidate in one word 206 to 213.  Not taken: all of the sum by bounds,
-// which decide too seldom (440 instead of 409); lists sorted by a bitonic network instead of ranked (270 instead
-// of 259); bounds also where the cut's bin has more than 256 (64 rows with flat ones 62).
+// moved, 217 (fp32 302 -> 268, 64 rows with some flat distributions 56 -> 57), a candidate in one word 206 to 213.
+// Not taken: all of the sum by bounds, which decide too seldom (440 instead of 409); lists sorted by a bitonic
+// network instead of ranked (270 instead of 259); bounds also where the cut's bin has more than 256 (64 rows with
+// flat ones 62).
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>
@@ -1213,11 +1214,12 @@ cudaError_t device_of(Device& out) {
 int part_of_row(int V, int C) { return ((V + C - 1) / C + 3) / 4 * 4; }
 
 // CTAs of a row.  Many rows: as few as let two CTAs share an SM (what a CTA does beside its part of the row
-// is the larger half: 384 rows of 102400 fp32 logits, top-p with probabilities, 302 us with 5, 387 with 8; bf16
-// 259 with 3, 272 with 4, 380 with 8).  Few rows: more, as long as each CTA has an SM (one row 27.6 us with
-// 8, 31.5 with 5; 20 rows 35.9 with 6, 38.7 with 8, which share SMs); then as many as let the batch be worked on at
-// once (44 rows 49 with 6, 63 with 8), or 8 if fewer do not save a turn (64 rows 58 with 8 and 84 with 5 where some of
-// the rows have flat distributions, which take longest, 79 and 74 where all are alike; 128 rows 92 and 75, 141 and 115).
+// is the larger half: 384 rows of 102400 fp32 logits, top-p with probabilities, 263 us with 5, 345 with 8; bf16
+// 215 with 3, 227 with 4, 339 with 8).  Few rows: more, as long as each CTA has an SM (one row 26 us with 8, 29
+// with 5; 20 rows with top-k 17.1 with 6, 19.5 with 8, which share SMs, but with top-p 41 and 38); then as many as let
+// the batch be worked on at once (44 rows 45 with 6, 57 with 8), or 8 if fewer do not save a turn (64 rows 58 with 8 and
+// 63 with 5 where some of the rows have flat distributions, which take longest, 66 and 64 where all are alike; 128
+// rows 85 and 67, 126 and 106).
 int cluster_size(int64_t rows, int V, size_t bytes, const Device& dev) {
   int least = 1;
   while (least < kMaxCluster && part_of_row(V, least) * bytes + kCandLeast * kCand + sizeof(Shared) > kSmemTwo) ++least;
