@@ -665,13 +665,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     wb = of_lanes(wb);
     r = (uint32_t)of_lanes(r);
-    if (target == 0) {
-      if (in && (int)r == min(k, n) - 1) sh.sum = wb + me.w;  // all lanes of the one element
-      __syncthreads();
-      target = top_p < 1.f ? part_of_sum(top_p, sh.sum, true) : ~0ull;
-    } else if (target != target_hi && __syncthreads_or(in && r > 0 && wb >= target && wb < target_hi)) {
-      return false;
-    }
+    // behind this barrier no warp reads the list's weights, or sh.part, as they were
+    if (target == 0 && in && (int)r == min(k, n) - 1) sh.sum = wb + me.w;  // all lanes of the one element
+    if (__syncthreads_or(in && r > 0 && wb >= target && wb < target_hi)) return false;  // never where the bounds are equal
+    if (target == 0) target = top_p < 1.f ? part_of_sum(top_p, sh.sum, true) : ~0ull;
     const uint64_t least = min_p > 0.f ? part_of_sum(min_p, kOne, true) : 0ull;
     const bool stay = in && (int)r < k && (r == 0 || (wb < target && me.w >= least));
     uint64_t s = stay ? wb + me.w : 0ull;  // the last that stays has them all
@@ -923,6 +920,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           __syncthreads();
           s = 0;
           for (int w = 0; w < kWarps; ++w) s += sh.part[w][0];
+          __syncthreads();  // the next sum's values are not among these
           return s;
         };
         int tries = 0;
