@@ -183,9 +183,11 @@ __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float(
 // NaN as -infinity, -0 as 0
 __device__ __forceinline__ float clean(float l) { return l == l ? l + 0.f : -INFINITY; }
 
-// Distance of a logit from the maximum in octaves of weight (<= 0; NaN or below -kOctaves: no weight).
-__device__ __forceinline__ float octaves(float l, float m, float h, float ch) { return l == m ? 0.f : fmaf(l, h, -h * m) * ch; }
-__device__ __forceinline__ int bin_of(float t) { return t > -kOctaves ? min(kBins - 2, (int)(-t * kBinScale)) : kBins - 1; }
+// Distance of a logit from the maximum in octaves of weight (<= 0; NaN or below -kOctaves: no weight).  h m overflows
+// where neighbouring logits are far more octaves apart than a weight has: the distance is then infinite, and negative
+// for a negative maximum too.
+__device__ __forceinline__ float octaves(float l, float m, float h, float ch) { return l == m ? 0.f : -fabsf(fmaf(l, h, -h * m)) * ch; }
+__device__ __forceinline__ int bin_of(float t) { return t > -kOctaves ? min(kBins - 2, (int)__float2uint_rz(-t * kBinScale)) : kBins - 1; }
 // The same inside a bin: its elements spread over kBins again.
 __device__ __forceinline__ int fine_of(float t, int bin) {
   return min(kBins - 1, max(0, (int)((-t * kBinScale - (float)bin) * (float)kBins)));
