@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
 
   auto cluster_sync = [&] {
-    __syncwarp();
+    __syncwarp();  // the barrier's instruction is a whole warp's
     cluster_arrive();
     cluster_wait();
   };
@@ -447,8 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (tid == 0 && first >= v0 && first < v0 + n_own) probs[first - v0] = 1.f;
     }
     if (a.token != nullptr && rank == 0 && tid == 0) a.token[b] = first;
-    cluster_arrive();  // no CTA ends while another may still store into it
-    cluster_wait();
+    cluster_sync();  // no CTA ends while another may still store into it
     return;
   }
   const float ch = sh.ch, half = sh.h;
@@ -694,8 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       x = of_lanes(x);
       if (stay && at >= x && at < x + me.w) a.token[b] = me.idx;
     }
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync();
     return true;
   };
 
@@ -1155,8 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       break;
     }
   }
-  cluster_arrive();
-  cluster_wait();
+  cluster_sync();
 }
 
 using Kernel = void (*)(SampleArgs);
