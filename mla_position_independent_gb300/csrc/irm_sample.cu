@@ -188,9 +188,10 @@ __device__ __forceinline__ float clean(float l) { return l == l ? l + 0.f : -INF
 // for a negative maximum too.
 __device__ __forceinline__ float octaves(float l, float m, float h, float ch) { return l == m ? 0.f : -fabsf(fmaf(l, h, -h * m)) * ch; }
 __device__ __forceinline__ int bin_of(float t) { return t > -kOctaves ? min(kBins - 2, (int)__float2uint_rz(-t * kBinScale)) : kBins - 1; }
-// The same inside a bin: its elements spread over kBins again.
+// The same inside a bin: its elements spread over kBins again.  Every pass has to place an element alike, so the product
+// and the difference are rounded one by one (fused by some passes and not by others they would differ by up to 1 / 32 of a part).
 __device__ __forceinline__ int fine_of(float t, int bin) {
-  return min(kBins - 1, max(0, (int)((-t * kBinScale - (float)bin) * (float)kBins)));
+  return min(kBins - 1, max(0, (int)(__fsub_rn(__fmul_rn(-t, kBinScale), (float)bin) * (float)kBins)));
 }
 
 // exp((l - m) / T) in units of 2^-43, for a logit with a weight (octaves > -kOctaves).
@@ -215,8 +216,8 @@ __device__ __forceinline__ uint64_t weight(float l, float m, const Shared& sh) {
   const float yh = fmaf(s, q, xh);
   const float yl = fmaf(s, q, xh - yh) + fmaf(xl, xh, xl);
   const float t4 = sh.th4[i], tl = sh.tl[i], t = t4 - 4.f;
-  const float ph = t * yh, pl = fmaf(t, yh, -ph);
-  const float a = t4 + ph;  // in [4, 8): multiples of 2^-21
+  const float ph = __fmul_rn(t, yh), pl = fmaf(t, yh, -ph);
+  const float a = t4 + ph;  // in [4, 8): multiples of 2^-21 (ph is the rounded product: what it lost is in pl)
   const float rest = fmaf(tl, yh, fmaf(t, yl, pl)) + (ph - (a - t4)) + tl;
   const float b = rest + 0x1.8p-19f;  // |rest| <= 2^-21 and a little: multiples of 2^-42
   const int64_t v = ((int64_t)(__float_as_int(a) - 0x40800000) << 21) + (__float_as_int(b) - __float_as_int(0x1.8p-19f));

@@ -36,3 +36,20 @@ def bin_of(t):
         x = -t * SCALE
         whole = np.where(np.abs(x) < 2.0 ** 31, np.trunc(x), np.where(x > 0, 2.0 ** 31 - 1, -2.0 ** 31))
         return np.where(t > -OCTAVES, np.minimum(BINS - 2, whole), BINS - 1)
+
+
+def fine_of(t, b, fused=False):
+    """The part of bin b in which t lies; fused: product and difference in one rounding."""
+    t = np.asarray(t, f32)
+    x = (-t.astype(f64) * f64(SCALE) - f64(b)).astype(f32) if fused else (-t * SCALE).astype(f32) - f32(b)
+    return np.clip(np.trunc(x * f32(BINS)), 0, BINS - 1).astype(int)
+
+
+def logits_of_a_bin(b, n, rng, T=1.0):
+    """n logits, whose largest is 0 elsewhere, that lie in bin b; those whose part of it depends on the fusing first."""
+    h, ch = scale_of(T)
+    l = -((b + rng.random(8 * n)) / f64(SCALE) / f64(ch)).astype(f32)
+    t = octaves(l, 0.0, T)
+    l, t = l[bin_of(t) == b], t[bin_of(t) == b]
+    differ = fine_of(t, b) != fine_of(t, b, fused=True)
+    return np.concatenate([l[differ], l[~differ]])[:n], int(differ.sum())

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import mla_position_independent_gb300 as irm
+import sample_bins as sb
 from test_gpu_sample import check, f32
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +34,26 @@ def test_low_temperatures_of_far_negative_rows(temperature, V):
         x = f32(l).to(dtype)
         for s in (dict(), dict(k=2), dict(k=V // 2 + 1), dict(p=0.5), dict(p=0.9, m=0.1), dict(k=V, p=0.3)):
             check(x, r, temperature=np.full(6, temperature), **{n: np.full(6, v) for n, v in s.items()})
+
+
+@pytest.mark.parametrize("b", [520, 800, 1000])
+@pytest.mark.parametrize("n", [3000, 40000])
+def test_a_full_bin_is_parted_alike_by_every_pass(b, n):
+    """Many logits of one bin of the histogram, which are looked at again by its 1024 parts: of those at a part's
+    border each pass has to think the same (whether it rounds the product before the difference or not)."""
+    rng = np.random.default_rng(b + n)
+    T = 10
+    l = np.full((T, n + 1), -np.inf, np.float32)
+    for t in range(T):
+        l[t, 1:] = rng.permutation(sb.logits_of_a_bin(b, n, rng)[0])
+    l[:, 0] = 0.0
+    r = rng.random(T, np.float32)
+    x = f32(l)
+    check(x, r, k=rng.integers(2, n, T))
+    check(x, r, k=n // 10 + np.arange(T))
+    # b = 800: p leaves out 2^-24, and the bin's weights, of 2^-34.3 each, have more together (2^-22.7 or more), so the cut is
+    # among them, where running sums lie 2^-34.3 apart: nearer than the 2^-32 within which check() does not decide
+    if b != 800:
+        check(x, r, k=np.full(T, n - 100), p=np.full(T, 1.0 - 2.0 ** -24))
+    if b == 520 and n == 40000:  # a weight of 2^-22.3 each: together 2^-7
+        check(x, r, p=1.0 - np.arange(1, T + 1) * 2.0 ** -11)

@@ -39,3 +39,11 @@ def test_a_distance_with_a_sign_is_noticed(T):
 def test_far_logits_have_no_weight_at_low_temperatures(T):
     l = np.array([-2e38, -3e38, -1e32], np.float32)
     assert list(sb.bin_of(sb.octaves(l, l.max(), T))) == [sb.BINS - 1, sb.BINS - 1, 0]
+
+
+@pytest.mark.parametrize("b", [520, 800, 1000])
+def test_there_are_logits_whose_part_of_a_bin_depends_on_fusing(b):
+    l, differ = sb.logits_of_a_bin(b, 40000, np.random.default_rng(b))
+    assert len(l) == 40000 and differ > 1000
+    t = sb.octaves(l, 0.0, 1.0)
+    assert (sb.bin_of(t) == b).all() and np.abs(sb.fine_of(t, b) - sb.fine_of(t, b, fused=True)).max() == 1
