@@ -121,8 +121,9 @@ struct Shared {
   float th4[32], tl[32];  // kPow: read at an index of each lane's own
   uint32_t n_own, scan[kWarps];
   float fscan[kWarps], mass;
-  // 1 / (h T) in two parts, and log2(e) / (h T).  h is 1; 1/2 for a temperature so high that differences of
-  // logits that overflow still count; 2^24 for one so low that differences of denormal logits do
+  // 1 / (h T) in two parts, and log2(e) / (h T).  h is 1; 2^-24 for a temperature so high that differences of
+  // logits that overflow still count, and that 1 / T may be denormal; 2^24 for one so low that differences of denormal
+  // logits count
   float ih, il, ch, h, m;
   float ch_off;  // what ch is off by, so that exp2(t) has to be changed by ch_off |t| of itself
   int bin, cut_idx;
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     sh.th4[tid] = kPow[0][tid];
     sh.tl[tid] = kPow[1][tid];
   } else if (tid == 32) {
-    const float h = temp > 0x1p100f ? 0.5f : temp < 0x1p-100f ? 0x1p24f : 1.f;
+    const float h = temp > 0x1p100f ? 0x1p-24f : temp < 0x1p-100f ? 0x1p24f : 1.f;
     const float ht = h * temp, inv = 1.f / ht;  // h T is exact
     sh.h = h;
     sh.ih = inv;

@@ -9,7 +9,7 @@ f32, f64 = np.float32, np.float64
 def scale_of(T):
     """(h, log2(e) / (h T)) of a temperature."""
     T = f32(T)
-    h = f32(0.5) if T > f32(2.0 ** 100) else f32(2.0 ** 24) if T < f32(2.0 ** -100) else f32(1)
+    h = f32(2.0 ** -24) if T > f32(2.0 ** 100) else f32(2.0 ** 24) if T < f32(2.0 ** -100) else f32(1)
     return h, f32(f32(1) / f32(h * T)) * f32(1.4426950408889634)
 
 

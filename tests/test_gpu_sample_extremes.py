@@ -57,3 +57,35 @@ def test_a_full_bin_is_parted_alike_by_every_pass(b, n):
         check(x, r, k=np.full(T, n - 100), p=np.full(T, 1.0 - 2.0 ** -24))
     if b == 520 and n == 40000:  # a weight of 2^-22.3 each: together 2^-7
         check(x, r, p=1.0 - np.arange(1, T + 1) * 2.0 ** -11)
+
+
+HIGH = [1e30, 2.0 ** 101, 1e37, 1.5e38, 1.75e38, 2e38, 3e38, 3.4028235e38]
+
+
+@pytest.mark.parametrize("temperature", HIGH)
+def test_high_temperatures(temperature):
+    """Logits up to the ends of fp32 over temperatures up to there, whose reciprocals would be denormal."""
+    T, V = 24, 1 << 16
+    rng = np.random.default_rng(3)
+    l = (rng.uniform(-1.0, 1.0, (T, V)) * min(3.4e38, 4.0 * temperature)).astype(np.float32)
+    r = rng.random(T, np.float32)
+    for s in (dict(), dict(p=0.7)):
+        check(f32(l), r, temperature=np.full(T, temperature), **{n: np.full(T, v) for n, v in s.items()})
+
+
+@pytest.mark.parametrize("temperature", HIGH)
+def test_min_p_between_neighbours_at_high_temperatures(temperature):
+    """Neighbouring fp32 logits around the one whose weight is min_p: each is on its side of it."""
+    T, V = 20, 4000
+    rng = np.random.default_rng(5)
+    m = rng.uniform(0.45, 0.9, T).astype(np.float32)  # nearer to 1 / e neighbours would be closer than check() decides
+    temperature = np.float32(temperature)
+    top = np.float32(min(3.4e38, float(temperature)))
+    l = np.empty((T, V), np.float32)
+    for t in range(T):
+        at = np.float32(float(top) + float(temperature) * np.log(float(m[t])))
+        key = lambda f: int(f.view(np.int32)) if f >= 0 else -(int(f.view(np.int32)) & 0x7fffffff)  # noqa: E731
+        keys = key(at) + np.arange(V) - V // 2
+        l[t] = np.where(keys >= 0, keys, -keys | -2 ** 31).astype(np.int64).astype(np.int32).view(np.float32)
+        l[t, 0] = top
+    check(f32(l), rng.random(T, np.float32), temperature=np.full(T, temperature), m=m)
