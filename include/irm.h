@@ -439,7 +439,8 @@ irm_status irm_mla_attn_tree8(const void* q_lat, const void* q_rope, int B, int 
  *   temperature, top_p, min_p  device fp32 [n_rows], top_k device int32 [n_rows]; each may be NULL.
  *            temperature NULL: 1; 0, negative or NaN: the first candidate alone.  top_k <= 0, top_p
  *            >= 1 or NaN, min_p <= 0 or NaN: no cut.  The first candidate always stays.
- *   uniforms device fp32 [n_rows] in [0, 1); needed for token
+ *   uniforms device fp32 [n_rows] in [0, 1); needed for token, and not read without it.  One outside is recorded as
+ *            IRM_ERR_DEVICE_BOUNDS, and counts as 0 (negative, NaN) or draws the last entry left
  *   token    device int32 [n_rows] or NULL; -1 for a row without a finite or +infinite logit
  *   probs    device fp32, row t at t * probs_stride, or NULL (one of the two is needed); such a row's
  *            are zeros

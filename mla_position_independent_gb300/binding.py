@@ -206,7 +206,7 @@ def new_workspace(nbytes: int, device="cuda") -> torch.Tensor:
 
 
 def device_status(workspace: torch.Tensor, stream=None):
-    """Raises IrmError if a kernel recorded a timeout or an out-of-range row (and clears it)."""
+    """Raises IrmError if a kernel recorded a timeout or a value out of its range (a row, a page, a uniform), and clears it."""
     _check(lib().irm_device_status(_ptr(workspace), _stream(stream)))
 
 
@@ -697,8 +697,9 @@ def irm_sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p
                stream=None):
     """Sampling from logits [T, vocab] (fp32 or bf16, rows may be strided) with uniforms [T] fp32: temperature, top_p, min_p
     fp32 [T] and top_k int32 [T] on the device, each optional.  probs: an fp32 [T, vocab] tensor that receives
-    the probabilities left (what irm_tree_verify takes).  uniforms None: probabilities alone.  Returns (token [T]
-    int32 or None, probs or None, workspace)."""
+    the probabilities left (what irm_tree_verify takes).  uniforms None: probabilities alone.  A uniform
+    outside [0, 1) is recorded in the workspace (device_status).  Returns (token [T] int32 or None, probs or None,
+    workspace)."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a 2-d torch.float32 or torch.bfloat16 tensor on the GPU")
     dev, (T, V) = logits.device, logits.shape

@@ -82,6 +82,7 @@ struct SampleArgs {
   int32_t* token;
   float* probs;
   int64_t probs_ld;
+  int* status;
   int vec_in, vec_out;  // whole vectors of logits, of probabilities
 };
 
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float temp = a.temperature ? a.temperature[b] : 1.f, top_p = a.top_p ? a.top_p[b] : 1.f;
   const float min_p = a.min_p ? a.min_p[b] : 0.f;
   const int top_k = a.top_k ? a.top_k[b] : 0;
-  const float rf = a.uniforms ? fminf(fmaxf(a.uniforms[b], 0.f), 1.f) : 0.f;
+  const float uniform = a.token ? a.uniforms[b] : 0.f, rf = fminf(fmaxf(uniform, 0.f), 1.f);
+  if (rank == 0 && tid == 0 && !(uniform >= 0.f && uniform < 1.f)) set_status(a.status, kDevErrBounds);
   const bool first_alone = !(temp > 0.f) || top_k == 1 || top_p <= 0.f || min_p > 1.f;
   if (tid < 32) {
     sh.th4[tid] = kPow[0][tid];
@@ -1287,6 +1289,7 @@ extern "C" irm_status irm_sample(const void* logits, int logits_type, int64_t ro
   a.token = token;
   a.probs = probs;
   a.probs_ld = probs_stride;
+  a.status = static_cast<int*>(workspace);
   a.vec_in = row_stride % 4 == 0 && aligned(logits, half ? 8 : 16);
   a.vec_out = probs_stride % 4 == 0 && aligned(probs, 16);
   // in shared memory, where a place in the part has 16 bits
