@@ -366,8 +366,8 @@ irm_status irm_rope_apply(const void* x, int64_t x_token, int64_t x_head, int64_
  *   bytes 512 .. 527  four fp32 scales, one for 128 columns: cKV[j] = code[j] * scale[j / 128]
  *   bytes 528 .. 655  k_r, 64 bf16
  * A scale is the smallest power of two in [2^-126, 2^7] for which the 128 columns fit e4m3 (448 at most;
- * 1 where all are zero), so code * scale is exact in bf16; codes are rounded to the nearest even, and
- * magnitudes beyond 448 * 2^7 become that.  A group with a NaN or an infinity gets a NaN scale and reads as
+ * 1 where all are zero), so code * scale is exact in bf16 in every row that the call writes; codes are rounded to the
+ * nearest even, and magnitudes beyond 448 * 2^7 become that.  A group with a NaN or an infinity gets a NaN scale and reads as
  * NaN.  Rows from elsewhere may bring any codes but 0x7f and 0xff (which read as +-480) and any scales
  * below 2^8: of a scale that is no power of two the upper 16 bits count, and the product is rounded to bf16.
  */
