@@ -49,8 +49,8 @@
  *
  * Errors.  Calls return an irm_status.  No exception crosses the ABI and nothing aborts.
  * Host-side checks happen before any copy or launch.  Device-side problems (a page index
- * outside the paged output, a source row outside the row store, or a pipeline wait that
- * exceeded its 2 s limit) set bits in the status word at the start of the workspace; read
+ * outside the paged output, a source row outside the row store, a uniform number outside
+ * [0, 1) in sampling, or a pipeline wait that exceeded its 2 s limit) set bits in the status word at the start of the workspace; read
  * and clear it with irm_device_status().
  *
  * Workspace.  Each call takes a caller-owned device workspace, 256-byte aligned, of at

@@ -7,7 +7,8 @@
 //   fp32 and rounded to bf16 once.
 //   8-bit rows: for each 128 columns e is the smallest exponent with max |c| <= 448 2^e, in [-126, 7];
 //   code = e4m3(c 2^-e), to the nearest even, at most 448 in magnitude.  A power of two as scale costs
-//   a floating code nothing (its steps are relative), and makes code x scale exact in bf16: what
+//   a floating code nothing (its steps are relative), and makes code x scale exact in bf16 (at the least scales
+//   too: the values are multiples of bf16's least step, 2^-133, and so is what rounding to a code makes of them): what
 //   attention reads is the code's value, rounded nowhere.  The maximum is compared by its
 //   bits, so NaN and infinity count as larger than every number; such a group's scale is NaN.
 //

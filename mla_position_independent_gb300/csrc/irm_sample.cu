@@ -20,7 +20,7 @@
 // Arithmetic.  Which token comes out must not depend on the split or the order of addition, and a flat
 // row of 100k entries has cumulative sums 1e-5 apart, so weights are integers in units of 2^-43 and
 // their sums are exact.  fp32 exponentials (2^-23) would move 100k boundaries by 1e-7 each, so that one
-// draw in a hundred came out wrong; here a weight is good to 2^-37 of the largest: the distance from the
+// draw in a hundred came out wrong; here a weight is good to 2^-37 of the largest and 2^-33 of itself: the distance from the
 // maximum and its product with 1 / T in two fp32 parts, 32 table values and a polynomial of degree 5, some
 // 70 instructions.  fp64 runs at 1 / 64 of the fp32 rate on this GPU.  Thresholds (p of a sum, r of a sum) are
 // exact products of 24 and 64 bits.  Probabilities are fp32 exponentials (2^-21) over the exact
@@ -32,7 +32,7 @@
 // What bounds it.  One row: latency, 14.7 us for 102400 logits with top-k 50 and top-p 0.9, of which the row and its
 // maximum take 2.6, the histogram and its exchange 4, the list and its exchange 4, the ranks 3.  Many rows:
 // instructions and what a CTA does whatever its part's length (scans, exchanges, ranks), which is why few CTAs
-// a row are best: 384 bf16 rows with top-p and probabilities 206 us (35 by their bytes), 111 instructions a warp and
+// a row are best: 384 bf16 rows with top-p and probabilities 209 us (35 by their bytes), 111 instructions a warp and
 // 32 logits at 0.58 a clock and scheduler, two CTAs of 512 threads on an SM.  Steps that were, for these 384 rows: a pass
 // over all elements, and one over those near the cut, for each sum 635; the candidates listed with their weights
 // 475; one element a lane, ranks by four lanes an element 409; fewer neighbours and shorter lists 390; bf16 rows held as
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       if (decltype(sum_others)::value) {
         // What rounding took from 1 / T goes by the octaves.  Else off by at most: an exponential 2^-22 of itself, its
-        // exponent two roundings; ten additions, each 2^-24; an exact weight 2^-34 of itself and half a unit.
+        // exponent two roundings; ten additions, each 2^-24; an exact weight 2^-33 of itself and half a unit.
         const float raw = (rest[0] + rest[1]) + (rest[2] + rest[3]), all = fmaf(slope, sh.ch_off, raw);
         const float off = 1.01f * (raw * (0x1p-22f + 12.f * 0x1p-24f) + slope * (0.6931472f * 2.f * 0x1p-24f));
         others[0] += (uint64_t)(all * (float)kOne);

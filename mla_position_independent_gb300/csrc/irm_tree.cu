@@ -34,7 +34,7 @@
 // 8-bit cache (tree_attn_kernel<true>; rows of 512 e4m3 codes, a scale for 128 columns, and k_r in bf16).  The
 // same kernel, but TMA brings codes (16 KiB a page and CTA, two pages in flight), and four warps turn them into
 // the bf16 tile that the tensor core reads, a thread a row of 128 columns: with a power of two as scale that
-// is exact, so scores, probabilities and O are rounded nowhere else than over a bf16 cache.  The tensor core's
+// is exact (down to bf16's least step, 2^-133), so scores, probabilities and O are rounded nowhere else than over a bf16 cache.  The tensor core's
 // own 8-bit form was not taken: it would need P in 8 bits, whose 2^-9 to 448 lose the many small probabilities
 // next to one large one.  A code takes 4 instructions with its loads, stores and waits; unseen rows are
 // converted with scale 0, which clears them.  Pages wait as codes, so four pages of bf16 do.
@@ -43,9 +43,9 @@
 // gaps); their normalised fp32 partials are merged by a second kernel.
 // Every wait is bounded (2 s) and reports a timeout in the status word.
 //
-// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 940 us under the power cap (1.77 GHz),
-// 1.24 PFLOP/s, 0.65 of the measured bf16 rate; 872 us and 0.70 in a run too short to reach the cap, where a
-// tile takes 0.94 us in the units' own time, ~1800 cycles.  Two limits are near it:
+// What bounds it.  64 requests x 32768 rows, 128 heads, two nodes: 850 to 866 us by replay, 1.36 PFLOP/s, 0.70 of
+// the measured bf16 rate (before the waits in fewer instructions 866 to 872, and 940 once under the power cap at 1.77
+// GHz); a tile takes 0.94 us in the units' own time, ~1800 cycles.  Two limits are near it:
 //   - Issue of MMAs: at N = 64 one takes 44.5 cycles, not 32, so that Q K^T (18) and P V (4 of 128
 //     cycles) keep the tensor core for 1313 cycles a tile.  N = 128 runs at the full rate, but two
 //     pages at once start both sets at once: 1066 us.
@@ -61,8 +61,10 @@
 // Few rows (16 heads, one node, 76 requests) stream 0.88 us a further page, 6.3 TB/s, 0.93 of the
 // measured copy rate.  One short request (512 rows, 16 heads) takes 12.1 us, of which one tile alone
 // (63 rows) is 8.4: it is set-up, the chain of one tile and the way out.
-// The 8-bit cache: 64 x 32768 rows, 128 heads, two nodes 1060 us (1.10 PFLOP/s, 0.57 of the measured rate; a bf16
-// cache of twice the bytes 856 on the same GPU); 8 x 8192, 16 heads, one node 25.8 us.  The conversion is as many
+// The 8-bit cache: 64 x 32768 rows, 128 heads, two nodes 1057 us (1.10 PFLOP/s, 0.57 of the measured rate).  It holds
+// 0.57 of the bytes, but at every shape measured it is slower than a bf16 cache on the same GPU: these 1057 against 850 to 866,
+// 8 x 8192 with 16 heads 26.2 against 23.9, 64 x 8192 130 against 118, 16 x 32768 122 against 117, 152 x 2048 82
+// against 79, one request of 512 rows 12.9 against 12.4.  The conversion is as many
 // instructions again as all other warps execute (ncu: 40.3 to 19.3 million for 38 x 8192 rows of 128 heads), and the
 // tile's chain has four pages to hide in, not five.  What it spent its time on first was fetching instructions: with the conversion
 // unrolled (1880 us) 3.5 warps waited for one at each issue, the SM's instruction cache hit 82% and the next
